@@ -33,6 +33,9 @@ __all__ = [
     "gdn_chunk_prefill_scan",
     "gdn_chunk_prefill_scan_workspace_size", "Problem",
     "GDN_BF16", "GDN_F32",
+    "gdn_short_conv", "gdn_short_conv_step",
+    "gdn_selective_scan", "gdn_selective_scan_step", "gdn_selective_scan_workspace_size",
+    "gdn_norm_gate_residual",
 ]
 
 GDN_BF16 = 0
@@ -146,6 +149,7 @@ def _load(path: str) -> ctypes.CDLL:
     lib.gdn_prefill_fused_mode.argtypes = [ctypes.c_int32]
     lib.gdn_prefill_path.restype = ctypes.c_int32
     lib.gdn_prefill_path.argtypes = [PP, ctypes.c_int32, ctypes.c_int32]
+    block.declare(lib)
     return lib
 
 
@@ -689,3 +693,9 @@ def prefill_launches(Hv: int, d: int, dtype, total_tokens: int = 1) -> int:
     if dtype == torch.bfloat16 and d == 128:
         return 3 if total_tokens > 0 else 2
     return 1
+
+
+from . import block  # noqa: E402  (uses the helpers above)
+from .block import (  # noqa: E402
+    gdn_norm_gate_residual, gdn_selective_scan, gdn_selective_scan_step,
+    gdn_selective_scan_workspace_size, gdn_short_conv, gdn_short_conv_step)

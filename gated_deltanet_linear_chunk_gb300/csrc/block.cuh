@@ -1,0 +1,164 @@
+// block.cuh -- shared pieces of the operators of include/gdn_block.h (not part
+// of the ABI): vector loads, elementary functions, the sequence of a token.
+#pragma once
+
+#include "common.cuh"
+#include "gdn_block.h"
+
+namespace gdn {
+
+constexpr int kGridSms = 152;  // SMs of a GB300: the grids are sized for it
+
+// ------------------------------------------------------- elementary functions
+// ex2.approx and rcp.approx: two ulp and one, flushing denormals.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / (1 + e^-v): e^-v overflows to infinity below -88, where the result is 0.
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + ex2(-kLog2e * v)); }
+__device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
+
+// log(1 + e^v) = max(v, 0) + log1p(e) with e = e^-|v| in (0, 1].  log1p(e) / e
+// is a polynomial of degree 9, fitted to the least largest relative error on
+// [0, 1] (5e-9; 1.2e-7 in fp32 arithmetic): relative accuracy is kept for
+// the small steps of very negative v, where log1p(e) is e.
+__device__ __forceinline__ float softplus(float v) {
+    const float e = ex2(-kLog2e * fabsf(v));
+    float p = -0.0032440233044326305f;
+    p = fmaf(p, e, 0.019851457327604294f);
+    p = fmaf(p, e, -0.05695953220129013f);
+    p = fmaf(p, e, 0.10603655129671097f);
+    p = fmaf(p, e, -0.15305593609809875f);
+    p = fmaf(p, e, 0.1967594027519226f);
+    p = fmaf(p, e, -0.24954134225845337f);
+    p = fmaf(p, e, 0.3332996368408203f);
+    p = fmaf(p, e, -0.4999990165233612f);
+    p = fmaf(p, e, 1.0f);
+    return fmaf(p, e, v > 0.f ? v : 0.f);
+}
+
+// ------------------------------------------------------------- vector access
+// V consecutive elements: one 16-byte word (16 / sizeof(T) elements) or one
+// element (V = 1).
+template <typename T, int V> struct Vec;
+template <typename T> struct Vec<T, 1> {
+    T w;
+    __device__ __forceinline__ static Vec load(const T *p) { return Vec{*p}; }
+    __device__ __forceinline__ void store(T *p) const { *p = w; }
+    __device__ __forceinline__ static Vec zero() { return Vec{from_f32<T>(0.f)}; }
+    __device__ __forceinline__ void to(float *r) const { r[0] = to_f32(w); }
+    __device__ __forceinline__ static Vec from(const float *r) { return Vec{from_f32<T>(r[0])}; }
+};
+template <> struct Vec<float, 4> {
+    float4 w;
+    __device__ __forceinline__ static Vec load(const float *p) {
+        return Vec{*reinterpret_cast<const float4 *>(p)};
+    }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float4 *>(p) = w; }
+    __device__ __forceinline__ static Vec zero() { return Vec{make_float4(0.f, 0.f, 0.f, 0.f)}; }
+    __device__ __forceinline__ void to(float *r) const {
+        r[0] = w.x; r[1] = w.y; r[2] = w.z; r[3] = w.w;
+    }
+    __device__ __forceinline__ static Vec from(const float *r) {
+        return Vec{make_float4(r[0], r[1], r[2], r[3])};
+    }
+};
+template <> struct Vec<__nv_bfloat16, 8> {
+    uint4 w;
+    __device__ __forceinline__ static Vec load(const __nv_bfloat16 *p) {
+        return Vec{*reinterpret_cast<const uint4 *>(p)};
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        *reinterpret_cast<uint4 *>(p) = w;
+    }
+    __device__ __forceinline__ static Vec zero() { return Vec{make_uint4(0, 0, 0, 0)}; }
+    __device__ __forceinline__ void to(float *r) const {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            r[2 * i] = __uint_as_float(u[i] << 16);
+            r[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ static Vec from(const float *r) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(r[2 * i], r[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        return Vec{make_uint4(u[0], u[1], u[2], u[3])};
+    }
+};
+template <typename T> constexpr int kWide = 16 / (int)sizeof(T);
+
+// Whether rows at p, `stride` elements apart, start on 16-byte boundaries.
+template <typename T> inline bool rows_aligned16(const void *p, int64_t stride) {
+    return !p || (aligned16(p) && (stride * (int64_t)sizeof(T)) % 16 == 0);
+}
+
+// ---------------------------------------------------- packed sequences
+// Sequence n holds tokens [start, end).  Values read from cu_seqlens are
+// clamped so that start <= t < end <= T for the token t asked for, whatever
+// the array holds.
+struct Span {
+    int n, start, end;
+};
+
+__device__ __forceinline__ Span span_at(const int32_t *cu, int N, int T, int t, int n) {
+    const int s = cu[n], e = cu[n + 1];
+    return Span{n, min(max(s, 0), t), min(max(e, t + 1), T)};
+}
+
+// The sequence of token t (0 <= t < T): the last n with cu[n] <= t.
+__device__ __forceinline__ Span locate(const int32_t *cu, int N, int T, int t) {
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= t) lo = mid;
+        else hi = mid - 1;
+    }
+    return span_at(cu, N, T, t, lo);
+}
+
+// The sequence of token t = s.end: the next one that is not empty.
+__device__ __forceinline__ Span next_span(const int32_t *cu, int N, int T, const Span &s) {
+    int n = s.n;
+    while (n < N - 1 && cu[n + 1] <= s.end) ++n;
+    Span r = span_at(cu, N, T, s.end, n);
+    r.start = s.end;
+    return r;
+}
+
+// ------------------------------------------------------------------ launchers
+gdn_status launch_short_conv(const gdn_conv_problem &p, const void *x, const float *weight,
+                             const float *bias, const int32_t *cu, const void *init, void *out,
+                             void *fin, cudaStream_t stream);
+gdn_status launch_short_conv_step(const gdn_conv_problem &p, const void *x, const float *weight,
+                                  const float *bias, const void *state, void *out, void *next,
+                                  cudaStream_t stream);
+size_t scan_workspace_size(const gdn_ssm_problem &p);
+gdn_status launch_selective_scan(const gdn_ssm_problem &p, const void *x, const void *dt,
+                                 const float *A, const void *B, const void *C, const float *skip,
+                                 const void *z, const float *bias, const int32_t *cu,
+                                 const float *init, void *out, float *fin, cudaStream_t stream);
+gdn_status launch_selective_scan_step(const gdn_ssm_problem &p, const void *x, const void *dt,
+                                      const float *A, const void *B, const void *C,
+                                      const float *skip, const void *z, const float *bias,
+                                      const float *state, void *out, float *next,
+                                      cudaStream_t stream);
+gdn_status launch_norm_gate_residual(const gdn_norm_problem &p, const void *y,
+                                     const float *weight, const void *gate, const void *residual,
+                                     const float *next_weight, void *out, void *next,
+                                     cudaStream_t stream);
+
+}  // namespace gdn

@@ -1,0 +1,669 @@
+// selective_scan.cu -- selective state space scan over packed sequences, and
+// its single-token step (gdn_selective_scan, gdn_selective_scan_step).
+//
+// Per sequence and channel d, with S states and s_t = softplus(dt_t + bias):
+//
+//   h_t = exp(s_t A) h_{t-1} + s_t x_t B_t,   y_t = C_t . h_t + skip x_t
+//   out_t = y_t silu(z_t)
+//
+// The decay differs per channel and state, so no matrix product carries the
+// recurrence: each (token, channel, state) costs one exponential and four
+// fp32 operations (s A, (s x) B, the update of h, the sum with C), against
+// 8 / S bytes of bf16 x, dt, z and out.  At S = 16 the arithmetic takes
+// longer than the memory traffic.
+//
+// A thread holds CH channels with all their states in registers and walks the
+// tokens in order, so the sums over the states need no exchange between
+// lanes.  States go in pairs through the packed fp32 instructions.  B and C,
+// the same for all channels of a group, are staged in shared memory as fp32;
+// x, dt and z arrive there by 16-byte asynchronous copies one tile ahead.
+//
+// D channels fill few threads, so the packed tokens are cut into W windows of
+// equal length, whatever sequences they hold:
+//   1. every window but the last: the state that its last sequence reaches at
+//      the window's end, if that sequence goes on, starting from zero (or from
+//      the sequence's own initial state if it starts in the window), and the
+//      sum of its steps there;
+//   2. the states entering the windows, in order: c <- exp(A sum s) c + h
+//      (one exponential per state for a whole window, because the decays of
+//      successive tokens multiply);
+//   3. the outputs of every window.
+// Windows of a fixed length balance exactly, and a window whose end falls
+// between two sequences skips step 1.
+#include <atomic>
+
+#include "block.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr int kTile = 16;        // tokens per shared-memory tile
+constexpr int kMaxThreads = 128;
+constexpr int kUnroll = 4;       // tokens in flight per thread
+
+template <typename T> struct ScanArgs {
+    const T *x, *dt, *B, *C, *z;
+    const float *A, *skip, *bias;
+    const int32_t *cu;
+    const float *init;
+    T *out;
+    float *fin;
+    float *carry;   // [W - 1, D, S]: state at each window's end, then entering the next
+    float *steps;   // [W - 1, D]: sum of steps up to the window's end
+    int N, T_, D, S, G;
+    int per_group, tiles;  // channels per group, blocks per group
+    int W, len;            // windows, tokens per window
+    int64_t xs, dts, bs, cs, zs, os;
+    bool softplus, wide, defer;
+};
+
+__device__ __forceinline__ uint64_t pack2f(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2f(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ void copy16_async(void *smem, const void *gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(smem))),
+                 "l"(gmem)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
+
+// Channels per thread: two while their states and decay rates fit half the
+// registers that a thread may have, so that each B and C read from shared
+// memory serves two channels.
+template <int NS> constexpr int kChannels = NS <= 16 ? 2 : 1;
+
+// NS: the states padded to a power of two (A = B = 0 beyond S: those states
+// stay zero).
+template <typename T, int NS> struct ScanThread {
+    static constexpr int CH = kChannels<NS>;
+    static constexpr int NP = NS / 2;
+    uint64_t A[CH][NP], h[CH][NP];
+    float bias[CH], skip[CH], sum[CH];
+    int d;      // first channel
+    int valid;  // channels of this thread that exist
+
+    __device__ __forceinline__ void setup(const ScanArgs<T> &a, int group, int in_group) {
+        d = group * a.per_group + in_group;
+        valid = min(max(a.per_group - in_group, 0), CH);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const bool ok = c < valid;
+            bias[c] = ok && a.bias ? a.bias[d + c] : 0.f;
+            skip[c] = ok && a.skip ? a.skip[d + c] : 0.f;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                float v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    v[i] = ok && 2 * p + i < a.S
+                               ? kLog2e * a.A[(int64_t)(d + c) * a.S + 2 * p + i] : 0.f;
+                A[c][p] = pack2f(v[0], v[1]);
+            }
+        }
+    }
+    // States of this thread's channels at row `row` of a [rows, D, S] array.
+    __device__ __forceinline__ void load(const ScanArgs<T> &a, const float *from, int64_t row) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const float *p0 = from + (row * a.D + d + c) * a.S;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                float v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    v[i] = from && c < valid && 2 * p + i < a.S ? p0[2 * p + i] : 0.f;
+                h[c][p] = pack2f(v[0], v[1]);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(const ScanArgs<T> &a, float *to, int64_t row) const {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            float *p0 = to + (row * a.D + d + c) * a.S;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const float2 v = unpack2f(h[c][p]);
+                if (c < valid && 2 * p < a.S) p0[2 * p] = v.x;
+                if (c < valid && 2 * p + 1 < a.S) p0[2 * p + 1] = v.y;
+            }
+        }
+    }
+    // One token: xv, dv of each channel, B and C of the group; y = C . h.
+    template <bool OUT>
+    __device__ __forceinline__ void token(bool softplus_on, const float *xv, const float *dv,
+                                          const float *sB, const float *sC, float *y) {
+        uint64_t s2[CH], u2[CH], y2[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            float s = dv[c] + bias[c];
+            if (softplus_on) s = softplus(s);
+            if (!OUT) sum[c] += s;
+            s2[c] = pack2f(s, s);
+            u2[c] = pack2f(s * xv[c], s * xv[c]);
+            y2[c] = 0;
+        }
+#pragma unroll
+        for (int q = 0; q < NP / 2; ++q) {
+            const ulonglong2 b4 = reinterpret_cast<const ulonglong2 *>(sB)[q];
+            ulonglong2 c4 = {0, 0};
+            if (OUT) c4 = reinterpret_cast<const ulonglong2 *>(sC)[q];
+            const uint64_t b[2] = {b4.x, b4.y}, cc[2] = {c4.x, c4.y};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const int p = 2 * q + i;
+                    const float2 e = unpack2f(fmul2(s2[c], A[c][p]));
+                    h[c][p] = ffma2(pack2f(ex2(e.x), ex2(e.y)), h[c][p], fmul2(u2[c], b[i]));
+                    if (OUT) y2[c] = ffma2(cc[i], h[c][p], y2[c]);
+                }
+        }
+        if (OUT)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const float2 v = unpack2f(y2[c]);
+                y[c] = v.x + v.y;
+            }
+    }
+};
+
+// Shared memory of a block: two tiles of x, dt (and z), and of B (and C).
+template <typename T, int NS, bool OUT> struct ScanTiles {
+    static constexpr int CH = kChannels<NS>;
+    T *in[2];      // [tensor][token][channel]
+    float *bc[2];  // [B, C][token][state]
+    int width;     // channels per block
+    __device__ ScanTiles(char *smem, int threads) : width(threads * CH) {
+        bc[0] = reinterpret_cast<float *>(smem);
+        bc[1] = bc[0] + (OUT ? 2 : 1) * kTile * NS;
+        in[0] = reinterpret_cast<T *>(bc[1] + (OUT ? 2 : 1) * kTile * NS);
+        in[1] = in[0] + (OUT ? 3 : 2) * kTile * width;
+    }
+    static size_t bytes(int threads) {
+        return 2 * ((OUT ? 2 : 1) * kTile * NS * sizeof(float) +
+                    (OUT ? 3 : 2) * kTile * threads * CH * sizeof(T));
+    }
+    // The inputs of tokens [t, te) for this block's channels, d0 the first.
+    __device__ __forceinline__ void inputs(const ScanArgs<T> &a, int buf, int t, int te, int d0,
+                                           int in_group0) const {
+        constexpr int V = kWide<T>;
+        const int cols = min(width, a.per_group - in_group0);
+        const T *src[3] = {a.x, a.dt, a.z};
+        const int64_t stride[3] = {a.xs, a.dts, a.zs};
+        if (a.wide) {
+            const int words = cols / V;
+            for (int i = threadIdx.x; i < kTile * words; i += blockDim.x) {
+                const int r = i / words, c = (i % words) * V;
+                if (t + r >= te) break;
+#pragma unroll
+                for (int k = 0; k < (OUT ? 3 : 2); ++k)
+                    if (k < 2 || a.z)
+                        copy16_async(in[buf] + (k * kTile + r) * width + c,
+                                     src[k] + (t + r) * stride[k] + d0 + c);
+            }
+        } else {
+            for (int i = threadIdx.x; i < kTile * cols; i += blockDim.x) {
+                const int r = i / cols, c = i % cols;
+                if (t + r >= te) break;
+#pragma unroll
+                for (int k = 0; k < (OUT ? 3 : 2); ++k)
+                    if (k < 2 || a.z)
+                        in[buf][(k * kTile + r) * width + c] =
+                            src[k][(t + r) * stride[k] + d0 + c];
+            }
+        }
+    }
+    // B and C of the same tokens as fp32, zero past the last state.
+    __device__ __forceinline__ void states(const ScanArgs<T> &a, int buf, int t, int te,
+                                           int group) const {
+        for (int i = threadIdx.x; i < kTile * NS; i += blockDim.x) {
+            const int r = i / NS, n = i % NS;
+            const bool ok = t + r < te && n < a.S;
+            bc[buf][i] = ok ? to_f32(a.B[(t + r) * a.bs + group * a.S + n]) : 0.f;
+            if (OUT) bc[buf][kTile * NS + i] = ok ? to_f32(a.C[(t + r) * a.cs + group * a.S + n]) : 0.f;
+        }
+    }
+};
+
+// Tokens [t, e) of tile `buf`, whose first token is t0.
+template <typename T, int NS, bool OUT, int U>
+__device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS> &th,
+                                         const ScanTiles<T, NS, OUT> &tl, int buf, int t0, int t) {
+    constexpr int CH = kChannels<NS>;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int r = t - t0 + u;
+        const T *in = tl.in[buf] + r * tl.width + threadIdx.x * CH;
+        float xv[CH], dv[CH], y[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            xv[c] = to_f32(in[c]);
+            dv[c] = to_f32(in[kTile * tl.width + c]);
+        }
+        th.template token<OUT>(a.softplus, xv, dv, tl.bc[buf] + r * NS,
+                               tl.bc[buf] + (kTile + r) * NS, y);
+        if (OUT) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                y[c] = fmaf(th.skip[c], xv[c], y[c]);
+                if (a.z) y[c] *= silu(to_f32(in[2 * kTile * tl.width + c]));
+            }
+            T *o = a.out + (t + u) * a.os + th.d;
+            if (CH == 2 && a.wide) {
+                if (th.valid) {
+                    if constexpr (sizeof(T) == 2) {
+                        *reinterpret_cast<__nv_bfloat162 *>(o) = __floats2bfloat162_rn(y[0], y[CH - 1]);
+                    } else {
+                        *reinterpret_cast<float2 *>(o) = make_float2(y[0], y[CH - 1]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+                    if (c < th.valid) o[c] = from_f32<T>(y[c]);
+            }
+        }
+    }
+}
+
+// Final states of empty sequences are their initial ones: one row of blocks
+// copies them.
+template <typename T>
+__device__ void copy_empty(const ScanArgs<T> &a, int d0, int cols) {
+    for (int n = 0; n < a.N; ++n) {
+        if (a.cu[n + 1] > a.cu[n]) continue;
+        const int64_t at = ((int64_t)n * a.D + d0) * a.S;
+        for (int i = threadIdx.x; i < cols * a.S; i += blockDim.x)
+            a.fin[at + i] = a.init ? a.init[at + i] : 0.f;
+    }
+}
+
+template <typename T, int NS, bool OUT>
+__global__ void __launch_bounds__(kMaxThreads, NS <= 16 ? 4 : 2) gdn_scan_kernel(const ScanArgs<T> a) {
+    extern __shared__ __align__(16) char smem[];
+    const ScanTiles<T, NS, OUT> tl(smem, blockDim.x);
+    const int group = blockIdx.x / a.tiles, in_group0 = (blockIdx.x % a.tiles) * tl.width;
+    const int w = blockIdx.y, d0 = group * a.per_group + in_group0;
+    if (OUT && w == a.W) {
+        copy_empty(a, d0, min(tl.width, a.per_group - in_group0));
+        return;
+    }
+    int t0 = w * a.len;
+    const int t1 = min(t0 + a.len, a.T_);
+    Span s;
+    ScanThread<T, NS> th;
+    bool from_carry = false;
+    if (OUT) {
+        s = locate(a.cu, a.N, a.T_, t0);
+        from_carry = s.start < t0;
+    } else {
+        // The sequence that goes on past this window's end.
+        s = locate(a.cu, a.N, a.T_, t1 - 1);
+        if (s.end <= t1) return;
+        from_carry = s.start < t0;
+        t0 = max(t0, s.start);
+    }
+    th.setup(a, group, in_group0 + threadIdx.x * th.CH);
+    if (from_carry) th.load(a, OUT ? a.carry : nullptr, w - 1);
+    else th.load(a, a.init, s.n);
+#pragma unroll
+    for (int c = 0; c < th.CH; ++c) th.sum[c] = 0.f;
+
+    tl.inputs(a, 0, t0, t1, d0, in_group0);
+    tl.states(a, 0, t0, t1, group);
+    int buf = 0;
+    for (int tt = t0; tt < t1; tt += kTile, buf ^= 1) {
+        const int te = min(tt + kTile, t1);
+        copies_wait();
+        __syncthreads();
+        if (te < t1) {
+            tl.inputs(a, buf ^ 1, te, t1, d0, in_group0);
+            tl.states(a, buf ^ 1, te, t1, group);
+        }
+        int t = tt;
+        while (t < te) {
+            const int e = min(te, s.end);
+            for (; t + kUnroll <= e; t += kUnroll)
+                scan_run<T, NS, OUT, kUnroll>(a, th, tl, buf, tt, t);
+            for (; t < e; ++t) scan_run<T, NS, OUT, 1>(a, th, tl, buf, tt, t);
+            if (OUT && t == s.end) {
+                // A final state written over the initial one must wait for
+                // the windows that read it: it takes the place of the state
+                // that entered this window, copied by a last launch.
+                if (a.fin && from_carry && a.defer) th.store(a, a.carry, w - 1);
+                else if (a.fin) th.store(a, a.fin, s.n);
+                if (t < t1) {
+                    s = next_span(a.cu, a.N, a.T_, s);
+                    th.load(a, a.init, s.n);
+                    from_carry = false;
+                }
+            }
+        }
+    }
+    if (!OUT) {
+        th.store(a, a.carry, w);
+#pragma unroll
+        for (int c = 0; c < th.CH; ++c)
+            if (c < th.valid) a.steps[(int64_t)w * a.D + th.d + c] = th.sum[c];
+    }
+}
+
+constexpr int kCombineThreads = 256;
+
+// States entering the windows: in window order, c <- exp(A sum s) c + h, from
+// the window's own state alone where its last sequence starts inside it.
+template <typename T>
+__global__ void __launch_bounds__(kCombineThreads) gdn_scan_combine_kernel(const ScanArgs<T> a) {
+    extern __shared__ char inside[];  // [W - 1]
+    for (int w = threadIdx.x; w < a.W - 1; w += blockDim.x)
+        inside[w] = locate(a.cu, a.N, a.T_, (w + 1) * a.len - 1).start >= w * a.len;
+    __syncthreads();
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, ds = (int64_t)a.D * a.S;
+    if (i >= ds) return;
+    const float rate = kLog2e * a.A[i];
+    const int d = (int)(i / a.S);
+    float c = 0.f;
+#pragma unroll 4
+    for (int w = 0; w < a.W - 1; ++w) {
+        const float h = a.carry[w * ds + i];
+        const float kept = ex2(rate * a.steps[(int64_t)w * a.D + d]) * c;
+        c = inside[w] ? h : h + kept;
+        a.carry[w * ds + i] = c;
+    }
+}
+
+// In place: the final states that gdn_scan_kernel left in the carries.
+template <typename T>
+__global__ void __launch_bounds__(kCombineThreads) gdn_scan_deferred_kernel(const ScanArgs<T> a) {
+    const int w = blockIdx.y + 1, t0 = w * a.len;
+    const Span s = locate(a.cu, a.N, a.T_, t0);
+    if (s.start >= t0 || s.end > min(t0 + a.len, a.T_)) return;
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, ds = (int64_t)a.D * a.S;
+    if (i < ds) a.fin[s.n * ds + i] = a.carry[(w - 1) * ds + i];
+}
+
+// ------------------------------------------------------------ single tokens
+constexpr int kStepThreads = 128;
+
+template <typename T> struct ScanStepArgs {
+    const T *x, *dt, *B, *C, *z;
+    const float *A, *skip, *bias, *state;
+    T *out;
+    float *next;
+    int N, D, S, per_group;
+    int64_t xs, dts, bs, cs, zs, os;
+    bool softplus;
+};
+
+// L lanes per channel, V consecutive states per lane at a time.
+template <typename T, int V, int L>
+__global__ void __launch_bounds__(kStepThreads) gdn_scan_step_kernel(const ScanStepArgs<T> a) {
+    const int lane = threadIdx.x % L;
+    const int d = blockIdx.x * (kStepThreads / L) + threadIdx.x / L;
+    const bool ok = d < a.D;
+    const int dd = ok ? d : a.D - 1, g = dd / a.per_group;
+    for (int64_t n = blockIdx.y; n < a.N; n += gridDim.y) {
+        float s = to_f32(a.dt[n * a.dts + dd]) + (a.bias ? a.bias[dd] : 0.f);
+        if (a.softplus) s = softplus(s);
+        const float xv = to_f32(a.x[n * a.xs + dd]);
+        const float u = s * xv;
+        float y = 0.f;
+        const int64_t row = (n * a.D + dd) * a.S;
+        for (int j0 = lane * V; ok && j0 < a.S; j0 += L * V) {
+            float h[V], A[V];
+            Vec<float, V>::load(a.state + row + j0).to(h);
+            Vec<float, V>::load(a.A + (int64_t)dd * a.S + j0).to(A);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float b = to_f32(a.B[n * a.bs + g * a.S + j0 + i]);
+                const float c = to_f32(a.C[n * a.cs + g * a.S + j0 + i]);
+                h[i] = fmaf(ex2(s * (kLog2e * A[i])), h[i], u * b);
+                y = fmaf(c, h[i], y);
+            }
+            Vec<float, V>::from(h).store(a.next + row + j0);
+        }
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        if (ok && lane == 0) {
+            if (a.skip) y = fmaf(a.skip[dd], xv, y);
+            if (a.z) y *= silu(to_f32(a.z[n * a.zs + dd]));
+            a.out[n * a.os + dd] = from_f32<T>(y);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ sizes
+// How a problem is cut: the states' padded count, threads per block, blocks
+// per group, windows and their length.
+struct ScanPlan {
+    int ns, threads, tiles, W, len;
+};
+
+// The shortest window: below it the carries' launches cost more than the
+// windows' parallel run saves.
+constexpr int kMinWindow = 64;
+
+ScanPlan scan_plan(const gdn_ssm_problem &p) {
+    ScanPlan s;
+    s.ns = 4;
+    while (s.ns < p.state_dim) s.ns *= 2;
+    const int ch = s.ns <= 16 ? 2 : 1;
+    const int per_group = p.channels / p.num_groups;
+    const int warps = (per_group + 32 * ch - 1) / (32 * ch);
+    s.threads = 32 * (warps < kMaxThreads / 32 ? warps : kMaxThreads / 32);
+    s.tiles = (per_group + s.threads * ch - 1) / (s.threads * ch);
+    const int64_t blocks = (int64_t)p.num_groups * s.tiles;
+    // Four blocks of 128 threads per SM.
+    const int64_t room = (int64_t)4 * kGridSms * (kMaxThreads / s.threads);
+    int64_t W = room / (blocks > 0 ? blocks : 1);
+    const int64_t most = p.total_tokens / kMinWindow;
+    W = W < most ? W : most;
+    W = W < 1 ? 1 : W;
+    const int64_t len = (p.total_tokens + W - 1) / W;
+    s.len = (int)(len > 0 ? len : 1);
+    s.W = (int)((p.total_tokens + s.len - 1) / s.len);
+    return s;
+}
+
+template <typename T> ScanArgs<T> scan_args(const gdn_ssm_problem &p, const ScanPlan &pl) {
+    ScanArgs<T> a{};
+    a.N = p.num_seqs;
+    a.T_ = (int)p.total_tokens;
+    a.D = p.channels;
+    a.S = p.state_dim;
+    a.G = p.num_groups;
+    a.per_group = p.channels / p.num_groups;
+    a.tiles = pl.tiles;
+    a.W = pl.W;
+    a.len = pl.len;
+    a.xs = p.x_stride;
+    a.dts = p.dt_stride;
+    a.bs = p.b_stride;
+    a.cs = p.c_stride;
+    a.zs = p.z_stride;
+    a.os = p.out_stride;
+    a.softplus = p.dt_softplus != 0;
+    a.carry = static_cast<float *>(p.workspace);
+    a.steps = a.carry + (int64_t)(pl.W > 1 ? pl.W - 1 : 0) * a.D * a.S;
+    return a;
+}
+
+// Blocks of full size need more shared memory than a kernel has by default;
+// the limit is raised once per device and variant.
+template <typename T, int NS> bool scan_shared_memory() {
+    static std::atomic<bool> done[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    if (done[dev].load(std::memory_order_acquire)) return true;
+    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if (cudaFuncSetAttribute(gdn_scan_kernel<T, NS, true>, attr,
+                             (int)ScanTiles<T, NS, true>::bytes(kMaxThreads)) != cudaSuccess ||
+        cudaFuncSetAttribute(gdn_scan_kernel<T, NS, false>, attr,
+                             (int)ScanTiles<T, NS, false>::bytes(kMaxThreads)) != cudaSuccess)
+        return false;
+    done[dev].store(true, std::memory_order_release);
+    return true;
+}
+
+template <typename T, int NS>
+gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cudaStream_t stream) {
+    const unsigned blocks = (unsigned)(a.G * pl.tiles);
+    const int64_t ds = (int64_t)a.D * a.S;
+    const unsigned each = (unsigned)((ds + kCombineThreads - 1) / kCombineThreads);
+    const size_t in_bytes = ScanTiles<T, NS, false>::bytes(pl.threads);
+    const size_t out_bytes = ScanTiles<T, NS, true>::bytes(pl.threads);
+    if (!scan_shared_memory<T, NS>()) return GDN_ERR_CUDA;
+    if (pl.W > 1) {
+        gdn_scan_kernel<T, NS, false>
+            <<<dim3(blocks, pl.W - 1), pl.threads, in_bytes, stream>>>(a);
+        gdn_scan_combine_kernel<T><<<each, kCombineThreads, pl.W - 1, stream>>>(a);
+    }
+    const unsigned rows = (unsigned)(pl.W + (empties ? 1 : 0));
+    if (rows > 0)
+        gdn_scan_kernel<T, NS, true><<<dim3(blocks, rows), pl.threads, out_bytes, stream>>>(a);
+    if (a.defer && pl.W > 1)
+        gdn_scan_deferred_kernel<T><<<dim3(each, pl.W - 1), kCombineThreads, 0, stream>>>(a);
+    return launch_status();
+}
+
+template <typename T>
+gdn_status scan_typed(const gdn_ssm_problem &p, const void *x, const void *dt, const float *A,
+                      const void *B, const void *C, const float *skip, const void *z,
+                      const float *bias, const int32_t *cu, const float *init, void *out,
+                      float *fin, cudaStream_t stream) {
+    const ScanPlan pl = scan_plan(p);
+    ScanArgs<T> a = scan_args<T>(p, pl);
+    if ((int64_t)a.G * pl.tiles > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    a.x = static_cast<const T *>(x);
+    a.dt = static_cast<const T *>(dt);
+    a.B = static_cast<const T *>(B);
+    a.C = static_cast<const T *>(C);
+    a.z = static_cast<const T *>(z);
+    a.A = A;
+    a.skip = skip;
+    a.bias = bias;
+    a.cu = cu;
+    a.init = init;
+    a.out = static_cast<T *>(out);
+    a.fin = fin;
+    a.defer = fin && fin == init;
+    a.wide = a.per_group % kWide<T> == 0 && rows_aligned16<T>(x, p.x_stride) &&
+             rows_aligned16<T>(dt, p.dt_stride) && rows_aligned16<T>(z, p.z_stride) &&
+             rows_aligned16<T>(out, p.out_stride);
+    // Only a batch of several sequences (or of no tokens) has empty ones.
+    const bool empties = fin && fin != init && (p.num_seqs > 1 || p.total_tokens == 0);
+    switch (pl.ns) {
+        case 4: return run_scan<T, 4>(pl, a, empties, stream);
+        case 8: return run_scan<T, 8>(pl, a, empties, stream);
+        case 16: return run_scan<T, 16>(pl, a, empties, stream);
+        case 32: return run_scan<T, 32>(pl, a, empties, stream);
+        case 64: return run_scan<T, 64>(pl, a, empties, stream);
+    }
+    return GDN_ERR_UNSUPPORTED;
+}
+
+template <typename T, int V, int L>
+void run_scan_step(const ScanStepArgs<T> &a, cudaStream_t stream) {
+    const int per_block = kStepThreads / L;
+    const unsigned gx = (unsigned)((a.D + per_block - 1) / per_block);
+    const unsigned gy = (unsigned)(a.N < 65535 ? a.N : 65535);
+    gdn_scan_step_kernel<T, V, L><<<dim3(gx, gy), kStepThreads, 0, stream>>>(a);
+}
+
+template <typename T>
+gdn_status scan_step_typed(const gdn_ssm_problem &p, const void *x, const void *dt,
+                           const float *A, const void *B, const void *C, const float *skip,
+                           const void *z, const float *bias, const float *state, void *out,
+                           float *next, cudaStream_t stream) {
+    ScanStepArgs<T> a;
+    a.x = static_cast<const T *>(x);
+    a.dt = static_cast<const T *>(dt);
+    a.B = static_cast<const T *>(B);
+    a.C = static_cast<const T *>(C);
+    a.z = static_cast<const T *>(z);
+    a.A = A;
+    a.skip = skip;
+    a.bias = bias;
+    a.state = state;
+    a.out = static_cast<T *>(out);
+    a.next = next;
+    a.N = p.num_seqs;
+    a.D = p.channels;
+    a.S = p.state_dim;
+    a.per_group = p.channels / p.num_groups;
+    a.xs = p.x_stride;
+    a.dts = p.dt_stride;
+    a.bs = p.b_stride;
+    a.cs = p.c_stride;
+    a.zs = p.z_stride;
+    a.os = p.out_stride;
+    a.softplus = p.dt_softplus != 0;
+    const bool wide = p.state_dim % 4 == 0 && aligned16(state) && aligned16(next) && aligned16(A);
+    const int lanes = wide ? p.state_dim / 4 : p.state_dim;
+    if (wide) {
+        if (lanes <= 1) run_scan_step<T, 4, 1>(a, stream);
+        else if (lanes <= 2) run_scan_step<T, 4, 2>(a, stream);
+        else if (lanes <= 4) run_scan_step<T, 4, 4>(a, stream);
+        else if (lanes <= 8) run_scan_step<T, 4, 8>(a, stream);
+        else run_scan_step<T, 4, 16>(a, stream);
+    } else {
+        if (lanes <= 1) run_scan_step<T, 1, 1>(a, stream);
+        else if (lanes <= 8) run_scan_step<T, 1, 8>(a, stream);
+        else run_scan_step<T, 1, 16>(a, stream);
+    }
+    return launch_status();
+}
+
+}  // namespace
+
+size_t scan_workspace_size(const gdn_ssm_problem &p) {
+    const ScanPlan pl = scan_plan(p);
+    if (pl.W <= 1) return 0;
+    return (size_t)(pl.W - 1) * p.channels * (p.state_dim + 1) * sizeof(float);
+}
+
+gdn_status launch_selective_scan(const gdn_ssm_problem &p, const void *x, const void *dt,
+                                 const float *A, const void *B, const void *C, const float *skip,
+                                 const void *z, const float *bias, const int32_t *cu,
+                                 const float *init, void *out, float *fin, cudaStream_t stream) {
+    return p.dtype == GDN_BF16
+               ? scan_typed<__nv_bfloat16>(p, x, dt, A, B, C, skip, z, bias, cu, init, out, fin,
+                                           stream)
+               : scan_typed<float>(p, x, dt, A, B, C, skip, z, bias, cu, init, out, fin, stream);
+}
+
+gdn_status launch_selective_scan_step(const gdn_ssm_problem &p, const void *x, const void *dt,
+                                      const float *A, const void *B, const void *C,
+                                      const float *skip, const void *z, const float *bias,
+                                      const float *state, void *out, float *next,
+                                      cudaStream_t stream) {
+    return p.dtype == GDN_BF16
+               ? scan_step_typed<__nv_bfloat16>(p, x, dt, A, B, C, skip, z, bias, state, out,
+                                                next, stream)
+               : scan_step_typed<float>(p, x, dt, A, B, C, skip, z, bias, state, out, next,
+                                        stream);
+}
+
+}  // namespace gdn

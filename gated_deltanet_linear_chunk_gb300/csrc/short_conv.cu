@@ -1,0 +1,349 @@
+// short_conv.cu -- short causal depthwise convolution over packed sequences,
+// and its single-token step (gdn_short_conv, gdn_short_conv_step).
+//
+//   out[t, c] = act(bias[c] + sum_{j < K} w[c, j] x[t - K + 1 + j, c])
+//
+// with the K - 1 inputs before a sequence's first taken from its state.  Each
+// input is read once and each output written once: 2 e bytes (e bytes per
+// element) against 2 K flops, so both kernels are bound by HBM bandwidth and,
+// for few tokens, by the latency of one load and one store.
+//
+// A thread takes one 16-byte word of channels (one element where the rows are
+// not 16-byte aligned) through a run of consecutive tokens.  The last K - 1
+// inputs stay in registers, so only a run's start reads rows again (K - 1
+// rows per run, from L2).  Sequences that end inside a block of tokens take
+// the general path, which gathers every tap from the tokens or the state.
+#include "block.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kStep = 4;  // tokens loaded at once
+
+template <typename T> struct ConvArgs {
+    const T *x;
+    const float *weight, *bias;
+    const int32_t *cu;
+    const T *init;
+    T *out, *fin;
+    int N, T_, C;
+    int64_t xs, os;
+    int tx;          // threads along the channels (a power of two)
+    int n_chan;      // blocks along the channels
+    int run;         // tokens per thread
+    int n_main;      // blocks of the convolution; the rest write states
+    int first;       // number of this launch's first block
+    bool act;
+};
+
+// The weights of this block's channels as [K][channels] in shared memory:
+// read from [C, K] in order, so that the threads' own columns are not a
+// strided walk over global memory.
+template <int K>
+__device__ __forceinline__ void stage_weights(float *sw, const float *w, int c0, int C, int width) {
+    const int cols = min(width, C - c0);
+    for (int i = threadIdx.x; i < cols * K; i += kThreads)
+        sw[(i % K) * width + i / K] = w[(int64_t)c0 * K + i];
+    __syncthreads();
+}
+
+// Input `pos` of the sequence that starts at token `start`: from the tokens,
+// or from its state (positions start - K + 1 .. start - 1).
+template <typename T, int V, int K>
+__device__ __forceinline__ Vec<T, V> tap(const ConvArgs<T> &a, int n, int start, int pos, int c) {
+    if (pos >= start) return Vec<T, V>::load(a.x + pos * a.xs + c);
+    const int r = K - 1 + pos - start;
+    if (!a.init || r < 0) return Vec<T, V>::zero();
+    return Vec<T, V>::load(a.init + ((int64_t)n * (K - 1) + r) * a.C + c);
+}
+
+// The states after the sequences' last tokens.  One thread per sequence and
+// word of channels reads all K - 1 rows before it writes the first, so that
+// the new state may replace the old one.
+template <typename T, int V, int K>
+__device__ __forceinline__ void write_state(const ConvArgs<T> &a, int64_t i) {
+    const int nv = a.C / V;
+    if (i >= (int64_t)a.N * nv) return;
+    const int n = (int)(i / nv), c = (int)(i % nv) * V;
+    const int start = min(max(a.cu[n], 0), a.T_), end = min(max(a.cu[n + 1], start), a.T_);
+    Vec<T, V> rows[K - 1];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+        rows[j] = tap<T, V, K>(a, n, start, end - (K - 1) + j, c);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) rows[j].store(a.fin + ((int64_t)n * (K - 1) + j) * a.C + c);
+}
+
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(kThreads) gdn_short_conv_kernel(const ConvArgs<T> a) {
+    extern __shared__ float sw[];
+    const int blk = blockIdx.x + a.first;
+    if (blk >= a.n_main) {
+        write_state<T, V, K>(a, (int64_t)(blk - a.n_main) * kThreads + threadIdx.x);
+        return;
+    }
+    const int tx = threadIdx.x & (a.tx - 1), ty = threadIdx.x / a.tx;
+    const int c0 = (blk % a.n_chan) * a.tx * V, c = c0 + tx * V;
+    stage_weights<K>(sw, a.weight, c0, a.C, a.tx * V);
+    const int64_t first = ((int64_t)(blk / a.n_chan) * (kThreads / a.tx) + ty) * a.run;
+    if (c >= a.C || first >= a.T_) return;
+    const int t1 = (int)min(first + a.run, (int64_t)a.T_);
+
+    float w[K][V], b[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) w[j][v] = sw[j * a.tx * V + tx * V + v];
+        b[v] = a.bias ? a.bias[c + v] : 0.f;
+    }
+    Span s = locate(a.cu, a.N, a.T_, (int)first);
+    float in[K - 1 + kStep][V];  // the K - 1 inputs before a block, and the block's
+    bool have = false;
+    for (int t = (int)first; t < t1; t += kStep) {
+        if (t >= s.end) {
+            s = next_span(a.cu, a.N, a.T_, s);
+            have = false;
+        }
+        if (t + kStep <= min(s.end, t1)) {
+            Vec<T, V> word[kStep];
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) word[u] = Vec<T, V>::load(a.x + (t + u) * a.xs + c);
+            if (!have) {
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j)
+                    tap<T, V, K>(a, s.n, s.start, t - (K - 1) + j, c).to(in[j]);
+                have = true;
+            }
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) word[u].to(in[K - 1 + u]);
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) {
+                float y[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    y[v] = b[v];
+#pragma unroll
+                    for (int j = 0; j < K; ++j) y[v] = fmaf(w[j][v], in[u + j][v], y[v]);
+                    if (a.act) y[v] = silu(y[v]);
+                }
+                Vec<T, V>::from(y).store(a.out + (t + u) * a.os + c);
+            }
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+                for (int v = 0; v < V; ++v) in[j][v] = in[kStep + j][v];
+        } else {
+            const int te = min(t + kStep, t1);
+#pragma unroll 1
+            for (int tok = t; tok < te; ++tok) {
+                if (tok >= s.end) s = next_span(a.cu, a.N, a.T_, s);
+                float y[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) y[v] = b[v];
+#pragma unroll
+                for (int j = 0; j < K; ++j) {
+                    float r[V];
+                    tap<T, V, K>(a, s.n, s.start, tok - (K - 1) + j, c).to(r);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) y[v] = fmaf(w[j][v], r[v], y[v]);
+                }
+                if (a.act)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) y[v] = silu(y[v]);
+                Vec<T, V>::from(y).store(a.out + tok * a.os + c);
+            }
+            have = false;
+        }
+    }
+}
+
+template <typename T> struct StepArgs {
+    const T *x;
+    const float *weight, *bias;
+    const T *state;
+    T *out, *next;
+    int N, C;
+    int64_t xs, os;
+    int tx, n_chan, run;
+    bool act;
+};
+
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(kThreads) gdn_short_conv_step_kernel(const StepArgs<T> a) {
+    extern __shared__ float sw[];
+    const int tx = threadIdx.x & (a.tx - 1), ty = threadIdx.x / a.tx;
+    const int c0 = (blockIdx.x % a.n_chan) * a.tx * V, c = c0 + tx * V;
+    const int64_t first = ((int64_t)(blockIdx.x / a.n_chan) * (kThreads / a.tx) + ty) * a.run;
+    stage_weights<K>(sw, a.weight, c0, a.C, a.tx * V);
+    if (c >= a.C) return;
+    const int last = (int)min(first + a.run, (int64_t)a.N);
+    for (int n = (int)first; n < last; ++n) {
+        Vec<T, V> rows[K];
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j)
+            rows[j] = Vec<T, V>::load(a.state + ((int64_t)n * (K - 1) + j) * a.C + c);
+        rows[K - 1] = Vec<T, V>::load(a.x + n * a.xs + c);
+        float y[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) y[v] = a.bias ? a.bias[c + v] : 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            float r[V];
+            rows[j].to(r);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                y[v] = fmaf(sw[j * a.tx * V + tx * V + v], r[v], y[v]);
+        }
+        if (a.act)
+#pragma unroll
+            for (int v = 0; v < V; ++v) y[v] = silu(y[v]);
+        Vec<T, V>::from(y).store(a.out + n * a.os + c);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j)
+            rows[j + 1].store(a.next + ((int64_t)n * (K - 1) + j) * a.C + c);
+    }
+}
+
+// Threads along the channels: the words of a row, up to the block.
+int threads_along(int words) {
+    int tx = 1;
+    while (tx < words && tx < kThreads) tx *= 2;
+    return tx;
+}
+
+template <typename T, int V, int K>
+gdn_status run_conv(const gdn_conv_problem &p, const void *x, const float *weight,
+                    const float *bias, const int32_t *cu, const void *init, void *out, void *fin,
+                    cudaStream_t stream) {
+    ConvArgs<T> a;
+    a.x = static_cast<const T *>(x);
+    a.weight = weight;
+    a.bias = bias;
+    a.cu = cu;
+    a.init = static_cast<const T *>(init);
+    a.out = static_cast<T *>(out);
+    a.fin = static_cast<T *>(fin);
+    a.N = p.num_seqs;
+    a.T_ = (int)p.total_tokens;
+    a.C = p.channels;
+    a.xs = p.x_stride;
+    a.os = p.out_stride;
+    a.act = p.activation == GDN_ACT_SILU;
+    const int words = p.channels / V;
+    a.tx = threads_along(words);
+    a.n_chan = (words + a.tx - 1) / a.tx;
+    const int ty = kThreads / a.tx;
+    // Tokens per thread: long runs read fewer rows twice (K - 1 of each
+    // run), short ones make enough blocks for the GPU.
+    auto blocks = [&](int run) {
+        return (int64_t)a.n_chan * ((p.total_tokens + (int64_t)run * ty - 1) / ((int64_t)run * ty));
+    };
+    a.run = 32;
+    while (a.run > kStep && blocks(a.run) < 8 * kGridSms) a.run /= 2;
+    const int64_t n_main = blocks(a.run);
+    const int64_t n_state =
+        fin ? ((int64_t)p.num_seqs * words + kThreads - 1) / kThreads : 0;
+    if (n_main + n_state > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    a.n_main = (int)n_main;
+    const size_t smem = (size_t)a.tx * V * K * sizeof(float);
+    // A state written in place must not replace what another block still
+    // reads: its blocks then run as a launch of their own.
+    const bool apart = fin && fin == init;
+    a.first = 0;
+    const int64_t together = n_main + (apart ? 0 : n_state);
+    if (together > 0) gdn_short_conv_kernel<T, V, K><<<(unsigned)together, kThreads, smem, stream>>>(a);
+    if (apart && n_state > 0) {
+        a.first = a.n_main;
+        gdn_short_conv_kernel<T, V, K><<<(unsigned)n_state, kThreads, smem, stream>>>(a);
+    }
+    return launch_status();
+}
+
+template <typename T, int V, int K>
+gdn_status run_step(const gdn_conv_problem &p, const void *x, const float *weight,
+                    const float *bias, const void *state, void *out, void *next,
+                    cudaStream_t stream) {
+    StepArgs<T> a;
+    a.x = static_cast<const T *>(x);
+    a.weight = weight;
+    a.bias = bias;
+    a.state = static_cast<const T *>(state);
+    a.out = static_cast<T *>(out);
+    a.next = static_cast<T *>(next);
+    a.N = p.num_seqs;
+    a.C = p.channels;
+    a.xs = p.x_stride;
+    a.os = p.out_stride;
+    a.act = p.activation == GDN_ACT_SILU;
+    const int words = p.channels / V;
+    a.tx = threads_along(words);
+    a.n_chan = (words + a.tx - 1) / a.tx;
+    const int ty = kThreads / a.tx;
+    auto blocks = [&](int run) {
+        return (int64_t)a.n_chan * ((p.num_seqs + (int64_t)run * ty - 1) / ((int64_t)run * ty));
+    };
+    a.run = 4;
+    while (a.run > 1 && blocks(a.run) < 4 * kGridSms) a.run /= 2;
+    if (blocks(a.run) > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    gdn_short_conv_step_kernel<T, V, K>
+        <<<(unsigned)blocks(a.run), kThreads, (size_t)a.tx * V * K * sizeof(float), stream>>>(a);
+    return launch_status();
+}
+
+// f(V, K) of one element type: the word width by `wide`, K by the width.
+#define GDN_CONV_DISPATCH(run, T)                                                              \
+    switch (p.width) {                                                                         \
+        case 2: return wide ? run<T, kWide<T>, 2>(GDN_CONV_ARGS) : run<T, 1, 2>(GDN_CONV_ARGS); \
+        case 3: return wide ? run<T, kWide<T>, 3>(GDN_CONV_ARGS) : run<T, 1, 3>(GDN_CONV_ARGS); \
+        case 4: return wide ? run<T, kWide<T>, 4>(GDN_CONV_ARGS) : run<T, 1, 4>(GDN_CONV_ARGS); \
+        case 5: return wide ? run<T, kWide<T>, 5>(GDN_CONV_ARGS) : run<T, 1, 5>(GDN_CONV_ARGS); \
+        case 6: return wide ? run<T, kWide<T>, 6>(GDN_CONV_ARGS) : run<T, 1, 6>(GDN_CONV_ARGS); \
+        case 7: return wide ? run<T, kWide<T>, 7>(GDN_CONV_ARGS) : run<T, 1, 7>(GDN_CONV_ARGS); \
+        case 8: return wide ? run<T, kWide<T>, 8>(GDN_CONV_ARGS) : run<T, 1, 8>(GDN_CONV_ARGS); \
+    }                                                                                          \
+    return GDN_ERR_UNSUPPORTED;
+
+template <typename T>
+gdn_status conv_typed(const gdn_conv_problem &p, const void *x, const float *weight,
+                      const float *bias, const int32_t *cu, const void *init, void *out,
+                      void *fin, cudaStream_t stream) {
+    const bool wide = p.channels % kWide<T> == 0 && rows_aligned16<T>(x, p.x_stride) &&
+                      rows_aligned16<T>(out, p.out_stride) && rows_aligned16<T>(init, 0) &&
+                      rows_aligned16<T>(fin, 0);
+#define GDN_CONV_ARGS p, x, weight, bias, cu, init, out, fin, stream
+    GDN_CONV_DISPATCH(run_conv, T)
+#undef GDN_CONV_ARGS
+}
+
+template <typename T>
+gdn_status step_typed(const gdn_conv_problem &p, const void *x, const float *weight,
+                      const float *bias, const void *state, void *out, void *next,
+                      cudaStream_t stream) {
+    const bool wide = p.channels % kWide<T> == 0 && rows_aligned16<T>(x, p.x_stride) &&
+                      rows_aligned16<T>(out, p.out_stride) && rows_aligned16<T>(state, 0) &&
+                      rows_aligned16<T>(next, 0);
+#define GDN_CONV_ARGS p, x, weight, bias, state, out, next, stream
+    GDN_CONV_DISPATCH(run_step, T)
+#undef GDN_CONV_ARGS
+}
+
+}  // namespace
+
+gdn_status launch_short_conv(const gdn_conv_problem &p, const void *x, const float *weight,
+                             const float *bias, const int32_t *cu, const void *init, void *out,
+                             void *fin, cudaStream_t stream) {
+    return p.dtype == GDN_BF16
+               ? conv_typed<__nv_bfloat16>(p, x, weight, bias, cu, init, out, fin, stream)
+               : conv_typed<float>(p, x, weight, bias, cu, init, out, fin, stream);
+}
+
+gdn_status launch_short_conv_step(const gdn_conv_problem &p, const void *x, const float *weight,
+                                  const float *bias, const void *state, void *out, void *next,
+                                  cudaStream_t stream) {
+    return p.dtype == GDN_BF16
+               ? step_typed<__nv_bfloat16>(p, x, weight, bias, state, out, next, stream)
+               : step_typed<float>(p, x, weight, bias, state, out, next, stream);
+}
+
+}  // namespace gdn
