@@ -31,6 +31,7 @@
 // Windows of a fixed length balance exactly, and a window whose end falls
 // between two sequences skips step 1.
 #include <atomic>
+#include <initializer_list>
 
 #include "block.cuh"
 
@@ -55,7 +56,10 @@ template <typename T> struct ScanArgs {
     int per_group, tiles;  // channels per group, blocks per group
     int W, len;            // windows, tokens per window
     int64_t xs, dts, bs, cs, zs, os;
-    bool softplus, wide, defer;
+    int in_word, bc_word;  // CopyWord of x, dt, z and of B, C
+    bool softplus, defer;
+    bool pairs;        // out's rows are aligned to two elements
+    bool state_words;  // A, the states and the workspace allow 16-byte words
 };
 
 __device__ __forceinline__ uint64_t pack2f(float a, float b) {
@@ -79,11 +83,12 @@ __device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
-__device__ __forceinline__ void copy16_async(void *smem, const void *gmem) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                     static_cast<uint32_t>(__cvta_generic_to_shared(smem))),
-                 "l"(gmem)
-                 : "memory");
+template <int BYTES> __device__ __forceinline__ void copy_async(void *smem, const void *gmem) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(gmem) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(gmem) : "memory");
 }
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
@@ -104,6 +109,29 @@ template <typename T, int NS> struct ScanThread {
     int d;      // first channel
     int valid;  // channels of this thread that exist
 
+    // This thread's part of row `row` of a [rows, D, S] array (zeros where it
+    // has none), in 16-byte words where the array allows.
+    __device__ __forceinline__ void read(const ScanArgs<T> &a, const float *from, int64_t row,
+                                         float scale, uint64_t (&to)[CH][NP]) const {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const float *p0 = from + (row * a.D + d + c) * a.S;
+            const bool ok = from && c < valid;
+#pragma unroll
+            for (int q = 0; q < NP / 2; ++q) {
+                float v[4] = {0.f, 0.f, 0.f, 0.f};
+                if (a.state_words) {
+                    if (ok && 4 * q < a.S) Vec<float, 4>::load(p0 + 4 * q).to(v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (ok && 4 * q + i < a.S) v[i] = p0[4 * q + i];
+                }
+                to[c][2 * q] = pack2f(scale * v[0], scale * v[1]);
+                to[c][2 * q + 1] = pack2f(scale * v[2], scale * v[3]);
+            }
+        }
+    }
     __device__ __forceinline__ void setup(const ScanArgs<T> &a, int group, int in_group) {
         d = group * a.per_group + in_group;
         valid = min(max(a.per_group - in_group, 0), CH);
@@ -112,41 +140,28 @@ template <typename T, int NS> struct ScanThread {
             const bool ok = c < valid;
             bias[c] = ok && a.bias ? a.bias[d + c] : 0.f;
             skip[c] = ok && a.skip ? a.skip[d + c] : 0.f;
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                float v[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    v[i] = ok && 2 * p + i < a.S
-                               ? kLog2e * a.A[(int64_t)(d + c) * a.S + 2 * p + i] : 0.f;
-                A[c][p] = pack2f(v[0], v[1]);
-            }
         }
+        read(a, a.A, 0, kLog2e, A);
     }
-    // States of this thread's channels at row `row` of a [rows, D, S] array.
     __device__ __forceinline__ void load(const ScanArgs<T> &a, const float *from, int64_t row) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const float *p0 = from + (row * a.D + d + c) * a.S;
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                float v[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    v[i] = from && c < valid && 2 * p + i < a.S ? p0[2 * p + i] : 0.f;
-                h[c][p] = pack2f(v[0], v[1]);
-            }
-        }
+        read(a, from, row, 1.f, h);
     }
     __device__ __forceinline__ void store(const ScanArgs<T> &a, float *to, int64_t row) const {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             float *p0 = to + (row * a.D + d + c) * a.S;
+            if (c >= valid) continue;
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                const float2 v = unpack2f(h[c][p]);
-                if (c < valid && 2 * p < a.S) p0[2 * p] = v.x;
-                if (c < valid && 2 * p + 1 < a.S) p0[2 * p + 1] = v.y;
+            for (int q = 0; q < NP / 2; ++q) {
+                const float2 u = unpack2f(h[c][2 * q]), w = unpack2f(h[c][2 * q + 1]);
+                const float v[4] = {u.x, u.y, w.x, w.y};
+                if (a.state_words) {
+                    if (4 * q < a.S) Vec<float, 4>::from(v).store(p0 + 4 * q);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (4 * q + i < a.S) p0[4 * q + i] = v[i];
+                }
             }
         }
     }
@@ -189,61 +204,72 @@ template <typename T, int NS> struct ScanThread {
     }
 };
 
-// Shared memory of a block: two tiles of x, dt (and z), and of B (and C).
+// How rows may be copied into shared memory: whole 16-byte words, 4-byte
+// words, or element by element (16-bit rows at odd elements).
+enum CopyWord : int { kCopy16 = 16, kCopy4 = 4, kCopyElement = 0 };
+
+// `rows` rows of `cols` elements from `src` (rows `stride` apart) to `dst`
+// (rows `pitch` apart): a warp takes every n-th row, its lanes the row's words.
+template <typename T>
+__device__ __forceinline__ void copy_rows(T *dst, int pitch, const T *src, int64_t stride,
+                                          int rows, int cols, int word) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    const int step = word == kCopy16 ? kWide<T> : word == kCopy4 ? 4 / (int)sizeof(T) : 1;
+    for (int c = lane * step; c < cols; c += 32 * step) {
+        int r = threadIdx.x / 32;
+        const T *from = src + r * stride + c;
+        T *to = dst + r * pitch + c;
+        const int64_t next = warps * stride;
+#pragma unroll 4
+        for (; r < rows; r += warps, from += next, to += warps * pitch) {
+            if (word == kCopy16) copy_async<16>(to, from);
+            else if (word == kCopy4) copy_async<4>(to, from);
+            else *to = *from;
+        }
+    }
+}
+
+// Shared memory of a block: two tiles of x, dt (and z), two of B (and C) as
+// they lie in global memory, and one of B (and C) as fp32, zero past the last
+// state.
 template <typename T, int NS, bool OUT> struct ScanTiles {
     static constexpr int CH = kChannels<NS>;
-    T *in[2];      // [tensor][token][channel]
-    float *bc[2];  // [B, C][token][state]
+    static constexpr int kIn = OUT ? 3 : 2, kBC = OUT ? 2 : 1;
+    float *bc;     // [B, C][token][state]
+    T *raw[2];     // the same, as loaded
+    T *in[2];      // [x, dt, z][token][channel]
     int width;     // channels per block
     __device__ ScanTiles(char *smem, int threads) : width(threads * CH) {
-        bc[0] = reinterpret_cast<float *>(smem);
-        bc[1] = bc[0] + (OUT ? 2 : 1) * kTile * NS;
-        in[0] = reinterpret_cast<T *>(bc[1] + (OUT ? 2 : 1) * kTile * NS);
-        in[1] = in[0] + (OUT ? 3 : 2) * kTile * width;
+        bc = reinterpret_cast<float *>(smem);
+        raw[0] = reinterpret_cast<T *>(bc + kBC * kTile * NS);
+        raw[1] = raw[0] + kBC * kTile * NS;
+        in[0] = raw[1] + kBC * kTile * NS;
+        in[1] = in[0] + kIn * kTile * width;
     }
     static size_t bytes(int threads) {
-        return 2 * ((OUT ? 2 : 1) * kTile * NS * sizeof(float) +
-                    (OUT ? 3 : 2) * kTile * threads * CH * sizeof(T));
+        return kBC * kTile * NS * (sizeof(float) + 2 * sizeof(T)) +
+               2 * kIn * kTile * threads * CH * sizeof(T);
     }
-    // The inputs of tokens [t, te) for this block's channels, d0 the first.
-    __device__ __forceinline__ void inputs(const ScanArgs<T> &a, int buf, int t, int te, int d0,
-                                           int in_group0) const {
-        constexpr int V = kWide<T>;
-        const int cols = min(width, a.per_group - in_group0);
-        const T *src[3] = {a.x, a.dt, a.z};
-        const int64_t stride[3] = {a.xs, a.dts, a.zs};
-        if (a.wide) {
-            const int words = cols / V;
-            for (int i = threadIdx.x; i < kTile * words; i += blockDim.x) {
-                const int r = i / words, c = (i % words) * V;
-                if (t + r >= te) break;
-#pragma unroll
-                for (int k = 0; k < (OUT ? 3 : 2); ++k)
-                    if (k < 2 || a.z)
-                        copy16_async(in[buf] + (k * kTile + r) * width + c,
-                                     src[k] + (t + r) * stride[k] + d0 + c);
-            }
-        } else {
-            for (int i = threadIdx.x; i < kTile * cols; i += blockDim.x) {
-                const int r = i / cols, c = i % cols;
-                if (t + r >= te) break;
-#pragma unroll
-                for (int k = 0; k < (OUT ? 3 : 2); ++k)
-                    if (k < 2 || a.z)
-                        in[buf][(k * kTile + r) * width + c] =
-                            src[k][(t + r) * stride[k] + d0 + c];
-            }
-        }
+    // Starts the copies of tokens [t, te) (one tile at most) of the block's
+    // channels, d the first of `cols`.
+    __device__ __forceinline__ void load(const ScanArgs<T> &a, int buf, int t, int te, int d,
+                                         int cols, int group) const {
+        const int rows = min(te - t, kTile);
+        copy_rows(in[buf], width, a.x + t * a.xs + d, a.xs, rows, cols, a.in_word);
+        copy_rows(in[buf] + kTile * width, width, a.dt + t * a.dts + d, a.dts, rows, cols,
+                  a.in_word);
+        if (OUT && a.z)
+            copy_rows(in[buf] + 2 * kTile * width, width, a.z + t * a.zs + d, a.zs, rows, cols,
+                      a.in_word);
+        copy_rows(raw[buf], NS, a.B + t * a.bs + group * a.S, a.bs, rows, a.S, a.bc_word);
+        if (OUT)
+            copy_rows(raw[buf] + kTile * NS, NS, a.C + t * a.cs + group * a.S, a.cs, rows, a.S,
+                      a.bc_word);
     }
-    // B and C of the same tokens as fp32, zero past the last state.
-    __device__ __forceinline__ void states(const ScanArgs<T> &a, int buf, int t, int te,
-                                           int group) const {
-        for (int i = threadIdx.x; i < kTile * NS; i += blockDim.x) {
-            const int r = i / NS, n = i % NS;
-            const bool ok = t + r < te && n < a.S;
-            bc[buf][i] = ok ? to_f32(a.B[(t + r) * a.bs + group * a.S + n]) : 0.f;
-            if (OUT) bc[buf][kTile * NS + i] = ok ? to_f32(a.C[(t + r) * a.cs + group * a.S + n]) : 0.f;
-        }
+    // B and C of the tile that has arrived, to fp32.
+    __device__ __forceinline__ void widen(const ScanArgs<T> &a, int buf) const {
+        for (int i = threadIdx.x; i < kBC * kTile * NS; i += blockDim.x)
+            bc[i] = i % NS < a.S ? to_f32(raw[buf][i]) : 0.f;
     }
 };
 
@@ -262,8 +288,7 @@ __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS>
             xv[c] = to_f32(in[c]);
             dv[c] = to_f32(in[kTile * tl.width + c]);
         }
-        th.template token<OUT>(a.softplus, xv, dv, tl.bc[buf] + r * NS,
-                               tl.bc[buf] + (kTile + r) * NS, y);
+        th.template token<OUT>(a.softplus, xv, dv, tl.bc + r * NS, tl.bc + (kTile + r) * NS, y);
         if (OUT) {
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
@@ -271,7 +296,7 @@ __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS>
                 if (a.z) y[c] *= silu(to_f32(in[2 * kTile * tl.width + c]));
             }
             T *o = a.out + (t + u) * a.os + th.d;
-            if (CH == 2 && a.wide) {
+            if (CH == 2 && a.pairs) {
                 if (th.valid) {
                     if constexpr (sizeof(T) == 2) {
                         *reinterpret_cast<__nv_bfloat162 *>(o) = __floats2bfloat162_rn(y[0], y[CH - 1]);
@@ -331,17 +356,16 @@ __global__ void __launch_bounds__(kMaxThreads, NS <= 16 ? 4 : 2) gdn_scan_kernel
 #pragma unroll
     for (int c = 0; c < th.CH; ++c) th.sum[c] = 0.f;
 
-    tl.inputs(a, 0, t0, t1, d0, in_group0);
-    tl.states(a, 0, t0, t1, group);
+    const int cols = min(tl.width, a.per_group - in_group0);
+    tl.load(a, 0, t0, t1, d0, cols, group);
     int buf = 0;
     for (int tt = t0; tt < t1; tt += kTile, buf ^= 1) {
         const int te = min(tt + kTile, t1);
         copies_wait();
+        __syncthreads();  // the tile has arrived, and the one before is done with
+        tl.widen(a, buf);
+        if (te < t1) tl.load(a, buf ^ 1, te, t1, d0, cols, group);
         __syncthreads();
-        if (te < t1) {
-            tl.inputs(a, buf ^ 1, te, t1, d0, in_group0);
-            tl.states(a, buf ^ 1, te, t1, group);
-        }
         int t = tt;
         while (t < te) {
             const int e = min(te, s.end);
@@ -384,13 +408,22 @@ __global__ void __launch_bounds__(kCombineThreads) gdn_scan_combine_kernel(const
     if (i >= ds) return;
     const float rate = kLog2e * a.A[i];
     const int d = (int)(i / a.S);
+    constexpr int kAhead = 8;  // windows loaded at once: only the products are sequential
     float c = 0.f;
-#pragma unroll 4
-    for (int w = 0; w < a.W - 1; ++w) {
-        const float h = a.carry[w * ds + i];
-        const float kept = ex2(rate * a.steps[(int64_t)w * a.D + d]) * c;
-        c = inside[w] ? h : h + kept;
-        a.carry[w * ds + i] = c;
+    for (int w0 = 0; w0 < a.W - 1; w0 += kAhead) {
+        float h[kAhead], kept[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int w = min(w0 + k, a.W - 2);
+            h[k] = a.carry[w * ds + i];
+            kept[k] = a.steps[(int64_t)w * a.D + d];
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (w0 + k >= a.W - 1) break;
+            c = inside[w0 + k] ? h[k] : fmaf(ex2(rate * kept[k]), c, h[k]);
+            a.carry[(w0 + k) * ds + i] = c;
+        }
     }
 }
 
@@ -569,9 +602,18 @@ gdn_status scan_typed(const gdn_ssm_problem &p, const void *x, const void *dt, c
     a.out = static_cast<T *>(out);
     a.fin = fin;
     a.defer = fin && fin == init;
-    a.wide = a.per_group % kWide<T> == 0 && rows_aligned16<T>(x, p.x_stride) &&
-             rows_aligned16<T>(dt, p.dt_stride) && rows_aligned16<T>(z, p.z_stride) &&
-             rows_aligned16<T>(out, p.out_stride);
+    // The widest word that all of these rows allow.
+    auto word = [](std::initializer_list<const void *> ptrs, std::initializer_list<int64_t> sizes) {
+        uint64_t bits = 0;
+        for (const void *q : ptrs) bits |= reinterpret_cast<uintptr_t>(q);
+        for (int64_t n : sizes) bits |= (uint64_t)n * sizeof(T);
+        return bits % 16 == 0 ? kCopy16 : bits % 4 == 0 ? kCopy4 : kCopyElement;
+    };
+    a.in_word = word({x, dt, z}, {p.x_stride, p.dt_stride, z ? p.z_stride : 0, a.per_group});
+    a.bc_word = word({B, C}, {p.b_stride, p.c_stride, p.state_dim});
+    a.state_words = p.state_dim % 4 == 0 && aligned16(A) && aligned16(init) && aligned16(fin);
+    a.pairs = (reinterpret_cast<uintptr_t>(out) | (uint64_t)p.out_stride * sizeof(T)) %
+                      (2 * sizeof(T)) == 0 && a.per_group % 2 == 0;
     // Only a batch of several sequences (or of no tokens) has empty ones.
     const bool empties = fin && fin != init && (p.num_seqs > 1 || p.total_tokens == 0);
     switch (pl.ns) {
