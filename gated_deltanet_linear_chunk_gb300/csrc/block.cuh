@@ -99,6 +99,34 @@ template <> struct Vec<__nv_bfloat16, 8> {
         return Vec{make_uint4(u[0], u[1], u[2], u[3])};
     }
 };
+template <> struct Vec<__nv_bfloat16, 2> {
+    uint32_t w;
+    __device__ __forceinline__ static Vec load(const __nv_bfloat16 *p) {
+        return Vec{*reinterpret_cast<const uint32_t *>(p)};
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        *reinterpret_cast<uint32_t *>(p) = w;
+    }
+    __device__ __forceinline__ void to(float *r) const {
+        r[0] = __uint_as_float(w << 16);
+        r[1] = __uint_as_float(w & 0xffff0000u);
+    }
+    __device__ __forceinline__ static Vec from(const float *r) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(r[0], r[1]);
+        return Vec{*reinterpret_cast<const uint32_t *>(&h)};
+    }
+};
+template <> struct Vec<float, 2> {
+    float2 w;
+    __device__ __forceinline__ static Vec load(const float *p) {
+        return Vec{*reinterpret_cast<const float2 *>(p)};
+    }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<float2 *>(p) = w; }
+    __device__ __forceinline__ void to(float *r) const { r[0] = w.x; r[1] = w.y; }
+    __device__ __forceinline__ static Vec from(const float *r) {
+        return Vec{make_float2(r[0], r[1])};
+    }
+};
 template <typename T> constexpr int kWide = 16 / (int)sizeof(T);
 
 // Whether rows at p, `stride` elements apart, start on 16-byte boundaries.

@@ -445,45 +445,108 @@ template <typename T> struct ScanStepArgs {
     const float *A, *skip, *bias, *state;
     T *out;
     float *next;
-    int N, D, S, per_group;
+    int N, D, S, per_group, tiles;  // tiles of 32 channels per group
     int64_t xs, dts, bs, cs, zs, os;
-    bool softplus;
+    bool softplus, bc_words;        // bc_words: B and C allow four elements at a time
 };
 
-// L lanes per channel, V consecutive states per lane at a time.
-template <typename T, int V, int L>
+// Four elements, aligned to four.
+__device__ __forceinline__ void load4(const float *p, float *r) { Vec<float, 4>::load(p).to(r); }
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *r) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    Vec<__nv_bfloat16, 2>{w.x}.to(r);
+    Vec<__nv_bfloat16, 2>{w.y}.to(r + 2);
+}
+
+// A warp takes 32 channels of one group through sequences a grid apart.  Each
+// lane first reads one channel's dt, x and z and forms its step; then L lanes
+// share a channel, each with V consecutive states (J times L V apart), and the
+// channels pass in rounds of 32 / L, their steps fetched from the lanes that
+// formed them and their sums returned there.  B and C, which depend only on
+// the lane's states, are read once per sequence, and all states of four
+// rounds are in flight at once.
+template <typename T, int V, int L, int J>
 __global__ void __launch_bounds__(kStepThreads) gdn_scan_step_kernel(const ScanStepArgs<T> a) {
-    const int lane = threadIdx.x % L;
-    const int d = blockIdx.x * (kStepThreads / L) + threadIdx.x / L;
-    const bool ok = d < a.D;
-    const int dd = ok ? d : a.D - 1, g = dd / a.per_group;
-    for (int64_t n = blockIdx.y; n < a.N; n += gridDim.y) {
-        float s = to_f32(a.dt[n * a.dts + dd]) + (a.bias ? a.bias[dd] : 0.f);
-        if (a.softplus) s = softplus(s);
-        const float xv = to_f32(a.x[n * a.xs + dd]);
-        const float u = s * xv;
-        float y = 0.f;
-        const int64_t row = (n * a.D + dd) * a.S;
-        for (int j0 = lane * V; ok && j0 < a.S; j0 += L * V) {
-            float h[V], A[V];
-            Vec<float, V>::load(a.state + row + j0).to(h);
-            Vec<float, V>::load(a.A + (int64_t)dd * a.S + j0).to(A);
+    constexpr int R = 32 / L;           // channels per round
+    constexpr int Q = L < 4 ? L : 4;    // rounds at once
+    const int lane = threadIdx.x & 31, part = lane % L;
+    const int g = blockIdx.x / a.tiles, in_group = (blockIdx.x % a.tiles) * 32;
+    const int d0 = g * a.per_group + in_group, count = min(32, a.per_group - in_group);
+    const int dl = d0 + min(lane, count - 1);  // this lane's channel
+    const float bias = a.bias ? a.bias[dl] : 0.f, skip = a.skip ? a.skip[dl] : 0.f;
+    for (int64_t n = blockIdx.y * (kStepThreads / 32) + threadIdx.x / 32; n < a.N;
+         n += gridDim.y * (kStepThreads / 32)) {
+        float s = to_f32(a.dt[n * a.dts + dl]) + bias;
+        const float x = to_f32(a.x[n * a.xs + dl]);
+        const float z = a.z ? to_f32(a.z[n * a.zs + dl]) : 0.f;
+        float B[J][V], C[J][V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float b = to_f32(a.B[n * a.bs + g * a.S + j0 + i]);
-                const float c = to_f32(a.C[n * a.cs + g * a.S + j0 + i]);
-                h[i] = fmaf(ex2(s * (kLog2e * A[i])), h[i], u * b);
-                y = fmaf(c, h[i], y);
+        for (int j = 0; j < J; ++j) {
+            const int k = (j * L + part) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) B[j][i] = C[j][i] = 0.f;
+            if (k < a.S) {
+                if (V == 4 && a.bc_words) {
+                    load4(a.B + n * a.bs + g * a.S + k, B[j]);
+                    load4(a.C + n * a.cs + g * a.S + k, C[j]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        B[j][i] = to_f32(a.B[n * a.bs + g * a.S + k + i]);
+                        C[j][i] = to_f32(a.C[n * a.cs + g * a.S + k + i]);
+                    }
+                }
             }
-            Vec<float, V>::from(h).store(a.next + row + j0);
         }
+        if (a.softplus) s = softplus(s);
+        float mine = 0.f;  // this lane's channel's sum
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-        if (ok && lane == 0) {
-            if (a.skip) y = fmaf(a.skip[dd], xv, y);
-            if (a.z) y *= silu(to_f32(a.z[n * a.zs + dd]));
-            a.out[n * a.os + dd] = from_f32<T>(y);
+        for (int r0 = 0; r0 < L; r0 += Q) {
+            if (r0 * R >= count) break;
+            Vec<float, V> h[Q][J], A[Q][J];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int ch = (r0 + q) * R + lane / L;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int k = (j * L + part) * V;
+                    h[q][j] = A[q][j] = Vec<float, V>::zero();
+                    if (ch < count && k < a.S) {
+                        h[q][j] = Vec<float, V>::load(a.state + (n * a.D + d0 + ch) * a.S + k);
+                        A[q][j] = Vec<float, V>::load(a.A + (int64_t)(d0 + ch) * a.S + k);
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int ch = (r0 + q) * R + lane / L;
+                const float sc = __shfl_sync(0xffffffffu, s, ch);
+                const float uc = sc * __shfl_sync(0xffffffffu, x, ch);
+                float y = 0.f;
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    const int k = (j * L + part) * V;
+                    float hv[V], av[V];
+                    h[q][j].to(hv);
+                    A[q][j].to(av);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        hv[i] = fmaf(ex2(sc * (kLog2e * av[i])), hv[i], uc * B[j][i]);
+                        y = fmaf(C[j][i], hv[i], y);
+                    }
+                    if (ch < count && k < a.S)
+                        Vec<float, V>::from(hv).store(a.next + (n * a.D + d0 + ch) * a.S + k);
+                }
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+                // Channel ch's sum goes to lane ch.
+                const float back = __shfl_sync(0xffffffffu, y, (lane % R) * L);
+                if (lane / R == r0 + q) mine = back;
+            }
         }
+        mine = fmaf(skip, x, mine);
+        if (a.z) mine *= silu(z);
+        if (lane < count) a.out[n * a.os + dl] = from_f32<T>(mine);
     }
 }
 
@@ -626,12 +689,13 @@ gdn_status scan_typed(const gdn_ssm_problem &p, const void *x, const void *dt, c
     return GDN_ERR_UNSUPPORTED;
 }
 
-template <typename T, int V, int L>
+template <typename T, int V, int L, int J>
 void run_scan_step(const ScanStepArgs<T> &a, cudaStream_t stream) {
-    const int per_block = kStepThreads / L;
-    const unsigned gx = (unsigned)((a.D + per_block - 1) / per_block);
-    const unsigned gy = (unsigned)(a.N < 65535 ? a.N : 65535);
-    gdn_scan_step_kernel<T, V, L><<<dim3(gx, gy), kStepThreads, 0, stream>>>(a);
+    const int64_t blocks = (int64_t)a.tiles * (a.D / a.per_group);
+    const int64_t rows = (a.N + kStepThreads / 32 - 1) / (kStepThreads / 32);
+    gdn_scan_step_kernel<T, V, L, J>
+        <<<dim3((unsigned)blocks, (unsigned)(rows < 65535 ? rows : 65535)), kStepThreads, 0,
+           stream>>>(a);
 }
 
 template <typename T>
@@ -662,18 +726,25 @@ gdn_status scan_step_typed(const gdn_ssm_problem &p, const void *x, const void *
     a.zs = p.z_stride;
     a.os = p.out_stride;
     a.softplus = p.dt_softplus != 0;
+    a.tiles = (a.per_group + 31) / 32;
     const bool wide = p.state_dim % 4 == 0 && aligned16(state) && aligned16(next) && aligned16(A);
-    const int lanes = wide ? p.state_dim / 4 : p.state_dim;
+    a.bc_words = ((reinterpret_cast<uintptr_t>(B) | reinterpret_cast<uintptr_t>(C) |
+                   (uint64_t)p.b_stride * sizeof(T) | (uint64_t)p.c_stride * sizeof(T)) %
+                  (4 * sizeof(T))) == 0;
+    const int S = p.state_dim;
     if (wide) {
-        if (lanes <= 1) run_scan_step<T, 4, 1>(a, stream);
-        else if (lanes <= 2) run_scan_step<T, 4, 2>(a, stream);
-        else if (lanes <= 4) run_scan_step<T, 4, 4>(a, stream);
-        else if (lanes <= 8) run_scan_step<T, 4, 8>(a, stream);
-        else run_scan_step<T, 4, 16>(a, stream);
+        if (S <= 4) run_scan_step<T, 4, 1, 1>(a, stream);
+        else if (S <= 8) run_scan_step<T, 4, 2, 1>(a, stream);
+        else if (S <= 16) run_scan_step<T, 4, 4, 1>(a, stream);
+        else if (S <= 32) run_scan_step<T, 4, 8, 1>(a, stream);
+        else run_scan_step<T, 4, 16, 1>(a, stream);
     } else {
-        if (lanes <= 1) run_scan_step<T, 1, 1>(a, stream);
-        else if (lanes <= 8) run_scan_step<T, 1, 8>(a, stream);
-        else run_scan_step<T, 1, 16>(a, stream);
+        if (S <= 1) run_scan_step<T, 1, 1, 1>(a, stream);
+        else if (S <= 4) run_scan_step<T, 1, 4, 1>(a, stream);
+        else if (S <= 8) run_scan_step<T, 1, 8, 1>(a, stream);
+        else if (S <= 16) run_scan_step<T, 1, 16, 1>(a, stream);
+        else if (S <= 32) run_scan_step<T, 1, 16, 2>(a, stream);
+        else run_scan_step<T, 1, 16, 4>(a, stream);
     }
     return launch_status();
 }

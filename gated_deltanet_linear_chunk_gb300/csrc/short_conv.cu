@@ -19,7 +19,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kStep = 4;  // tokens loaded at once
+constexpr int kStep = 8;  // tokens loaded at once
 
 template <typename T> struct ConvArgs {
     const T *x;
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) gdn_short_conv_kernel(const ConvArgs
         b[v] = a.bias ? a.bias[c + v] : 0.f;
     }
     Span s = locate(a.cu, a.N, a.T_, (int)first);
-    float in[K - 1 + kStep][V];  // the K - 1 inputs before a block, and the block's
+    float in[K][V];  // the K - 1 inputs before a token, and the token's
     bool have = false;
     for (int t = (int)first; t < t1; t += kStep) {
         if (t >= s.end) {
@@ -107,32 +107,33 @@ __global__ void __launch_bounds__(kThreads) gdn_short_conv_kernel(const ConvArgs
         }
         if (t + kStep <= min(s.end, t1)) {
             Vec<T, V> word[kStep];
+            const T *from = a.x + t * a.xs + c;
 #pragma unroll
-            for (int u = 0; u < kStep; ++u) word[u] = Vec<T, V>::load(a.x + (t + u) * a.xs + c);
+            for (int u = 0; u < kStep; ++u, from += a.xs) word[u] = Vec<T, V>::load(from);
             if (!have) {
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j)
                     tap<T, V, K>(a, s.n, s.start, t - (K - 1) + j, c).to(in[j]);
                 have = true;
             }
+            T *to = a.out + t * a.os + c;
 #pragma unroll
-            for (int u = 0; u < kStep; ++u) word[u].to(in[K - 1 + u]);
-#pragma unroll
-            for (int u = 0; u < kStep; ++u) {
+            for (int u = 0; u < kStep; ++u, to += a.os) {
+                word[u].to(in[K - 1]);
                 float y[V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     y[v] = b[v];
 #pragma unroll
-                    for (int j = 0; j < K; ++j) y[v] = fmaf(w[j][v], in[u + j][v], y[v]);
-                    if (a.act) y[v] = silu(y[v]);
+                    for (int j = 0; j < K; ++j) y[v] = fmaf(w[j][v], in[j][v], y[v]);
+#pragma unroll
+                    for (int j = 0; j < K - 1; ++j) in[j][v] = in[j + 1][v];
                 }
-                Vec<T, V>::from(y).store(a.out + (t + u) * a.os + c);
+                if (a.act)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) y[v] = silu(y[v]);
+                Vec<T, V>::from(y).store(to);
             }
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) in[j][v] = in[kStep + j][v];
         } else {
             const int te = min(t + kStep, t1);
 #pragma unroll 1
@@ -240,7 +241,7 @@ gdn_status run_conv(const gdn_conv_problem &p, const void *x, const float *weigh
         return (int64_t)a.n_chan * ((p.total_tokens + (int64_t)run * ty - 1) / ((int64_t)run * ty));
     };
     a.run = 32;
-    while (a.run > kStep && blocks(a.run) < 8 * kGridSms) a.run /= 2;
+    while (a.run > 1 && blocks(a.run) < 8 * kGridSms) a.run /= 2;
     const int64_t n_main = blocks(a.run);
     const int64_t n_state =
         fin ? ((int64_t)p.num_seqs * words + kThreads - 1) / kThreads : 0;
