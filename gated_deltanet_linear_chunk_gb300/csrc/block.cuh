@@ -46,6 +46,40 @@ __device__ __forceinline__ float softplus(float v) {
     return fmaf(p, e, fmaxf(v, 0.f));
 }
 
+// ------------------------------------------------------- pairs of fp32 values
+// Two values in one 64-bit register pair, and the packed operations on them.
+__device__ __forceinline__ uint64_t pack2f(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2f(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+// silu of both.
+__device__ __forceinline__ uint64_t silu2(uint64_t v) {
+    const float2 e = unpack2f(fmul2(v, pack2f(-kLog2e, -kLog2e)));
+    const float2 f = unpack2f(fadd2(pack2f(ex2(e.x), ex2(e.y)), pack2f(1.f, 1.f)));
+    return fmul2(v, pack2f(rcp(f.x), rcp(f.y)));
+}
+
 // ------------------------------------------------------------- vector access
 // V consecutive elements: one 16-byte word (16 / sizeof(T) elements) or one
 // element (V = 1).

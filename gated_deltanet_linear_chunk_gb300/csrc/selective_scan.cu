@@ -62,27 +62,6 @@ template <typename T> struct ScanArgs {
     bool state_words;  // A, the states and the workspace allow 16-byte words
 };
 
-__device__ __forceinline__ uint64_t pack2f(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2f(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
 template <int BYTES> __device__ __forceinline__ void copy_async(void *smem, const void *gmem) {
     const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
     if constexpr (BYTES == 16)
@@ -445,7 +424,8 @@ template <typename T> struct ScanStepArgs {
     const float *A, *skip, *bias, *state;
     T *out;
     float *next;
-    int N, D, S, per_group, tiles;  // tiles of 32 channels per group
+    int N, D, S, per_group;
+    int tiles, run;                 // warps' channel tiles per group, sequences per warp
     int64_t xs, dts, bs, cs, zs, os;
     bool softplus, bc_words;        // bc_words: B and C allow four elements at a time
 };
@@ -458,95 +438,119 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *r) {
     Vec<__nv_bfloat16, 2>{w.y}.to(r + 2);
 }
 
-// A warp takes 32 channels of one group through sequences a grid apart.  Each
-// lane first reads one channel's dt, x and z and forms its step; then L lanes
-// share a channel, each with V consecutive states (J times L V apart), and the
-// channels pass in rounds of 32 / L, their steps fetched from the lanes that
-// formed them and their sums returned there.  B and C, which depend only on
-// the lane's states, are read once per sequence, and all states of four
-// rounds are in flight at once.
+// A warp takes Q R channels of one group through `run` sequences.  L lanes
+// share a channel, each with V consecutive states (J times L V apart); the
+// channels pass in Q rounds of R = 32 / L.  Lane i forms the step of channel
+// i, the rounds fetch it from there, and return their sums there.  The decay
+// rates stay in registers for all sequences; the next sequence's states and
+// inputs are loaded before the one at hand is computed, so that half the
+// state traffic is in flight at all times.
+template <typename T, int V, int L, int J> struct StepTile {
+    static constexpr int R = 32 / L;
+    static constexpr int Q = L < 4 ? L : 4;
+    static constexpr int kChannelsPerWarp = Q * R;
+};
+
 template <typename T, int V, int L, int J>
 __global__ void __launch_bounds__(kStepThreads) gdn_scan_step_kernel(const ScanStepArgs<T> a) {
-    constexpr int R = 32 / L;           // channels per round
-    constexpr int Q = L < 4 ? L : 4;    // rounds at once
+    using Tile = StepTile<T, V, L, J>;
+    constexpr int R = Tile::R, Q = Tile::Q, W = Tile::kChannelsPerWarp;
     const int lane = threadIdx.x & 31, part = lane % L;
-    const int g = blockIdx.x / a.tiles, in_group = (blockIdx.x % a.tiles) * 32;
-    const int d0 = g * a.per_group + in_group, count = min(32, a.per_group - in_group);
+    const int g = blockIdx.x / a.tiles, in_group = (blockIdx.x % a.tiles) * W;
+    const int d0 = g * a.per_group + in_group, count = min(W, a.per_group - in_group);
     const int dl = d0 + min(lane, count - 1);  // this lane's channel
+    const int64_t first = ((int64_t)blockIdx.y * (kStepThreads / 32) + threadIdx.x / 32) * a.run;
+    const int64_t last = min(first + a.run, (int64_t)a.N);
+    if (first >= last) return;
     const float bias = a.bias ? a.bias[dl] : 0.f, skip = a.skip ? a.skip[dl] : 0.f;
-    for (int64_t n = blockIdx.y * (kStepThreads / 32) + threadIdx.x / 32; n < a.N;
-         n += gridDim.y * (kStepThreads / 32)) {
-        float s = to_f32(a.dt[n * a.dts + dl]) + bias;
-        const float x = to_f32(a.x[n * a.xs + dl]);
-        const float z = a.z ? to_f32(a.z[n * a.zs + dl]) : 0.f;
-        float B[J][V], C[J][V];
+
+    // What a sequence brings: loaded one ahead.
+    struct Inputs {
+        float dt, x, z, B[J][V], C[J][V];
+        Vec<float, V> h[Q][J];
+    };
+    auto fetch = [&](Inputs &f, int64_t n) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int ch = q * R + lane / L, k = (j * L + part) * V;
+                f.h[q][j] = Vec<float, V>::zero();
+                if (ch < count && k < a.S)
+                    f.h[q][j] = Vec<float, V>::load(a.state + (n * a.D + d0 + ch) * a.S + k);
+            }
+        f.dt = to_f32(a.dt[n * a.dts + dl]);
+        f.x = to_f32(a.x[n * a.xs + dl]);
+        f.z = a.z ? to_f32(a.z[n * a.zs + dl]) : 0.f;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int k = (j * L + part) * V;
 #pragma unroll
-            for (int i = 0; i < V; ++i) B[j][i] = C[j][i] = 0.f;
+            for (int i = 0; i < V; ++i) f.B[j][i] = f.C[j][i] = 0.f;
             if (k < a.S) {
+                const T *b = a.B + n * a.bs + g * a.S + k, *c = a.C + n * a.cs + g * a.S + k;
                 if (V == 4 && a.bc_words) {
-                    load4(a.B + n * a.bs + g * a.S + k, B[j]);
-                    load4(a.C + n * a.cs + g * a.S + k, C[j]);
+                    load4(b, f.B[j]);
+                    load4(c, f.C[j]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        B[j][i] = to_f32(a.B[n * a.bs + g * a.S + k + i]);
-                        C[j][i] = to_f32(a.C[n * a.cs + g * a.S + k + i]);
+                        f.B[j][i] = to_f32(b[i]);
+                        f.C[j][i] = to_f32(c[i]);
                     }
                 }
             }
         }
+    };
+    Inputs cur, ahead;
+    fetch(cur, first);
+    float A[Q][J][V];
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int ch = q * R + lane / L, k = (j * L + part) * V;
+            Vec<float, V> w = Vec<float, V>::zero();
+            if (ch < count && k < a.S)
+                w = Vec<float, V>::load(a.A + (int64_t)(d0 + ch) * a.S + k);
+            w.to(A[q][j]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) A[q][j][i] *= kLog2e;
+        }
+    for (int64_t n = first; n < last; ++n) {
+        if (n + 1 < last) fetch(ahead, n + 1);
+        float s = cur.dt + bias;
         if (a.softplus) s = softplus(s);
-        float mine = 0.f;  // this lane's channel's sum
+        float sum = 0.f;  // this lane's channel's
 #pragma unroll
-        for (int r0 = 0; r0 < L; r0 += Q) {
-            if (r0 * R >= count) break;
-            Vec<float, V> h[Q][J], A[Q][J];
+        for (int q = 0; q < Q; ++q) {
+            const int ch = q * R + lane / L;
+            const float sc = __shfl_sync(0xffffffffu, s, ch);
+            const float uc = sc * __shfl_sync(0xffffffffu, cur.x, ch);
+            float y = 0.f;
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                const int ch = (r0 + q) * R + lane / L;
+            for (int j = 0; j < J; ++j) {
+                const int k = (j * L + part) * V;
+                float h[V];
+                cur.h[q][j].to(h);
 #pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const int k = (j * L + part) * V;
-                    h[q][j] = A[q][j] = Vec<float, V>::zero();
-                    if (ch < count && k < a.S) {
-                        h[q][j] = Vec<float, V>::load(a.state + (n * a.D + d0 + ch) * a.S + k);
-                        A[q][j] = Vec<float, V>::load(a.A + (int64_t)(d0 + ch) * a.S + k);
-                    }
+                for (int i = 0; i < V; ++i) {
+                    h[i] = fmaf(ex2(sc * A[q][j][i]), h[i], uc * cur.B[j][i]);
+                    y = fmaf(cur.C[j][i], h[i], y);
                 }
+                if (ch < count && k < a.S)
+                    Vec<float, V>::from(h).store(a.next + (n * a.D + d0 + ch) * a.S + k);
             }
 #pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                const int ch = (r0 + q) * R + lane / L;
-                const float sc = __shfl_sync(0xffffffffu, s, ch);
-                const float uc = sc * __shfl_sync(0xffffffffu, x, ch);
-                float y = 0.f;
-#pragma unroll
-                for (int j = 0; j < J; ++j) {
-                    const int k = (j * L + part) * V;
-                    float hv[V], av[V];
-                    h[q][j].to(hv);
-                    A[q][j].to(av);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        hv[i] = fmaf(ex2(sc * (kLog2e * av[i])), hv[i], uc * B[j][i]);
-                        y = fmaf(C[j][i], hv[i], y);
-                    }
-                    if (ch < count && k < a.S)
-                        Vec<float, V>::from(hv).store(a.next + (n * a.D + d0 + ch) * a.S + k);
-                }
-#pragma unroll
-                for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-                // Channel ch's sum goes to lane ch.
-                const float back = __shfl_sync(0xffffffffu, y, (lane % R) * L);
-                if (lane / R == r0 + q) mine = back;
-            }
+            for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+            // Channel ch's sum goes to lane ch.
+            const float back = __shfl_sync(0xffffffffu, y, (lane % R) * L);
+            if (lane / R == q) sum = back;
         }
-        mine = fmaf(skip, x, mine);
-        if (a.z) mine *= silu(z);
-        if (lane < count) a.out[n * a.os + dl] = from_f32<T>(mine);
+        sum = fmaf(skip, cur.x, sum);
+        if (a.z) sum *= silu(cur.z);
+        if (lane < count) a.out[n * a.os + dl] = from_f32<T>(sum);
+        cur = ahead;
     }
 }
 
@@ -690,12 +694,21 @@ gdn_status scan_typed(const gdn_ssm_problem &p, const void *x, const void *dt, c
 }
 
 template <typename T, int V, int L, int J>
-void run_scan_step(const ScanStepArgs<T> &a, cudaStream_t stream) {
-    const int64_t blocks = (int64_t)a.tiles * (a.D / a.per_group);
-    const int64_t rows = (a.N + kStepThreads / 32 - 1) / (kStepThreads / 32);
+void run_scan_step(ScanStepArgs<T> &a, cudaStream_t stream) {
+    constexpr int W = StepTile<T, V, L, J>::kChannelsPerWarp;
+    a.tiles = (a.per_group + W - 1) / W;
+    const int64_t tiles = (int64_t)a.tiles * (a.D / a.per_group);
+    auto rows = [&](int run) {
+        const int per = run * (kStepThreads / 32);
+        return ((int64_t)a.N + per - 1) / per;
+    };
+    // Up to four sequences per warp, while two waves of five blocks per SM
+    // are left.
+    a.run = 4;
+    while (a.run > 1 && tiles * rows(a.run) < 10 * kGridSms) a.run /= 2;
+    while (rows(a.run) > 65535) a.run *= 2;
     gdn_scan_step_kernel<T, V, L, J>
-        <<<dim3((unsigned)blocks, (unsigned)(rows < 65535 ? rows : 65535)), kStepThreads, 0,
-           stream>>>(a);
+        <<<dim3((unsigned)tiles, (unsigned)rows(a.run)), kStepThreads, 0, stream>>>(a);
 }
 
 template <typename T>
@@ -726,7 +739,6 @@ gdn_status scan_step_typed(const gdn_ssm_problem &p, const void *x, const void *
     a.zs = p.z_stride;
     a.os = p.out_stride;
     a.softplus = p.dt_softplus != 0;
-    a.tiles = (a.per_group + 31) / 32;
     const bool wide = p.state_dim % 4 == 0 && aligned16(state) && aligned16(next) && aligned16(A);
     a.bc_words = ((reinterpret_cast<uintptr_t>(B) | reinterpret_cast<uintptr_t>(C) |
                    (uint64_t)p.b_stride * sizeof(T) | (uint64_t)p.c_stride * sizeof(T)) %

@@ -11,15 +11,15 @@
 // A thread takes one 16-byte word of channels (one element where the rows are
 // not 16-byte aligned) through a run of consecutive tokens.  The last K - 1
 // inputs stay in registers, so only a run's start reads rows again (K - 1
-// rows per run, from L2).  Sequences that end inside a block of tokens take
-// the general path, which gathers every tap from the tokens or the state.
+// rows per run, from L2).  The next block of tokens is loaded before the one at
+// hand is computed.  Channels go in pairs through the packed fp32 instructions.
 #include "block.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kStep = 8;  // tokens loaded at once
+constexpr int kStep = 4;  // tokens loaded at once, one block of them ahead
 
 template <typename T> struct ConvArgs {
     const T *x;
@@ -58,6 +58,16 @@ __device__ __forceinline__ Vec<T, V> tap(const ConvArgs<T> &a, int n, int start,
     return Vec<T, V>::load(a.init + ((int64_t)n * (K - 1) + r) * a.C + c);
 }
 
+// A word's elements as pairs (an element alone: with a zero).
+template <typename T, int V, int P>
+__device__ __forceinline__ void pairs(const Vec<T, V> &x, uint64_t (&p)[P]) {
+    float r[2 * P];
+    r[2 * P - 1] = 0.f;
+    x.to(r);
+#pragma unroll
+    for (int i = 0; i < P; ++i) p[i] = pack2f(r[2 * i], r[2 * i + 1]);
+}
+
 // The states after the sequences' last tokens.  One thread per sequence and
 // word of channels reads all K - 1 rows before it writes the first, so that
 // the new state may replace the old one.
@@ -77,6 +87,7 @@ __device__ __forceinline__ void write_state(const ConvArgs<T> &a, int64_t i) {
 
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(kThreads) gdn_short_conv_kernel(const ConvArgs<T> a) {
+    constexpr int P = (V + 1) / 2;  // pairs of channels
     extern __shared__ float sw[];
     const int blk = blockIdx.x + a.first;
     if (blk >= a.n_main) {
@@ -90,72 +101,77 @@ __global__ void __launch_bounds__(kThreads) gdn_short_conv_kernel(const ConvArgs
     if (c >= a.C || first >= a.T_) return;
     const int t1 = (int)min(first + a.run, (int64_t)a.T_);
 
-    float w[K][V], b[V];
+    uint64_t w[K][P], b[P];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int i = 0; i < P; ++i) {
 #pragma unroll
-        for (int j = 0; j < K; ++j) w[j][v] = sw[j * a.tx * V + tx * V + v];
-        b[v] = a.bias ? a.bias[c + v] : 0.f;
+        for (int j = 0; j < K; ++j) {
+            const float *wj = sw + j * a.tx * V + tx * V;
+            w[j][i] = pack2f(wj[2 * i], V > 1 ? wj[2 * i + 1] : 0.f);
+        }
+        b[i] = a.bias ? pack2f(a.bias[c + 2 * i], V > 1 ? a.bias[c + 2 * i + 1] : 0.f) : 0;
     }
+    // One token's result from the K inputs up to it.
+    auto finish = [&](const uint64_t (&in)[K][P], T *to) {
+        float y[2 * P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            uint64_t sum = b[i];
+#pragma unroll
+            for (int j = 0; j < K; ++j) sum = ffma2(w[j][i], in[j][i], sum);
+            if (a.act) sum = silu2(sum);
+            const float2 v = unpack2f(sum);
+            y[2 * i] = v.x;
+            y[2 * i + 1] = v.y;
+        }
+        Vec<T, V>::from(y).store(to);
+    };
     Span s = locate(a.cu, a.N, a.T_, (int)first);
-    float in[K][V];  // the K - 1 inputs before a token, and the token's
-    bool have = false;
-    for (int t = (int)first; t < t1; t += kStep) {
-        if (t >= s.end) {
-            s = next_span(a.cu, a.N, a.T_, s);
-            have = false;
+    uint64_t in[K][P];  // the K - 1 inputs before a token, and the token's
+    int t = (int)first;
+    while (t < t1) {
+        if (t >= s.end) s = next_span(a.cu, a.N, a.T_, s);
+        const int e = min(s.end, t1);
+        // The K - 1 inputs before token t, then token by token.
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) pairs(tap<T, V, K>(a, s.n, s.start, t - (K - 1) + j, c), in[j]);
+        const T *from = a.x + t * a.xs + c;
+        T *to = a.out + t * a.os + c;
+        Vec<T, V> word[kStep];
+        auto fetch = [&](Vec<T, V> (&into)[kStep]) {
+#pragma unroll
+            for (int u = 0; u < kStep; ++u, from += a.xs) into[u] = Vec<T, V>::load(from);
+        };
+        auto step = [&](const Vec<T, V> &x) {
+            pairs(x, in[K - 1]);
+            finish(in, to);
+            to += a.os;
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+                for (int i = 0; i < P; ++i) in[j][i] = in[j + 1][i];
+        };
+        if (t + kStep <= e) {
+            fetch(word);
+            for (; t + kStep <= e; t += kStep) {
+                Vec<T, V> next[kStep];
+                const bool more = t + 2 * kStep <= e;
+                if (more) fetch(next);
+#pragma unroll
+                for (int u = 0; u < kStep; ++u) step(word[u]);
+                if (more)
+#pragma unroll
+                    for (int u = 0; u < kStep; ++u) word[u] = next[u];
+            }
         }
-        if (t + kStep <= min(s.end, t1)) {
-            Vec<T, V> word[kStep];
-            const T *from = a.x + t * a.xs + c;
+        // Fewer than a block are left: loaded together as well.
 #pragma unroll
-            for (int u = 0; u < kStep; ++u, from += a.xs) word[u] = Vec<T, V>::load(from);
-            if (!have) {
+        for (int u = 0; u < kStep - 1; ++u)
+            if (t + u < e) word[u] = Vec<T, V>::load(from + u * a.xs);
 #pragma unroll
-                for (int j = 0; j < K - 1; ++j)
-                    tap<T, V, K>(a, s.n, s.start, t - (K - 1) + j, c).to(in[j]);
-                have = true;
-            }
-            T *to = a.out + t * a.os + c;
-#pragma unroll
-            for (int u = 0; u < kStep; ++u, to += a.os) {
-                word[u].to(in[K - 1]);
-                float y[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    y[v] = b[v];
-#pragma unroll
-                    for (int j = 0; j < K; ++j) y[v] = fmaf(w[j][v], in[j][v], y[v]);
-#pragma unroll
-                    for (int j = 0; j < K - 1; ++j) in[j][v] = in[j + 1][v];
-                }
-                if (a.act)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) y[v] = silu(y[v]);
-                Vec<T, V>::from(y).store(to);
-            }
-        } else {
-            const int te = min(t + kStep, t1);
-#pragma unroll 1
-            for (int tok = t; tok < te; ++tok) {
-                if (tok >= s.end) s = next_span(a.cu, a.N, a.T_, s);
-                float y[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) y[v] = b[v];
-#pragma unroll
-                for (int j = 0; j < K; ++j) {
-                    float r[V];
-                    tap<T, V, K>(a, s.n, s.start, tok - (K - 1) + j, c).to(r);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) y[v] = fmaf(w[j][v], r[v], y[v]);
-                }
-                if (a.act)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) y[v] = silu(y[v]);
-                Vec<T, V>::from(y).store(a.out + tok * a.os + c);
-            }
-            have = false;
-        }
+        for (int u = 0; u < kStep - 1; ++u)
+            if (t + u < e) step(word[u]);
+        t = e;
     }
 }
 
