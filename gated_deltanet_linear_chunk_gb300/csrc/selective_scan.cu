@@ -12,11 +12,12 @@
 // 8 / S bytes of bf16 x, dt, z and out.  At S = 16 the arithmetic takes
 // longer than the memory traffic.
 //
-// A thread holds CH channels with all their states in registers and walks the
-// tokens in order, so the sums over the states need no exchange between
-// lanes.  States go in pairs through the packed fp32 instructions.  B and C,
-// the same for all channels of a group, are staged in shared memory as fp32;
-// x, dt and z arrive there by 16-byte asynchronous copies one tile ahead.
+// A thread walks the tokens in order with CH channels and all their states in
+// registers, so the sums over the states need no exchange between lanes, and
+// each B and C read from shared memory serves CH channels.  States go in
+// pairs through the packed fp32 instructions.  B and C, the same for all
+// channels of a group, are staged in shared memory as fp32; x, dt, z and the
+// raw B and C arrive by asynchronous copies one tile of tokens ahead.
 //
 // D channels fill few threads, so the packed tokens are cut into W windows of
 // equal length, whatever sequences they hold:
@@ -34,14 +35,25 @@
 #include <initializer_list>
 
 #include "block.cuh"
+#include "sm103.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kTile = 16;        // tokens per shared-memory tile
 constexpr int kMaxThreads = 128;
-constexpr int kUnroll = 4;       // tokens in flight per thread
+constexpr int kUnroll = 4;      // tokens in flight per thread
+
+// NS: the states padded to a power of two (A = B = 0 beyond S: those states
+// stay zero).  Channels per thread: states and decay rates take half of 128
+// registers up to NS = 16, of 255 above.  (At NS = 16, 4000 x 6144: two
+// channels in four blocks per SM 137 us for the output pass, four channels in
+// two blocks 143, one channel in six blocks 176: B and C are read twice as
+// often.)
+template <int NS> constexpr int kChannels = NS <= 8 ? 4 : NS <= 32 ? 2 : 1;
+template <int NS> constexpr int kResident = NS <= 16 ? 4 : 2;  // blocks of kMaxThreads per SM
+// Tokens per shared-memory tile: two tiles of four blocks fit an SM.
+template <typename T, int CH> constexpr int kTile = 64 / ((int)sizeof(T) * CH) < 16 ? 64 / ((int)sizeof(T) * CH) : 16;
 
 template <typename T> struct ScanArgs {
     const T *x, *dt, *B, *C, *z;
@@ -58,7 +70,7 @@ template <typename T> struct ScanArgs {
     int64_t xs, dts, bs, cs, zs, os;
     int in_word, bc_word;  // CopyWord of x, dt, z and of B, C
     bool softplus, defer;
-    bool pairs;        // out's rows are aligned to two elements
+    bool out_own;      // out's rows are aligned to a thread's channels
     bool state_words;  // A, the states and the workspace allow 16-byte words
 };
 
@@ -69,25 +81,37 @@ template <int BYTES> __device__ __forceinline__ void copy_async(void *smem, cons
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(gmem) : "memory");
 }
+// The first `bytes` (2 or 4) of a 4-byte word; the rest of it becomes zero.
+__device__ __forceinline__ void copy_async_part(void *smem, const void *gmem, int bytes) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(gmem), "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
 }
 
-// Channels per thread: two while their states and decay rates fit half the
-// registers that a thread may have, so that each B and C read from shared
-// memory serves two channels.
-template <int NS> constexpr int kChannels = NS <= 16 ? 2 : 1;
-
-// NS: the states padded to a power of two (A = B = 0 beyond S: those states
-// stay zero).
+// A thread's channels and all their states.
 template <typename T, int NS> struct ScanThread {
     static constexpr int CH = kChannels<NS>;
     static constexpr int NP = NS / 2;
     uint64_t A[CH][NP], h[CH][NP];
     float bias[CH], skip[CH], sum[CH];
-    int d;      // first channel
-    int valid;  // channels of this thread that exist
+    int d, col;  // first channel: in the tensors, in the block
+    int valid;   // channels that exist
 
+    __device__ __forceinline__ void setup(const ScanArgs<T> &a, int group, int in_group0) {
+        col = threadIdx.x * CH;
+        d = group * a.per_group + in_group0 + col;
+        valid = min(max(a.per_group - in_group0 - col, 0), CH);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            bias[c] = c < valid && a.bias ? a.bias[d + c] : 0.f;
+            skip[c] = c < valid && a.skip ? a.skip[d + c] : 0.f;
+            sum[c] = 0.f;
+        }
+        read(a, a.A, 0, kLog2e, A);
+    }
     // This thread's part of row `row` of a [rows, D, S] array (zeros where it
     // has none), in 16-byte words where the array allows.
     __device__ __forceinline__ void read(const ScanArgs<T> &a, const float *from, int64_t row,
@@ -95,32 +119,20 @@ template <typename T, int NS> struct ScanThread {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const float *p0 = from + (row * a.D + d + c) * a.S;
-            const bool ok = from && c < valid;
 #pragma unroll
-            for (int q = 0; q < NP / 2; ++q) {
+            for (int k = 0; k < NS; k += 4) {
                 float v[4] = {0.f, 0.f, 0.f, 0.f};
                 if (a.state_words) {
-                    if (ok && 4 * q < a.S) Vec<float, 4>::load(p0 + 4 * q).to(v);
+                    if (from && c < valid && k < a.S) Vec<float, 4>::load(p0 + k).to(v);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (ok && 4 * q + i < a.S) v[i] = p0[4 * q + i];
+                        if (from && c < valid && k + i < a.S) v[i] = p0[k + i];
                 }
-                to[c][2 * q] = pack2f(scale * v[0], scale * v[1]);
-                to[c][2 * q + 1] = pack2f(scale * v[2], scale * v[3]);
+                to[c][k / 2] = pack2f(scale * v[0], scale * v[1]);
+                to[c][k / 2 + 1] = pack2f(scale * v[2], scale * v[3]);
             }
         }
-    }
-    __device__ __forceinline__ void setup(const ScanArgs<T> &a, int group, int in_group) {
-        d = group * a.per_group + in_group;
-        valid = min(max(a.per_group - in_group, 0), CH);
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const bool ok = c < valid;
-            bias[c] = ok && a.bias ? a.bias[d + c] : 0.f;
-            skip[c] = ok && a.skip ? a.skip[d + c] : 0.f;
-        }
-        read(a, a.A, 0, kLog2e, A);
     }
     __device__ __forceinline__ void load(const ScanArgs<T> &a, const float *from, int64_t row) {
         read(a, from, row, 1.f, h);
@@ -131,20 +143,20 @@ template <typename T, int NS> struct ScanThread {
             float *p0 = to + (row * a.D + d + c) * a.S;
             if (c >= valid) continue;
 #pragma unroll
-            for (int q = 0; q < NP / 2; ++q) {
-                const float2 u = unpack2f(h[c][2 * q]), w = unpack2f(h[c][2 * q + 1]);
+            for (int k = 0; k < NS; k += 4) {
+                const float2 u = unpack2f(h[c][k / 2]), w = unpack2f(h[c][k / 2 + 1]);
                 const float v[4] = {u.x, u.y, w.x, w.y};
                 if (a.state_words) {
-                    if (4 * q < a.S) Vec<float, 4>::from(v).store(p0 + 4 * q);
+                    if (k < a.S) Vec<float, 4>::from(v).store(p0 + k);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (4 * q + i < a.S) p0[4 * q + i] = v[i];
+                        if (k + i < a.S) p0[k + i] = v[i];
                 }
             }
         }
     }
-    // One token: xv, dv of each channel, B and C of the group; y = C . h.
+    // One token: xv, dv of the channels, B and C of the group; y = C . h.
     template <bool OUT>
     __device__ __forceinline__ void token(bool softplus_on, const float *xv, const float *dv,
                                           const float *sB, const float *sC, float *y) {
@@ -159,16 +171,16 @@ template <typename T, int NS> struct ScanThread {
             y2[c] = 0;
         }
 #pragma unroll
-        for (int q = 0; q < NP / 2; ++q) {
-            const ulonglong2 b4 = reinterpret_cast<const ulonglong2 *>(sB)[q];
+        for (int k = 0; k < NS; k += 4) {
+            const ulonglong2 b4 = *reinterpret_cast<const ulonglong2 *>(sB + k);
             ulonglong2 c4 = {0, 0};
-            if (OUT) c4 = reinterpret_cast<const ulonglong2 *>(sC)[q];
+            if (OUT) c4 = *reinterpret_cast<const ulonglong2 *>(sC + k);
             const uint64_t b[2] = {b4.x, b4.y}, cc[2] = {c4.x, c4.y};
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
-                    const int p = 2 * q + i;
+                    const int p = k / 2 + i;
                     const float2 e = unpack2f(fmul2(s2[c], A[c][p]));
                     h[c][p] = ffma2(pack2f(ex2(e.x), ex2(e.y)), h[c][p], fmul2(u2[c], b[i]));
                     if (OUT) y2[c] = ffma2(cc[i], h[c][p], y2[c]);
@@ -192,101 +204,191 @@ enum CopyWord : int { kCopy16 = 16, kCopy4 = 4, kCopyElement = 0 };
 template <typename T>
 __device__ __forceinline__ void copy_rows(T *dst, int pitch, const T *src, int64_t stride,
                                           int rows, int cols, int word) {
-    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
-    const int step = word == kCopy16 ? kWide<T> : word == kCopy4 ? 4 / (int)sizeof(T) : 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    if (word == kCopyElement) {
+        // Four rows' loads before the first store.
+        for (int c = lane; c < cols; c += 32)
+            for (int r0 = warp; r0 < rows; r0 += 4 * warps) {
+                T v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (r0 + k * warps < rows) v[k] = src[(r0 + k * warps) * stride + c];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (r0 + k * warps < rows) dst[(r0 + k * warps) * pitch + c] = v[k];
+            }
+        return;
+    }
+    const int step = word == kCopy16 ? kWide<T> : 4 / (int)sizeof(T);
     for (int c = lane * step; c < cols; c += 32 * step) {
-        int r = threadIdx.x / 32;
+        int r = warp;
         const T *from = src + r * stride + c;
         T *to = dst + r * pitch + c;
         const int64_t next = warps * stride;
 #pragma unroll 4
         for (; r < rows; r += warps, from += next, to += warps * pitch) {
             if (word == kCopy16) copy_async<16>(to, from);
-            else if (word == kCopy4) copy_async<4>(to, from);
-            else *to = *from;
+            else copy_async<4>(to, from);
         }
+    }
+}
+
+// Whether element p lies in the upper half of its 4-byte word.
+template <typename T> __device__ __forceinline__ int odd(const T *p) {
+    return (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & 1;
+}
+
+// The same for 16-bit rows that may start at odd elements: element c of a
+// row goes to place c + odd(row), so that both sides of the copies are whole
+// 4-byte words.  A row's first element, where odd, is left to copy_first.
+template <typename T>
+__device__ __forceinline__ void copy_rows_odd(T *dst, int pitch, const T *src, int64_t stride,
+                                              int rows, int cols) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    for (int r = threadIdx.x / 32; r < rows; r += warps) {
+        const T *from = src + r * stride;
+        const int o = odd(from);
+        T *to = dst + r * pitch + o;
+        for (int c = o + 2 * lane; c < cols; c += 64)
+            copy_async_part(to + c, from + c, c + 1 < cols ? 4 : 2);
+    }
+}
+template <typename T, int K>
+__device__ __forceinline__ void copy_first(T *const (&dst)[K], int pitch, const T *const (&src)[K],
+                                           const int64_t (&stride)[K], int rows) {
+    for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+        T v[K];
+        bool is[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            is[k] = src[k] && odd(src[k] + r * stride[k]);
+            if (is[k]) v[k] = src[k][r * stride[k]];
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (is[k]) dst[k][r * pitch + 1] = v[k];
     }
 }
 
 // Shared memory of a block: two tiles of x, dt (and z), two of B (and C) as
 // they lie in global memory, and one of B (and C) as fp32, zero past the last
-// state.
-template <typename T, int NS, bool OUT> struct ScanTiles {
+// state.  ODD: rows of x, dt and z may start at odd 16-bit elements.
+template <typename T, int NS, bool OUT, bool ODD> struct ScanTiles {
     static constexpr int CH = kChannels<NS>;
+    static constexpr int TILE = kTile<T, CH>;
     static constexpr int kIn = OUT ? 3 : 2, kBC = OUT ? 2 : 1;
     float *bc;     // [B, C][token][state]
     T *raw[2];     // the same, as loaded
     T *in[2];      // [x, dt, z][token][channel]
     int width;     // channels per block
+    int pitch;     // elements between rows of `in`
     __device__ ScanTiles(char *smem, int threads) : width(threads * CH) {
+        pitch = width + (ODD ? 2 : 0);
         bc = reinterpret_cast<float *>(smem);
-        raw[0] = reinterpret_cast<T *>(bc + kBC * kTile * NS);
-        raw[1] = raw[0] + kBC * kTile * NS;
-        in[0] = raw[1] + kBC * kTile * NS;
-        in[1] = in[0] + kIn * kTile * width;
+        raw[0] = reinterpret_cast<T *>(bc + kBC * TILE * NS);
+        raw[1] = raw[0] + kBC * TILE * NS;
+        in[0] = raw[1] + kBC * TILE * NS;
+        in[1] = in[0] + kIn * TILE * pitch;
     }
     static size_t bytes(int threads) {
-        return kBC * kTile * NS * (sizeof(float) + 2 * sizeof(T)) +
-               2 * kIn * kTile * threads * CH * sizeof(T);
+        return kBC * TILE * NS * (sizeof(float) + 2 * sizeof(T)) +
+               2 * kIn * TILE * (threads * CH + (ODD ? 2 : 0)) * sizeof(T);
     }
     // Starts the copies of tokens [t, te) (one tile at most) of the block's
     // channels, d the first of `cols`.
     __device__ __forceinline__ void load(const ScanArgs<T> &a, int buf, int t, int te, int d,
                                          int cols, int group) const {
-        const int rows = min(te - t, kTile);
-        copy_rows(in[buf], width, a.x + t * a.xs + d, a.xs, rows, cols, a.in_word);
-        copy_rows(in[buf] + kTile * width, width, a.dt + t * a.dts + d, a.dts, rows, cols,
-                  a.in_word);
-        if (OUT && a.z)
-            copy_rows(in[buf] + 2 * kTile * width, width, a.z + t * a.zs + d, a.zs, rows, cols,
-                      a.in_word);
+        const int rows = min(te - t, TILE);
+        const T *const src[3] = {a.x + t * a.xs + d, a.dt + t * a.dts + d,
+                                 OUT && a.z ? a.z + t * a.zs + d : nullptr};
+        const int64_t stride[3] = {a.xs, a.dts, a.zs};
+        T *const dst[3] = {in[buf], in[buf] + TILE * pitch, in[buf] + 2 * TILE * pitch};
+#pragma unroll
+        for (int k = 0; k < kIn; ++k) {
+            if (k == 2 && !a.z) break;
+            if (ODD) copy_rows_odd(dst[k], pitch, src[k], stride[k], rows, cols);
+            else copy_rows(dst[k], pitch, src[k], stride[k], rows, cols, a.in_word);
+        }
         copy_rows(raw[buf], NS, a.B + t * a.bs + group * a.S, a.bs, rows, a.S, a.bc_word);
         if (OUT)
-            copy_rows(raw[buf] + kTile * NS, NS, a.C + t * a.cs + group * a.S, a.cs, rows, a.S,
+            copy_rows(raw[buf] + TILE * NS, NS, a.C + t * a.cs + group * a.S, a.cs, rows, a.S,
                       a.bc_word);
+        if (ODD) copy_first(dst, pitch, src, stride, rows);
     }
     // B and C of the tile that has arrived, to fp32.
     __device__ __forceinline__ void widen(const ScanArgs<T> &a, int buf) const {
-        for (int i = threadIdx.x; i < kBC * kTile * NS; i += blockDim.x)
+        for (int i = threadIdx.x; i < kBC * TILE * NS; i += blockDim.x)
             bc[i] = i % NS < a.S ? to_f32(raw[buf][i]) : 0.f;
     }
 };
 
-// Tokens [t, e) of tile `buf`, whose first token is t0.
-template <typename T, int NS, bool OUT, int U>
+// CH elements of shared memory, aligned to CH.
+template <int CH> __device__ __forceinline__ void load_own(const float *p, float *r) {
+    Vec<float, CH>::load(p).to(r);
+}
+template <int CH> __device__ __forceinline__ void load_own(const __nv_bfloat16 *p, float *r) {
+    if constexpr (CH == 4) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        Vec<__nv_bfloat16, 2>{w.x}.to(r);
+        Vec<__nv_bfloat16, 2>{w.y}.to(r + 2);
+    } else {
+        Vec<__nv_bfloat16, CH>::load(p).to(r);
+    }
+}
+// The same to global memory.
+template <int CH> __device__ __forceinline__ void store_own(float *p, const float *r) {
+    Vec<float, CH>::from(r).store(p);
+}
+template <int CH> __device__ __forceinline__ void store_own(__nv_bfloat16 *p, const float *r) {
+    if constexpr (CH == 4)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(Vec<__nv_bfloat16, 2>::from(r).w,
+                                                   Vec<__nv_bfloat16, 2>::from(r + 2).w);
+    else
+        Vec<__nv_bfloat16, CH>::from(r).store(p);
+}
+
+// U tokens from t of tile `buf`, whose first token is t0.  `odds`: whether
+// the tile's first rows of x, dt and z are odd, in bits 0 to 2, and whether
+// their strides are, in bits 4 to 6.
+template <typename T, int NS, bool OUT, bool ODD, int U>
 __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS> &th,
-                                         const ScanTiles<T, NS, OUT> &tl, int buf, int t0, int t) {
-    constexpr int CH = kChannels<NS>;
+                                         const ScanTiles<T, NS, OUT, ODD> &tl, int buf, int t0,
+                                         int t, int odds) {
+    constexpr int CH = kChannels<NS>, TILE = kTile<T, CH>;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int r = t - t0 + u;
-        const T *in = tl.in[buf] + r * tl.width + threadIdx.x * CH;
-        float xv[CH], dv[CH], y[CH];
+        const T *in = tl.in[buf] + r * tl.pitch + th.col;
+        const int o = ODD ? odds ^ ((odds >> 4) & -(r & 1)) : 0;
+        auto own = [&](int k, float *v) {
+            const T *p = in + k * TILE * tl.pitch;
+            if (ODD) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            xv[c] = to_f32(in[c]);
-            dv[c] = to_f32(in[kTile * tl.width + c]);
-        }
-        th.template token<OUT>(a.softplus, xv, dv, tl.bc + r * NS, tl.bc + (kTile + r) * NS, y);
+                for (int c = 0; c < CH; ++c) v[c] = to_f32(p[c + ((o >> k) & 1)]);
+            } else {
+                load_own<CH>(p, v);
+            }
+        };
+        float xv[CH], dv[CH], y[CH];
+        own(0, xv);
+        own(1, dv);
+        th.template token<OUT>(a.softplus, xv, dv, tl.bc + r * NS, tl.bc + (TILE + r) * NS, y);
         if (OUT) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                y[c] = fmaf(th.skip[c], xv[c], y[c]);
-                if (a.z) y[c] *= silu(to_f32(in[2 * kTile * tl.width + c]));
+            for (int c = 0; c < CH; ++c) y[c] = fmaf(th.skip[c], xv[c], y[c]);
+            if (a.z) {
+                float zv[CH];
+                own(2, zv);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) y[c] *= silu(zv[c]);
             }
-            T *o = a.out + (t + u) * a.os + th.d;
-            if (CH == 2 && a.pairs) {
-                if (th.valid) {
-                    if constexpr (sizeof(T) == 2) {
-                        *reinterpret_cast<__nv_bfloat162 *>(o) = __floats2bfloat162_rn(y[0], y[CH - 1]);
-                    } else {
-                        *reinterpret_cast<float2 *>(o) = make_float2(y[0], y[CH - 1]);
-                    }
-                }
+            T *out = a.out + (t + u) * a.os + th.d;
+            if (!ODD && a.out_own) {
+                if (th.valid) store_own<CH>(out, y);
             } else {
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
-                    if (c < th.valid) o[c] = from_f32<T>(y[c]);
+                    if (c < th.valid) out[c] = from_f32<T>(y[c]);
             }
         }
     }
@@ -304,20 +406,21 @@ __device__ void copy_empty(const ScanArgs<T> &a, int d0, int cols) {
     }
 }
 
-template <typename T, int NS, bool OUT>
-__global__ void __launch_bounds__(kMaxThreads, NS <= 16 ? 4 : 2) gdn_scan_kernel(const ScanArgs<T> a) {
+template <typename T, int NS, bool OUT, bool ODD>
+__global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(const ScanArgs<T> a) {
+    constexpr int CH = kChannels<NS>, TILE = kTile<T, CH>;
     extern __shared__ __align__(16) char smem[];
-    const ScanTiles<T, NS, OUT> tl(smem, blockDim.x);
+    const ScanTiles<T, NS, OUT, ODD> tl(smem, blockDim.x);
     const int group = blockIdx.x / a.tiles, in_group0 = (blockIdx.x % a.tiles) * tl.width;
     const int w = blockIdx.y, d0 = group * a.per_group + in_group0;
+    const int cols = min(tl.width, a.per_group - in_group0);
     if (OUT && w == a.W) {
-        copy_empty(a, d0, min(tl.width, a.per_group - in_group0));
+        copy_empty(a, d0, cols);
         return;
     }
     int t0 = w * a.len;
     const int t1 = min(t0 + a.len, a.T_);
     Span s;
-    ScanThread<T, NS> th;
     bool from_carry = false;
     if (OUT) {
         s = locate(a.cu, a.N, a.T_, t0);
@@ -329,28 +432,32 @@ __global__ void __launch_bounds__(kMaxThreads, NS <= 16 ? 4 : 2) gdn_scan_kernel
         from_carry = s.start < t0;
         t0 = max(t0, s.start);
     }
-    th.setup(a, group, in_group0 + threadIdx.x * th.CH);
+    tl.load(a, 0, t0, t1, d0, cols, group);
+    ScanThread<T, NS> th;
+    th.setup(a, group, in_group0);
+    if (OUT) ptx::griddep_wait();  // the carries: all above is input to the whole call
     if (from_carry) th.load(a, OUT ? a.carry : nullptr, w - 1);
     else th.load(a, a.init, s.n);
-#pragma unroll
-    for (int c = 0; c < th.CH; ++c) th.sum[c] = 0.f;
 
-    const int cols = min(tl.width, a.per_group - in_group0);
-    tl.load(a, 0, t0, t1, d0, cols, group);
     int buf = 0;
-    for (int tt = t0; tt < t1; tt += kTile, buf ^= 1) {
-        const int te = min(tt + kTile, t1);
+    for (int tt = t0; tt < t1; tt += TILE, buf ^= 1) {
+        const int te = min(tt + TILE, t1);
         copies_wait();
         __syncthreads();  // the tile has arrived, and the one before is done with
         tl.widen(a, buf);
         if (te < t1) tl.load(a, buf ^ 1, te, t1, d0, cols, group);
+        int odds = 0;
+        if (ODD)
+            odds = odd(a.x + tt * a.xs + d0) | odd(a.dt + tt * a.dts + d0) << 1 |
+                   odd(a.z + tt * a.zs + d0) << 2 | (int)(a.xs & 1) << 4 |
+                   (int)(a.dts & 1) << 5 | (int)(a.zs & 1) << 6;
         __syncthreads();
         int t = tt;
         while (t < te) {
             const int e = min(te, s.end);
             for (; t + kUnroll <= e; t += kUnroll)
-                scan_run<T, NS, OUT, kUnroll>(a, th, tl, buf, tt, t);
-            for (; t < e; ++t) scan_run<T, NS, OUT, 1>(a, th, tl, buf, tt, t);
+                scan_run<T, NS, OUT, ODD, kUnroll>(a, th, tl, buf, tt, t, odds);
+            for (; t < e; ++t) scan_run<T, NS, OUT, ODD, 1>(a, th, tl, buf, tt, t, odds);
             if (OUT && t == s.end) {
                 // A final state written over the initial one must wait for
                 // the windows that read it: it takes the place of the state
@@ -366,9 +473,10 @@ __global__ void __launch_bounds__(kMaxThreads, NS <= 16 ? 4 : 2) gdn_scan_kernel
         }
     }
     if (!OUT) {
+        ptx::griddep_launch_dependents();
         th.store(a, a.carry, w);
 #pragma unroll
-        for (int c = 0; c < th.CH; ++c)
+        for (int c = 0; c < CH; ++c)
             if (c < th.valid) a.steps[(int64_t)w * a.D + th.d + c] = th.sum[c];
     }
 }
@@ -376,34 +484,58 @@ __global__ void __launch_bounds__(kMaxThreads, NS <= 16 ? 4 : 2) gdn_scan_kernel
 constexpr int kCombineThreads = 256;
 
 // States entering the windows: in window order, c <- exp(A sum s) c + h, from
-// the window's own state alone where its last sequence starts inside it.
-template <typename T>
+// the window's own state alone where its last sequence starts inside it.  The
+// steps compose, (h, k) then (h', k') being (k' h + h', k k'), so a block cuts
+// many windows into SEG runs, walks all runs at once from zero, joins them in
+// shared memory and walks them again from the states that enter them.
+template <typename T, int SEG>
 __global__ void __launch_bounds__(kCombineThreads) gdn_scan_combine_kernel(const ScanArgs<T> a) {
+    constexpr int E = kCombineThreads / SEG;  // states per block
+    __shared__ float end[SEG][E], kept[SEG][E];
     extern __shared__ char inside[];  // [W - 1]
-    for (int w = threadIdx.x; w < a.W - 1; w += blockDim.x)
+    ptx::griddep_launch_dependents();
+    const int n = a.W - 1;
+    for (int w = threadIdx.x; w < n; w += blockDim.x)
         inside[w] = locate(a.cu, a.N, a.T_, (w + 1) * a.len - 1).start >= w * a.len;
-    __syncthreads();
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, ds = (int64_t)a.D * a.S;
-    if (i >= ds) return;
-    const float rate = kLog2e * a.A[i];
+    const int e = threadIdx.x % E, seg = threadIdx.x / E, run = (n + SEG - 1) / SEG;
+    const int64_t ds = (int64_t)a.D * a.S, i = (int64_t)blockIdx.x * E + e;
+    const bool ok = i < ds;
+    const float rate = ok ? kLog2e * a.A[i] : 0.f;
     const int d = (int)(i / a.S);
+    const int w0 = seg * run, w1 = min(w0 + run, n);
+    __syncthreads();
+    ptx::griddep_wait();
     constexpr int kAhead = 8;  // windows loaded at once: only the products are sequential
-    float c = 0.f;
-    for (int w0 = 0; w0 < a.W - 1; w0 += kAhead) {
-        float h[kAhead], kept[kAhead];
+    auto walk = [&](float c, bool write, float &steps, bool &fresh) {
+        for (int w = w0; w < w1; w += kAhead) {
+            float h[kAhead], s[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int w = min(w0 + k, a.W - 2);
-            h[k] = a.carry[w * ds + i];
-            kept[k] = a.steps[(int64_t)w * a.D + d];
-        }
+            for (int k = 0; k < kAhead; ++k) {
+                const int at = min(w + k, w1 - 1);
+                h[k] = ok ? a.carry[at * ds + i] : 0.f;
+                s[k] = ok ? a.steps[(int64_t)at * a.D + d] : 0.f;
+            }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (w0 + k >= a.W - 1) break;
-            c = inside[w0 + k] ? h[k] : fmaf(ex2(rate * kept[k]), c, h[k]);
-            a.carry[(w0 + k) * ds + i] = c;
+            for (int k = 0; k < kAhead; ++k) {
+                if (w + k >= w1) break;
+                if (inside[w + k]) fresh = true;
+                steps += s[k];
+                c = inside[w + k] ? h[k] : fmaf(ex2(rate * s[k]), c, h[k]);
+                if (write && ok) a.carry[(w + k) * ds + i] = c;
+            }
         }
+        return c;
+    };
+    float steps = 0.f, c = 0.f;
+    bool fresh = false;  // a sequence starts in this run: nothing enters past it
+    if (SEG > 1) {
+        end[seg][e] = walk(0.f, false, steps, fresh);
+        kept[seg][e] = fresh ? -1.f : ex2(rate * steps);
+        __syncthreads();
+        for (int k = 0; k < seg; ++k)
+            c = kept[k][e] < 0.f ? end[k][e] : fmaf(kept[k][e], c, end[k][e]);
     }
+    walk(c, true, steps, fresh);
 }
 
 // In place: the final states that gdn_scan_kernel left in the carries.
@@ -561,25 +693,23 @@ struct ScanPlan {
     int ns, threads, tiles, W, len;
 };
 
-// The shortest window: below it the carries' launches cost more than the
-// windows' parallel run saves.
-constexpr int kMinWindow = 64;
+// The shortest window.
+constexpr int kMinWindow = 16;
 
 ScanPlan scan_plan(const gdn_ssm_problem &p) {
     ScanPlan s;
     s.ns = 4;
     while (s.ns < p.state_dim) s.ns *= 2;
-    const int ch = s.ns <= 16 ? 2 : 1;
+    const int ch = s.ns <= 8 ? 4 : s.ns <= 32 ? 2 : 1, resident = s.ns <= 16 ? 4 : 2;
     const int per_group = p.channels / p.num_groups;
-    const int warps = (per_group + 32 * ch - 1) / (32 * ch);
-    s.threads = 32 * (warps < kMaxThreads / 32 ? warps : kMaxThreads / 32);
+    const int warps = (per_group + 32 * ch - 1) / (32 * ch), most = kMaxThreads / 32;
+    s.threads = 32 * (warps < most ? warps : most);
     s.tiles = (per_group + s.threads * ch - 1) / (s.threads * ch);
+    // One wave of blocks.
     const int64_t blocks = (int64_t)p.num_groups * s.tiles;
-    // Four blocks of 128 threads per SM.
-    const int64_t room = (int64_t)4 * kGridSms * (kMaxThreads / s.threads);
-    int64_t W = room / (blocks > 0 ? blocks : 1);
-    const int64_t most = p.total_tokens / kMinWindow;
-    W = W < most ? W : most;
+    int64_t W = (int64_t)resident * kGridSms * (kMaxThreads / s.threads) / blocks;
+    const int64_t short_enough = p.total_tokens / kMinWindow;
+    W = W < short_enough ? W : short_enough;
     W = W < 1 ? 1 : W;
     const int64_t len = (p.total_tokens + W - 1) / W;
     s.len = (int)(len > 0 ? len : 1);
@@ -612,40 +742,72 @@ template <typename T> ScanArgs<T> scan_args(const gdn_ssm_problem &p, const Scan
 
 // Blocks of full size need more shared memory than a kernel has by default;
 // the limit is raised once per device and variant.
-template <typename T, int NS> bool scan_shared_memory() {
+template <typename T, int NS, bool ODD> bool scan_shared_memory() {
     static std::atomic<bool> done[kMaxDevices];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
     if (done[dev].load(std::memory_order_acquire)) return true;
     const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    if (cudaFuncSetAttribute(gdn_scan_kernel<T, NS, true>, attr,
-                             (int)ScanTiles<T, NS, true>::bytes(kMaxThreads)) != cudaSuccess ||
-        cudaFuncSetAttribute(gdn_scan_kernel<T, NS, false>, attr,
-                             (int)ScanTiles<T, NS, false>::bytes(kMaxThreads)) != cudaSuccess)
+    if (cudaFuncSetAttribute(gdn_scan_kernel<T, NS, true, ODD>, attr,
+                             (int)ScanTiles<T, NS, true, ODD>::bytes(kMaxThreads)) != cudaSuccess ||
+        cudaFuncSetAttribute(gdn_scan_kernel<T, NS, false, ODD>, attr,
+                             (int)ScanTiles<T, NS, false, ODD>::bytes(kMaxThreads)) != cudaSuccess)
         return false;
     done[dev].store(true, std::memory_order_release);
     return true;
 }
 
-template <typename T, int NS>
+template <typename T, int NS, bool ODD>
 gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cudaStream_t stream) {
     const unsigned blocks = (unsigned)(a.G * pl.tiles);
     const int64_t ds = (int64_t)a.D * a.S;
-    const unsigned each = (unsigned)((ds + kCombineThreads - 1) / kCombineThreads);
-    const size_t in_bytes = ScanTiles<T, NS, false>::bytes(pl.threads);
-    const size_t out_bytes = ScanTiles<T, NS, true>::bytes(pl.threads);
-    if (!scan_shared_memory<T, NS>()) return GDN_ERR_CUDA;
+    const size_t in_bytes = ScanTiles<T, NS, false, ODD>::bytes(pl.threads);
+    const size_t out_bytes = ScanTiles<T, NS, true, ODD>::bytes(pl.threads);
+    if (!scan_shared_memory<T, NS, ODD>()) return GDN_ERR_CUDA;
+    // With several windows the second and third launch may start while the
+    // one before ends; they wait for it before they touch the carries.
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = pl.W > 1 ? 1 : 0;
     if (pl.W > 1) {
-        gdn_scan_kernel<T, NS, false>
+        gdn_scan_kernel<T, NS, false, ODD>
             <<<dim3(blocks, pl.W - 1), pl.threads, in_bytes, stream>>>(a);
-        gdn_scan_combine_kernel<T><<<each, kCombineThreads, pl.W - 1, stream>>>(a);
+        if (launch_status() != GDN_OK) return GDN_ERR_CUDA;
+        // Eight windows are loaded at once: more than a few rounds of them
+        // are cut into runs.
+        const bool runs = pl.W - 1 > 32;
+        const int64_t each = kCombineThreads / (runs ? 16 : 1);
+        cfg.gridDim = dim3((unsigned)((ds + each - 1) / each));
+        cfg.blockDim = dim3(kCombineThreads);
+        cfg.dynamicSmemBytes = pl.W - 1;
+        if (cudaLaunchKernelEx(&cfg, runs ? gdn_scan_combine_kernel<T, 16>
+                                          : gdn_scan_combine_kernel<T, 1>, a) != cudaSuccess)
+            return GDN_ERR_CUDA;
     }
     const unsigned rows = (unsigned)(pl.W + (empties ? 1 : 0));
-    if (rows > 0)
-        gdn_scan_kernel<T, NS, true><<<dim3(blocks, rows), pl.threads, out_bytes, stream>>>(a);
+    if (rows > 0) {
+        cfg.gridDim = dim3(blocks, rows);
+        cfg.blockDim = dim3(pl.threads);
+        cfg.dynamicSmemBytes = out_bytes;
+        if (cudaLaunchKernelEx(&cfg, gdn_scan_kernel<T, NS, true, ODD>, a) != cudaSuccess)
+            return GDN_ERR_CUDA;
+    }
     if (a.defer && pl.W > 1)
-        gdn_scan_deferred_kernel<T><<<dim3(each, pl.W - 1), kCombineThreads, 0, stream>>>(a);
+        gdn_scan_deferred_kernel<T>
+            <<<dim3((unsigned)((ds + kCombineThreads - 1) / kCombineThreads), pl.W - 1),
+               kCombineThreads, 0, stream>>>(a);
     return launch_status();
+}
+
+template <typename T, int NS>
+gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cudaStream_t stream) {
+    if constexpr (sizeof(T) == 2)
+        if (a.in_word == kCopyElement) return run_scan<T, NS, true>(pl, a, empties, stream);
+    return run_scan<T, NS, false>(pl, a, empties, stream);
 }
 
 template <typename T>
@@ -679,8 +841,9 @@ gdn_status scan_typed(const gdn_ssm_problem &p, const void *x, const void *dt, c
     a.in_word = word({x, dt, z}, {p.x_stride, p.dt_stride, z ? p.z_stride : 0, a.per_group});
     a.bc_word = word({B, C}, {p.b_stride, p.c_stride, p.state_dim});
     a.state_words = p.state_dim % 4 == 0 && aligned16(A) && aligned16(init) && aligned16(fin);
-    a.pairs = (reinterpret_cast<uintptr_t>(out) | (uint64_t)p.out_stride * sizeof(T)) %
-                      (2 * sizeof(T)) == 0 && a.per_group % 2 == 0;
+    const int ch = pl.ns <= 8 ? 4 : pl.ns <= 32 ? 2 : 1;
+    a.out_own = (reinterpret_cast<uintptr_t>(out) | (uint64_t)p.out_stride * sizeof(T)) %
+                        (ch * sizeof(T)) == 0 && a.per_group % ch == 0;
     // Only a batch of several sequences (or of no tokens) has empty ones.
     const bool empties = fin && fin != init && (p.num_seqs > 1 || p.total_tokens == 0);
     switch (pl.ns) {
