@@ -51,7 +51,7 @@ constexpr int kUnroll = 4;      // tokens in flight per thread
 // two blocks 143, one channel in six blocks 176: B and C are read twice as
 // often.)
 template <int NS> constexpr int kChannels = NS <= 8 ? 4 : NS <= 32 ? 2 : 1;
-template <int NS> constexpr int kResident = NS <= 16 ? 4 : 2;  // blocks of kMaxThreads per SM
+template <int NS> constexpr int kResident = NS <= 16 ? 3 : 2;  // blocks of kMaxThreads per SM
 // Tokens per shared-memory tile: two tiles of four blocks fit an SM.
 template <typename T, int CH> constexpr int kTile = 64 / ((int)sizeof(T) * CH) < 16 ? 64 / ((int)sizeof(T) * CH) : 16;
 
@@ -163,8 +163,9 @@ template <typename T, int NS> struct ScanThread {
         uint64_t s2[CH], u2[CH], y2[CH];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            float s = dv[c] + bias[c];
-            if (softplus_on) s = softplus(s);
+            // (A choice, not a branch: the tokens of a run are one basic block,
+            // which the compiler can interleave.)
+            const float v = dv[c] + bias[c], sp = softplus(v), s = softplus_on ? sp : v;
             if (!OUT) sum[c] += s;
             s2[c] = pack2f(s, s);
             u2[c] = pack2f(s * xv[c], s * xv[c]);
@@ -278,18 +279,20 @@ template <typename T, int NS, bool OUT, bool ODD> struct ScanTiles {
     static constexpr int TILE = kTile<T, CH>;
     static constexpr int kIn = OUT ? 3 : 2, kBC = OUT ? 2 : 1;
     float *bc;     // [B, C][token][state]
-    T *raw[2];     // the same, as loaded
-    T *in[2];      // [x, dt, z][token][channel]
+    T *raws;       // the same, as loaded, of two tiles
+    T *ins;        // [x, dt, z][token][channel], of two tiles
     int width;     // channels per block
-    int pitch;     // elements between rows of `in`
+    int pitch;     // elements between rows of `ins`
     __device__ ScanTiles(char *smem, int threads) : width(threads * CH) {
         pitch = width + (ODD ? 2 : 0);
         bc = reinterpret_cast<float *>(smem);
-        raw[0] = reinterpret_cast<T *>(bc + kBC * TILE * NS);
-        raw[1] = raw[0] + kBC * TILE * NS;
-        in[0] = raw[1] + kBC * TILE * NS;
-        in[1] = in[0] + kIn * TILE * pitch;
+        raws = reinterpret_cast<T *>(bc + kBC * TILE * NS);
+        ins = raws + 2 * kBC * TILE * NS;
     }
+    // Tile `buf` (an offset, not an array of pointers: those would lose the
+    // knowledge that they point to shared memory).
+    __device__ __forceinline__ T *raw(int buf) const { return raws + buf * (kBC * TILE * NS); }
+    __device__ __forceinline__ T *in(int buf) const { return ins + buf * (kIn * TILE * pitch); }
     static size_t bytes(int threads) {
         return kBC * TILE * NS * (sizeof(float) + 2 * sizeof(T)) +
                2 * kIn * TILE * (threads * CH + (ODD ? 2 : 0)) * sizeof(T);
@@ -302,23 +305,23 @@ template <typename T, int NS, bool OUT, bool ODD> struct ScanTiles {
         const T *const src[3] = {a.x + t * a.xs + d, a.dt + t * a.dts + d,
                                  OUT && a.z ? a.z + t * a.zs + d : nullptr};
         const int64_t stride[3] = {a.xs, a.dts, a.zs};
-        T *const dst[3] = {in[buf], in[buf] + TILE * pitch, in[buf] + 2 * TILE * pitch};
+        T *const dst[3] = {in(buf), in(buf) + TILE * pitch, in(buf) + 2 * TILE * pitch};
 #pragma unroll
         for (int k = 0; k < kIn; ++k) {
             if (k == 2 && !a.z) break;
             if (ODD) copy_rows_odd(dst[k], pitch, src[k], stride[k], rows, cols);
             else copy_rows(dst[k], pitch, src[k], stride[k], rows, cols, a.in_word);
         }
-        copy_rows(raw[buf], NS, a.B + t * a.bs + group * a.S, a.bs, rows, a.S, a.bc_word);
+        copy_rows(raw(buf), NS, a.B + t * a.bs + group * a.S, a.bs, rows, a.S, a.bc_word);
         if (OUT)
-            copy_rows(raw[buf] + TILE * NS, NS, a.C + t * a.cs + group * a.S, a.cs, rows, a.S,
+            copy_rows(raw(buf) + TILE * NS, NS, a.C + t * a.cs + group * a.S, a.cs, rows, a.S,
                       a.bc_word);
         if (ODD) copy_first(dst, pitch, src, stride, rows);
     }
     // B and C of the tile that has arrived, to fp32.
     __device__ __forceinline__ void widen(const ScanArgs<T> &a, int buf) const {
         for (int i = threadIdx.x; i < kBC * TILE * NS; i += blockDim.x)
-            bc[i] = i % NS < a.S ? to_f32(raw[buf][i]) : 0.f;
+            bc[i] = i % NS < a.S ? to_f32(raw(buf)[i]) : 0.f;
     }
 };
 
@@ -355,10 +358,11 @@ __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS>
                                          const ScanTiles<T, NS, OUT, ODD> &tl, int buf, int t0,
                                          int t, int odds) {
     constexpr int CH = kChannels<NS>, TILE = kTile<T, CH>;
+    float y[U][CH];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int r = t - t0 + u;
-        const T *in = tl.in[buf] + r * tl.pitch + th.col;
+        const T *in = tl.in(buf) + r * tl.pitch + th.col;
         const int o = ODD ? odds ^ ((odds >> 4) & -(r & 1)) : 0;
         auto own = [&](int k, float *v) {
             const T *p = in + k * TILE * tl.pitch;
@@ -369,28 +373,32 @@ __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS>
                 load_own<CH>(p, v);
             }
         };
-        float xv[CH], dv[CH], y[CH];
+        float xv[CH], dv[CH];
         own(0, xv);
         own(1, dv);
-        th.template token<OUT>(a.softplus, xv, dv, tl.bc + r * NS, tl.bc + (TILE + r) * NS, y);
+        th.template token<OUT>(a.softplus, xv, dv, tl.bc + r * NS, tl.bc + (TILE + r) * NS, y[u]);
         if (OUT) {
+            float zv[CH];
+            own(2, zv);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) y[c] = fmaf(th.skip[c], xv[c], y[c]);
-            if (a.z) {
-                float zv[CH];
-                own(2, zv);
-#pragma unroll
-                for (int c = 0; c < CH; ++c) y[c] *= silu(zv[c]);
-            }
-            T *out = a.out + (t + u) * a.os + th.d;
-            if (!ODD && a.out_own) {
-                if (th.valid) store_own<CH>(out, y);
-            } else {
-#pragma unroll
-                for (int c = 0; c < CH; ++c)
-                    if (c < th.valid) out[c] = from_f32<T>(y[c]);
+            for (int c = 0; c < CH; ++c) {
+                const float gate = silu(zv[c]);
+                y[u][c] = fmaf(th.skip[c], xv[c], y[u][c]) * (a.z ? gate : 1.f);
             }
         }
+    }
+    if (!OUT) return;
+    T *out = a.out + t * a.os + th.d;
+    if (!ODD && a.out_own) {
+#pragma unroll
+        for (int u = 0; u < U; ++u, out += a.os)
+            if (th.valid) store_own<CH>(out, y[u]);
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u, out += a.os)
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                if (c < th.valid) out[c] = from_f32<T>(y[u][c]);
     }
 }
 
@@ -700,7 +708,7 @@ ScanPlan scan_plan(const gdn_ssm_problem &p) {
     ScanPlan s;
     s.ns = 4;
     while (s.ns < p.state_dim) s.ns *= 2;
-    const int ch = s.ns <= 8 ? 4 : s.ns <= 32 ? 2 : 1, resident = s.ns <= 16 ? 4 : 2;
+    const int ch = s.ns <= 8 ? 4 : s.ns <= 32 ? 2 : 1, resident = s.ns <= 16 ? 3 : 2;
     const int per_group = p.channels / p.num_groups;
     const int warps = (per_group + 32 * ch - 1) / (32 * ch), most = kMaxThreads / 32;
     s.threads = 32 * (warps < most ? warps : most);
