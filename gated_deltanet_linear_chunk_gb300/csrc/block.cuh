@@ -168,6 +168,27 @@ template <typename T> inline bool rows_aligned16(const void *p, int64_t stride) 
     return !p || (aligned16(p) && (stride * (int64_t)sizeof(T)) % 16 == 0);
 }
 
+// ------------------------------------------------------- asynchronous copies
+// From global to shared memory, 4 or 16 bytes, both sides aligned to them.
+template <int BYTES> __device__ __forceinline__ void copy_async(void *smem, const void *gmem) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(gmem) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(gmem) : "memory");
+}
+// The first `bytes` (2 or 4) of a 4-byte word; the rest of it becomes zero.
+__device__ __forceinline__ void copy_async_part(void *smem, const void *gmem, int bytes) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(gmem), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N committed groups of this thread's copies are on their way.
+template <int N> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ---------------------------------------------------- packed sequences
 // Sequence n holds tokens [start, end).  Values read from cu_seqlens are
 // clamped so that start <= t < end <= T for the token t asked for, whatever

@@ -74,23 +74,6 @@ template <typename T> struct ScanArgs {
     bool state_words;  // A, the states and the workspace allow 16-byte words
 };
 
-template <int BYTES> __device__ __forceinline__ void copy_async(void *smem, const void *gmem) {
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(gmem) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(gmem) : "memory");
-}
-// The first `bytes` (2 or 4) of a 4-byte word; the rest of it becomes zero.
-__device__ __forceinline__ void copy_async_part(void *smem, const void *gmem, int bytes) {
-    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(gmem), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-}
-
 // A thread's channels and all their states.
 template <typename T, int NS> struct ScanThread {
     static constexpr int CH = kChannels<NS>;
@@ -450,7 +433,8 @@ __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(co
     int buf = 0;
     for (int tt = t0; tt < t1; tt += TILE, buf ^= 1) {
         const int te = min(tt + TILE, t1);
-        copies_wait();
+        copies_commit();
+        copies_wait<0>();
         __syncthreads();  // the tile has arrived, and the one before is done with
         tl.widen(a, buf);
         if (te < t1) tl.load(a, buf ^ 1, te, t1, d0, cols, group);

@@ -11,15 +11,18 @@
 // A thread takes one 16-byte word of channels (one element where the rows are
 // not 16-byte aligned) through a run of consecutive tokens.  The last K - 1
 // inputs stay in registers, so only a run's start reads rows again (K - 1
-// rows per run, from L2).  The next block of tokens is loaded before the one at
-// hand is computed.  Channels go in pairs through the packed fp32 instructions.
+// rows per run, from L2).  The run's rows come through a ring in shared memory
+// by asynchronous copies, 12 tokens ahead: 24 KB in flight per block without
+// a register.  Channels go in pairs through the packed fp32 instructions.
 #include "block.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kStep = 4;  // tokens loaded at once, one block of them ahead
+constexpr int kStep = 4;   // tokens per group of copies
+constexpr int kAhead = 3;  // groups in flight
+constexpr int kRing = (kAhead + 1) * kStep;
 
 template <typename T> struct ConvArgs {
     const T *x;
@@ -88,7 +91,7 @@ __device__ __forceinline__ void write_state(const ConvArgs<T> &a, int64_t i) {
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(kThreads) gdn_short_conv_kernel(const ConvArgs<T> a) {
     constexpr int P = (V + 1) / 2;  // pairs of channels
-    extern __shared__ float sw[];
+    extern __shared__ __align__(16) float sw[];
     const int blk = blockIdx.x + a.first;
     if (blk >= a.n_main) {
         write_state<T, V, K>(a, (int64_t)(blk - a.n_main) * kThreads + threadIdx.x);
@@ -96,11 +99,12 @@ __global__ void __launch_bounds__(kThreads) gdn_short_conv_kernel(const ConvArgs
     }
     const int tx = threadIdx.x & (a.tx - 1), ty = threadIdx.x / a.tx;
     const int c0 = (blk % a.n_chan) * a.tx * V, c = c0 + tx * V;
-    stage_weights<K>(sw, a.weight, c0, a.C, a.tx * V);
     const int64_t first = ((int64_t)(blk / a.n_chan) * (kThreads / a.tx) + ty) * a.run;
-    if (c >= a.C || first >= a.T_) return;
-    const int t1 = (int)min(first + a.run, (int64_t)a.T_);
+    const bool live = c < a.C && first < a.T_;
+    const int t0 = live ? (int)first : 0;
+    const int t1 = live ? (int)min(first + a.run, (int64_t)a.T_) : 0;
 
+    stage_weights<K>(sw, a.weight, c0, a.C, a.tx * V);
     uint64_t w[K][P], b[P];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
@@ -109,10 +113,46 @@ __global__ void __launch_bounds__(kThreads) gdn_short_conv_kernel(const ConvArgs
             const float *wj = sw + j * a.tx * V + tx * V;
             w[j][i] = pack2f(wj[2 * i], V > 1 ? wj[2 * i + 1] : 0.f);
         }
-        b[i] = a.bias ? pack2f(a.bias[c + 2 * i], V > 1 ? a.bias[c + 2 * i + 1] : 0.f) : 0;
+        b[i] = live && a.bias ? pack2f(a.bias[c + 2 * i], V > 1 ? a.bias[c + 2 * i + 1] : 0.f) : 0;
     }
-    // One token's result from the K inputs up to it.
-    auto finish = [&](const uint64_t (&in)[K][P], T *to) {
+    __syncthreads();  // the ring takes the weights' place
+    if (!live) return;
+
+    // A ring of this thread's words: kAhead groups of kStep tokens on their
+    // way while one is computed.  A thread reads only what it copied itself,
+    // so its own wait is all the synchronisation needed.
+    using Word = Vec<T, V>;
+    Word *ring = reinterpret_cast<Word *>(sw) + threadIdx.x;
+    // (Single 16-bit elements are too small for that: their loads are started
+    // together and stored.)
+    auto issue = [&](int t) {
+        const T *from = a.x + t * a.xs + c;
+        Word *to = ring + ((t - t0) % kRing) * kThreads;
+        if constexpr (sizeof(Word) >= 4) {
+#pragma unroll
+            for (int u = 0; u < kStep; ++u)
+                if (t + u < t1) copy_async<sizeof(Word)>(to + u * kThreads, from + u * a.xs);
+        } else {
+            Word word[kStep];
+#pragma unroll
+            for (int u = 0; u < kStep; ++u)
+                if (t + u < t1) word[u] = Word::load(from + u * a.xs);
+#pragma unroll
+            for (int u = 0; u < kStep; ++u)
+                if (t + u < t1) to[u * kThreads] = word[u];
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int g = 0; g < kAhead; ++g) issue(t0 + g * kStep);
+
+    Span s = locate(a.cu, a.N, a.T_, t0);
+    uint64_t in[K][P];  // the K - 1 inputs before a token, and the token's
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) pairs(tap<T, V, K>(a, s.n, s.start, t0 - (K - 1) + j, c), in[j]);
+    T *to = a.out + t0 * a.os + c;
+    auto token = [&](int t) {
+        pairs(ring[((t - t0) % kRing) * kThreads], in[K - 1]);
         float y[2 * P];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -123,55 +163,31 @@ __global__ void __launch_bounds__(kThreads) gdn_short_conv_kernel(const ConvArgs
             const float2 v = unpack2f(sum);
             y[2 * i] = v.x;
             y[2 * i + 1] = v.y;
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) in[j][i] = in[j + 1][i];
         }
-        Vec<T, V>::from(y).store(to);
+        Word::from(y).store(to);
+        to += a.os;
     };
-    Span s = locate(a.cu, a.N, a.T_, (int)first);
-    uint64_t in[K][P];  // the K - 1 inputs before a token, and the token's
-    int t = (int)first;
-    while (t < t1) {
-        if (t >= s.end) s = next_span(a.cu, a.N, a.T_, s);
-        const int e = min(s.end, t1);
-        // The K - 1 inputs before token t, then token by token.
+    for (int t = t0; t < t1; t += kStep) {
+        copies_wait<kAhead - 1>();
+        if (t + kStep <= min(s.end, t1)) {
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) pairs(tap<T, V, K>(a, s.n, s.start, t - (K - 1) + j, c), in[j]);
-        const T *from = a.x + t * a.xs + c;
-        T *to = a.out + t * a.os + c;
-        Vec<T, V> word[kStep];
-        auto fetch = [&](Vec<T, V> (&into)[kStep]) {
+            for (int u = 0; u < kStep; ++u) token(t + u);
+        } else {
+            const int te = min(t + kStep, t1);
+#pragma unroll 1
+            for (int tok = t; tok < te; ++tok) {
+                if (tok >= s.end) {  // the next sequence: its state comes before its tokens
+                    s = next_span(a.cu, a.N, a.T_, s);
 #pragma unroll
-            for (int u = 0; u < kStep; ++u, from += a.xs) into[u] = Vec<T, V>::load(from);
-        };
-        auto step = [&](const Vec<T, V> &x) {
-            pairs(x, in[K - 1]);
-            finish(in, to);
-            to += a.os;
-#pragma unroll
-            for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-                for (int i = 0; i < P; ++i) in[j][i] = in[j + 1][i];
-        };
-        if (t + kStep <= e) {
-            fetch(word);
-            for (; t + kStep <= e; t += kStep) {
-                Vec<T, V> next[kStep];
-                const bool more = t + 2 * kStep <= e;
-                if (more) fetch(next);
-#pragma unroll
-                for (int u = 0; u < kStep; ++u) step(word[u]);
-                if (more)
-#pragma unroll
-                    for (int u = 0; u < kStep; ++u) word[u] = next[u];
+                    for (int j = 0; j < K - 1; ++j)
+                        pairs(tap<T, V, K>(a, s.n, s.start, tok - (K - 1) + j, c), in[j]);
+                }
+                token(tok);
             }
         }
-        // Fewer than a block are left: loaded together as well.
-#pragma unroll
-        for (int u = 0; u < kStep - 1; ++u)
-            if (t + u < e) word[u] = Vec<T, V>::load(from + u * a.xs);
-#pragma unroll
-        for (int u = 0; u < kStep - 1; ++u)
-            if (t + u < e) step(word[u]);
-        t = e;
+        issue(t + kAhead * kStep);
     }
 }
 
@@ -263,7 +279,9 @@ gdn_status run_conv(const gdn_conv_problem &p, const void *x, const float *weigh
         fin ? ((int64_t)p.num_seqs * words + kThreads - 1) / kThreads : 0;
     if (n_main + n_state > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     a.n_main = (int)n_main;
-    const size_t smem = (size_t)a.tx * V * K * sizeof(float);
+    const size_t weights = (size_t)a.tx * V * K * sizeof(float);
+    const size_t ring = kRing * kThreads * sizeof(Vec<T, V>);
+    const size_t smem = weights > ring ? weights : ring;
     // A state written in place must not replace what another block still
     // reads: its blocks then run as a launch of their own.
     const bool apart = fin && fin == init;
