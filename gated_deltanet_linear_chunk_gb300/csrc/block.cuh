@@ -213,6 +213,19 @@ __device__ __forceinline__ Span locate(const int32_t *cu, int N, int T, int t) {
     return span_at(cu, N, T, t, lo);
 }
 
+// The same by all 32 lanes of a warp, for one t: a probe per lane and round.
+__device__ __forceinline__ Span locate_by_warp(const int32_t *cu, int N, int T, int t) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+        const int passed = __popc(__ballot_sync(0xffffffffu, at <= hi && cu[at] <= t));
+        lo += passed * step;
+        hi = min(hi, lo + step - 1);
+    }
+    return span_at(cu, N, T, t, lo);
+}
+
 // The sequence of token t = s.end: the next one that is not empty.
 __device__ __forceinline__ Span next_span(const int32_t *cu, int N, int T, const Span &s) {
     int n = s.n;

@@ -50,10 +50,14 @@ constexpr int kUnroll = 4;      // tokens in flight per thread
 // channels in four blocks per SM 137 us for the output pass, four channels in
 // two blocks 143, one channel in six blocks 176: B and C are read twice as
 // often.)
-template <int NS> constexpr int kChannels = NS <= 8 ? 4 : NS <= 32 ? 2 : 1;
+// (In fp32 two at most: four would leave no shared memory for tiles ahead.)
+template <typename T, int NS>
+constexpr int kChannels = NS <= 8 && sizeof(T) == 2 ? 4 : NS <= 32 ? 2 : 1;
 template <int NS> constexpr int kResident = NS <= 16 ? 3 : 2;  // blocks of kMaxThreads per SM
-// Tokens per shared-memory tile: two tiles of four blocks fit an SM.
-template <typename T, int CH> constexpr int kTile = 64 / ((int)sizeof(T) * CH) < 16 ? 64 / ((int)sizeof(T) * CH) : 16;
+// Tokens per shared-memory tile, and tiles: one is computed, the others are on
+// their way.  Three blocks' tiles fit an SM.
+template <typename T, int CH> constexpr int kTileOf = sizeof(T) * CH <= 4 ? 16 : 8;
+template <typename T, int CH> constexpr int kTilesOf = CH == 2 ? 2 : 3;
 
 template <typename T> struct ScanArgs {
     const T *x, *dt, *B, *C, *z;
@@ -76,7 +80,7 @@ template <typename T> struct ScanArgs {
 
 // A thread's channels and all their states.
 template <typename T, int NS> struct ScanThread {
-    static constexpr int CH = kChannels<NS>;
+    static constexpr int CH = kChannels<T, NS>;
     static constexpr int NP = NS / 2;
     uint64_t A[CH][NP], h[CH][NP];
     float bias[CH], skip[CH], sum[CH];
@@ -254,41 +258,41 @@ __device__ __forceinline__ void copy_first(T *const (&dst)[K], int pitch, const 
     }
 }
 
-// Shared memory of a block: two tiles of x, dt (and z), two of B (and C) as
+// Shared memory of a block: kTiles tiles of x, dt (and z) and of B (and C) as
 // they lie in global memory, and one of B (and C) as fp32, zero past the last
 // state.  ODD: rows of x, dt and z may start at odd 16-bit elements.
 template <typename T, int NS, bool OUT, bool ODD> struct ScanTiles {
-    static constexpr int CH = kChannels<NS>;
-    static constexpr int TILE = kTile<T, CH>;
+    static constexpr int CH = kChannels<T, NS>;
+    static constexpr int kTile = kTileOf<T, CH>, kTiles = kTilesOf<T, CH>;
     static constexpr int kIn = OUT ? 3 : 2, kBC = OUT ? 2 : 1;
     float *bc;     // [B, C][token][state]
-    T *raws;       // the same, as loaded, of two tiles
-    T *ins;        // [x, dt, z][token][channel], of two tiles
+    T *raws;       // the same, as loaded, of every tile
+    T *ins;        // [x, dt, z][token][channel], of every tile
     int width;     // channels per block
     int pitch;     // elements between rows of `ins`
     __device__ ScanTiles(char *smem, int threads) : width(threads * CH) {
         pitch = width + (ODD ? 2 : 0);
         bc = reinterpret_cast<float *>(smem);
-        raws = reinterpret_cast<T *>(bc + kBC * TILE * NS);
-        ins = raws + 2 * kBC * TILE * NS;
+        raws = reinterpret_cast<T *>(bc + kBC * kTile * NS);
+        ins = raws + kTiles * kBC * kTile * NS;
     }
     // Tile `buf` (an offset, not an array of pointers: those would lose the
     // knowledge that they point to shared memory).
-    __device__ __forceinline__ T *raw(int buf) const { return raws + buf * (kBC * TILE * NS); }
-    __device__ __forceinline__ T *in(int buf) const { return ins + buf * (kIn * TILE * pitch); }
+    __device__ __forceinline__ T *raw(int buf) const { return raws + buf * (kBC * kTile * NS); }
+    __device__ __forceinline__ T *in(int buf) const { return ins + buf * (kIn * kTile * pitch); }
     static size_t bytes(int threads) {
-        return kBC * TILE * NS * (sizeof(float) + 2 * sizeof(T)) +
-               2 * kIn * TILE * (threads * CH + (ODD ? 2 : 0)) * sizeof(T);
+        return kBC * kTile * NS * (sizeof(float) + kTiles * sizeof(T)) +
+               kTiles * kIn * kTile * (threads * CH + (ODD ? 2 : 0)) * sizeof(T);
     }
     // Starts the copies of tokens [t, te) (one tile at most) of the block's
     // channels, d the first of `cols`.
     __device__ __forceinline__ void load(const ScanArgs<T> &a, int buf, int t, int te, int d,
                                          int cols, int group) const {
-        const int rows = min(te - t, TILE);
+        const int rows = min(te - t, kTile);
         const T *const src[3] = {a.x + t * a.xs + d, a.dt + t * a.dts + d,
                                  OUT && a.z ? a.z + t * a.zs + d : nullptr};
         const int64_t stride[3] = {a.xs, a.dts, a.zs};
-        T *const dst[3] = {in(buf), in(buf) + TILE * pitch, in(buf) + 2 * TILE * pitch};
+        T *const dst[3] = {in(buf), in(buf) + kTile * pitch, in(buf) + 2 * kTile * pitch};
 #pragma unroll
         for (int k = 0; k < kIn; ++k) {
             if (k == 2 && !a.z) break;
@@ -297,13 +301,13 @@ template <typename T, int NS, bool OUT, bool ODD> struct ScanTiles {
         }
         copy_rows(raw(buf), NS, a.B + t * a.bs + group * a.S, a.bs, rows, a.S, a.bc_word);
         if (OUT)
-            copy_rows(raw(buf) + TILE * NS, NS, a.C + t * a.cs + group * a.S, a.cs, rows, a.S,
+            copy_rows(raw(buf) + kTile * NS, NS, a.C + t * a.cs + group * a.S, a.cs, rows, a.S,
                       a.bc_word);
         if (ODD) copy_first(dst, pitch, src, stride, rows);
     }
     // B and C of the tile that has arrived, to fp32.
     __device__ __forceinline__ void widen(const ScanArgs<T> &a, int buf) const {
-        for (int i = threadIdx.x; i < kBC * TILE * NS; i += blockDim.x)
+        for (int i = threadIdx.x; i < kBC * kTile * NS; i += blockDim.x)
             bc[i] = i % NS < a.S ? to_f32(raw(buf)[i]) : 0.f;
     }
 };
@@ -340,7 +344,7 @@ template <typename T, int NS, bool OUT, bool ODD, int U>
 __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS> &th,
                                          const ScanTiles<T, NS, OUT, ODD> &tl, int buf, int t0,
                                          int t, int odds) {
-    constexpr int CH = kChannels<NS>, TILE = kTile<T, CH>;
+    constexpr int CH = kChannels<T, NS>, kTile = kTileOf<T, CH>;
     float y[U][CH];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -348,7 +352,7 @@ __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS>
         const T *in = tl.in(buf) + r * tl.pitch + th.col;
         const int o = ODD ? odds ^ ((odds >> 4) & -(r & 1)) : 0;
         auto own = [&](int k, float *v) {
-            const T *p = in + k * TILE * tl.pitch;
+            const T *p = in + k * kTile * tl.pitch;
             if (ODD) {
 #pragma unroll
                 for (int c = 0; c < CH; ++c) v[c] = to_f32(p[c + ((o >> k) & 1)]);
@@ -359,7 +363,7 @@ __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS>
         float xv[CH], dv[CH];
         own(0, xv);
         own(1, dv);
-        th.template token<OUT>(a.softplus, xv, dv, tl.bc + r * NS, tl.bc + (TILE + r) * NS, y[u]);
+        th.template token<OUT>(a.softplus, xv, dv, tl.bc + r * NS, tl.bc + (kTile + r) * NS, y[u]);
         if (OUT) {
             float zv[CH];
             own(2, zv);
@@ -385,11 +389,13 @@ __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS>
     }
 }
 
-// Final states of empty sequences are their initial ones: one row of blocks
-// copies them.
+// Final states of empty sequences are their initial ones: rows of blocks of
+// their own copy them, each every kEmptyRows-th sequence.
+constexpr int kEmptyRows = 64;
+
 template <typename T>
-__device__ void copy_empty(const ScanArgs<T> &a, int d0, int cols) {
-    for (int n = 0; n < a.N; ++n) {
+__device__ void copy_empty(const ScanArgs<T> &a, int first, int step, int d0, int cols) {
+    for (int n = first; n < a.N; n += step) {
         if (a.cu[n + 1] > a.cu[n]) continue;
         const int64_t at = ((int64_t)n * a.D + d0) * a.S;
         for (int i = threadIdx.x; i < cols * a.S; i += blockDim.x)
@@ -399,14 +405,14 @@ __device__ void copy_empty(const ScanArgs<T> &a, int d0, int cols) {
 
 template <typename T, int NS, bool OUT, bool ODD>
 __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(const ScanArgs<T> a) {
-    constexpr int CH = kChannels<NS>, TILE = kTile<T, CH>;
+    constexpr int CH = kChannels<T, NS>, kTile = kTileOf<T, CH>, kTiles = kTilesOf<T, CH>;
     extern __shared__ __align__(16) char smem[];
     const ScanTiles<T, NS, OUT, ODD> tl(smem, blockDim.x);
     const int group = blockIdx.x / a.tiles, in_group0 = (blockIdx.x % a.tiles) * tl.width;
     const int w = blockIdx.y, d0 = group * a.per_group + in_group0;
     const int cols = min(tl.width, a.per_group - in_group0);
-    if (OUT && w == a.W) {
-        copy_empty(a, d0, cols);
+    if (OUT && w >= a.W) {
+        copy_empty(a, w - a.W, gridDim.y - a.W, d0, cols);
         return;
     }
     int t0 = w * a.len;
@@ -414,30 +420,35 @@ __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(co
     Span s;
     bool from_carry = false;
     if (OUT) {
-        s = locate(a.cu, a.N, a.T_, t0);
+        s = locate_by_warp(a.cu, a.N, a.T_, t0);
         from_carry = s.start < t0;
     } else {
         // The sequence that goes on past this window's end.
-        s = locate(a.cu, a.N, a.T_, t1 - 1);
+        s = locate_by_warp(a.cu, a.N, a.T_, t1 - 1);
         if (s.end <= t1) return;
         from_carry = s.start < t0;
         t0 = max(t0, s.start);
     }
-    tl.load(a, 0, t0, t1, d0, cols, group);
+    auto fetch = [&](int tile) {
+        const int t = t0 + tile * kTile;
+        if (t < t1) tl.load(a, tile % kTiles, t, t1, d0, cols, group);
+        copies_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < kTiles - 1; ++k) fetch(k);
     ScanThread<T, NS> th;
     th.setup(a, group, in_group0);
     if (OUT) ptx::griddep_wait();  // the carries: all above is input to the whole call
     if (from_carry) th.load(a, OUT ? a.carry : nullptr, w - 1);
     else th.load(a, a.init, s.n);
+    Span next = OUT && s.end < t1 ? next_span(a.cu, a.N, a.T_, s) : s;
 
-    int buf = 0;
-    for (int tt = t0; tt < t1; tt += TILE, buf ^= 1) {
-        const int te = min(tt + TILE, t1);
-        copies_commit();
-        copies_wait<0>();
+    for (int tile = 0, tt = t0; tt < t1; ++tile, tt += kTile) {
+        const int te = min(tt + kTile, t1), buf = tile % kTiles;
+        copies_wait<kTiles - 2>();
         __syncthreads();  // the tile has arrived, and the one before is done with
         tl.widen(a, buf);
-        if (te < t1) tl.load(a, buf ^ 1, te, t1, d0, cols, group);
+        fetch(tile + kTiles - 1);
         int odds = 0;
         if (ODD)
             odds = odd(a.x + tt * a.xs + d0) | odd(a.dt + tt * a.dts + d0) << 1 |
@@ -457,9 +468,10 @@ __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(co
                 if (a.fin && from_carry && a.defer) th.store(a, a.carry, w - 1);
                 else if (a.fin) th.store(a, a.fin, s.n);
                 if (t < t1) {
-                    s = next_span(a.cu, a.N, a.T_, s);
+                    s = next;
                     th.load(a, a.init, s.n);
                     from_carry = false;
+                    if (s.end < t1) next = next_span(a.cu, a.N, a.T_, s);
                 }
             }
         }
@@ -688,11 +700,16 @@ struct ScanPlan {
 // The shortest window.
 constexpr int kMinWindow = 16;
 
+// kChannels, kResident of the variant that runs.
+int channels_per_thread(int dtype, int ns) {
+    return ns <= 8 && dtype == GDN_BF16 ? 4 : ns <= 32 ? 2 : 1;
+}
+
 ScanPlan scan_plan(const gdn_ssm_problem &p) {
     ScanPlan s;
     s.ns = 4;
     while (s.ns < p.state_dim) s.ns *= 2;
-    const int ch = s.ns <= 8 ? 4 : s.ns <= 32 ? 2 : 1, resident = s.ns <= 16 ? 3 : 2;
+    const int ch = channels_per_thread(p.dtype, s.ns), resident = s.ns <= 16 ? 3 : 2;
     const int per_group = p.channels / p.num_groups;
     const int warps = (per_group + 32 * ch - 1) / (32 * ch), most = kMaxThreads / 32;
     s.threads = 32 * (warps < most ? warps : most);
@@ -780,7 +797,7 @@ gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cuda
                                           : gdn_scan_combine_kernel<T, 1>, a) != cudaSuccess)
             return GDN_ERR_CUDA;
     }
-    const unsigned rows = (unsigned)(pl.W + (empties ? 1 : 0));
+    const unsigned rows = (unsigned)(pl.W + (empties ? (a.N < kEmptyRows ? a.N : kEmptyRows) : 0));
     if (rows > 0) {
         cfg.gridDim = dim3(blocks, rows);
         cfg.blockDim = dim3(pl.threads);
@@ -833,7 +850,7 @@ gdn_status scan_typed(const gdn_ssm_problem &p, const void *x, const void *dt, c
     a.in_word = word({x, dt, z}, {p.x_stride, p.dt_stride, z ? p.z_stride : 0, a.per_group});
     a.bc_word = word({B, C}, {p.b_stride, p.c_stride, p.state_dim});
     a.state_words = p.state_dim % 4 == 0 && aligned16(A) && aligned16(init) && aligned16(fin);
-    const int ch = pl.ns <= 8 ? 4 : pl.ns <= 32 ? 2 : 1;
+    const int ch = channels_per_thread(p.dtype, pl.ns);
     a.out_own = (reinterpret_cast<uintptr_t>(out) | (uint64_t)p.out_stride * sizeof(T)) %
                         (ch * sizeof(T)) == 0 && a.per_group % ch == 0;
     // Only a batch of several sequences (or of no tokens) has empty ones.

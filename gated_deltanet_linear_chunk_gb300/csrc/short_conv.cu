@@ -12,7 +12,7 @@
 // not 16-byte aligned) through a run of consecutive tokens.  The last K - 1
 // inputs stay in registers, so only a run's start reads rows again (K - 1
 // rows per run, from L2).  The run's rows come through a ring in shared memory
-// by asynchronous copies, 12 tokens ahead: 24 KB in flight per block without
+// by asynchronous copies, 8 tokens ahead: 16 KB in flight per block without
 // a register.  Channels go in pairs through the packed fp32 instructions.
 #include "block.cuh"
 
@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kStep = 4;   // tokens per group of copies
-constexpr int kAhead = 3;  // groups in flight
+constexpr int kAhead = 2;  // groups in flight
 constexpr int kRing = (kAhead + 1) * kStep;
 
 template <typename T> struct ConvArgs {
@@ -42,12 +42,22 @@ template <typename T> struct ConvArgs {
 
 // The weights of this block's channels as [K][channels] in shared memory:
 // read from [C, K] in order, so that the threads' own columns are not a
-// strided walk over global memory.
+// strided walk over global memory, eight loads before their stores.
 template <int K>
 __device__ __forceinline__ void stage_weights(float *sw, const float *w, int c0, int C, int width) {
-    const int cols = min(width, C - c0);
-    for (int i = threadIdx.x; i < cols * K; i += kThreads)
-        sw[(i % K) * width + i / K] = w[(int64_t)c0 * K + i];
+    const int n = min(width, C - c0) * K;
+    const float *from = w + (int64_t)c0 * K;
+    for (int i0 = threadIdx.x; i0 < n; i0 += 8 * kThreads) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i0 + k * kThreads < n) v[k] = from[i0 + k * kThreads];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kThreads;
+            if (i < n) sw[(i % K) * width + i / K] = v[k];
+        }
+    }
     __syncthreads();
 }
 
@@ -89,7 +99,7 @@ __device__ __forceinline__ void write_state(const ConvArgs<T> &a, int64_t i) {
 }
 
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(kThreads) gdn_short_conv_kernel(const ConvArgs<T> a) {
+__global__ void __launch_bounds__(kThreads, K <= 4 ? 5 : 2) gdn_short_conv_kernel(const ConvArgs<T> a) {
     constexpr int P = (V + 1) / 2;  // pairs of channels
     extern __shared__ __align__(16) float sw[];
     const int blk = blockIdx.x + a.first;
@@ -104,25 +114,11 @@ __global__ void __launch_bounds__(kThreads) gdn_short_conv_kernel(const ConvArgs
     const int t0 = live ? (int)first : 0;
     const int t1 = live ? (int)min(first + a.run, (int64_t)a.T_) : 0;
 
-    stage_weights<K>(sw, a.weight, c0, a.C, a.tx * V);
-    uint64_t w[K][P], b[P];
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-#pragma unroll
-        for (int j = 0; j < K; ++j) {
-            const float *wj = sw + j * a.tx * V + tx * V;
-            w[j][i] = pack2f(wj[2 * i], V > 1 ? wj[2 * i + 1] : 0.f);
-        }
-        b[i] = live && a.bias ? pack2f(a.bias[c + 2 * i], V > 1 ? a.bias[c + 2 * i + 1] : 0.f) : 0;
-    }
-    __syncthreads();  // the ring takes the weights' place
-    if (!live) return;
-
     // A ring of this thread's words: kAhead groups of kStep tokens on their
     // way while one is computed.  A thread reads only what it copied itself,
     // so its own wait is all the synchronisation needed.
     using Word = Vec<T, V>;
-    Word *ring = reinterpret_cast<Word *>(sw) + threadIdx.x;
+    Word *ring = reinterpret_cast<Word *>(sw + a.tx * V * K) + threadIdx.x;
     // (Single 16-bit elements are too small for that: their loads are started
     // together and stored.)
     auto issue = [&](int t) {
@@ -146,10 +142,30 @@ __global__ void __launch_bounds__(kThreads) gdn_short_conv_kernel(const ConvArgs
 #pragma unroll
     for (int g = 0; g < kAhead; ++g) issue(t0 + g * kStep);
 
-    Span s = locate(a.cu, a.N, a.T_, t0);
+    // Then, while they come: the sequence, the inputs before the run, the weights.
+    Span s{};
     uint64_t in[K][P];  // the K - 1 inputs before a token, and the token's
+    if (live) {
+        s = locate(a.cu, a.N, a.T_, t0);
+        Word word[K - 1];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) pairs(tap<T, V, K>(a, s.n, s.start, t0 - (K - 1) + j, c), in[j]);
+        for (int j = 0; j < K - 1; ++j)
+            word[j] = tap<T, V, K>(a, s.n, s.start, t0 - (K - 1) + j, c);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) pairs(word[j], in[j]);
+    }
+    stage_weights<K>(sw, a.weight, c0, a.C, a.tx * V);
+    if (!live) return;
+    uint64_t w[K][P], b[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            const float *wj = sw + j * a.tx * V + tx * V;
+            w[j][i] = pack2f(wj[2 * i], V > 1 ? wj[2 * i + 1] : 0.f);
+        }
+        b[i] = a.bias ? pack2f(a.bias[c + 2 * i], V > 1 ? a.bias[c + 2 * i + 1] : 0.f) : 0;
+    }
     T *to = a.out + t0 * a.os + c;
     auto token = [&](int t) {
         pairs(ring[((t - t0) % kRing) * kThreads], in[K - 1]);
@@ -238,10 +254,10 @@ __global__ void __launch_bounds__(kThreads) gdn_short_conv_step_kernel(const Ste
     }
 }
 
-// Threads along the channels: the words of a row, up to the block.
-int threads_along(int words) {
+// Threads along the channels: the words of a row, up to `most`.
+int threads_along(int words, int most) {
     int tx = 1;
-    while (tx < words && tx < kThreads) tx *= 2;
+    while (tx < words && tx < most) tx *= 2;
     return tx;
 }
 
@@ -264,7 +280,9 @@ gdn_status run_conv(const gdn_conv_problem &p, const void *x, const float *weigh
     a.os = p.out_stride;
     a.act = p.activation == GDN_ACT_SILU;
     const int words = p.channels / V;
-    a.tx = threads_along(words);
+    // (Half a block along the channels where all of it would need more than
+    // the 48 KB of shared memory that a kernel has by default.)
+    a.tx = threads_along(words, V * K > 48 ? kThreads / 2 : kThreads);
     a.n_chan = (words + a.tx - 1) / a.tx;
     const int ty = kThreads / a.tx;
     // Tokens per thread: long runs read fewer rows twice (K - 1 of each
@@ -272,16 +290,19 @@ gdn_status run_conv(const gdn_conv_problem &p, const void *x, const float *weigh
     auto blocks = [&](int run) {
         return (int64_t)a.n_chan * ((p.total_tokens + (int64_t)run * ty - 1) / ((int64_t)run * ty));
     };
-    a.run = 32;
-    while (a.run > 1 && blocks(a.run) < 8 * kGridSms) a.run /= 2;
+    // One wave of blocks with runs of up to 64 tokens, or so many full waves;
+    // at least 8 tokens while four blocks per SM are left.
+    const int64_t slots = (K <= 4 ? 5 : 2) * kGridSms;
+    const int64_t each = (p.total_tokens * a.n_chan + slots * ty - 1) / (slots * ty);
+    const int64_t waves = (each + 63) / 64;
+    a.run = (int)((each + waves - 1) / (waves > 0 ? waves : 1));
+    a.run = a.run < 1 ? 1 : a.run;
     const int64_t n_main = blocks(a.run);
     const int64_t n_state =
         fin ? ((int64_t)p.num_seqs * words + kThreads - 1) / kThreads : 0;
     if (n_main + n_state > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     a.n_main = (int)n_main;
-    const size_t weights = (size_t)a.tx * V * K * sizeof(float);
-    const size_t ring = kRing * kThreads * sizeof(Vec<T, V>);
-    const size_t smem = weights > ring ? weights : ring;
+    const size_t smem = (size_t)a.tx * V * K * sizeof(float) + kRing * kThreads * sizeof(Vec<T, V>);
     // A state written in place must not replace what another block still
     // reads: its blocks then run as a launch of their own.
     const bool apart = fin && fin == init;
@@ -312,7 +333,7 @@ gdn_status run_step(const gdn_conv_problem &p, const void *x, const float *weigh
     a.os = p.out_stride;
     a.act = p.activation == GDN_ACT_SILU;
     const int words = p.channels / V;
-    a.tx = threads_along(words);
+    a.tx = threads_along(words, kThreads);
     a.n_chan = (words + a.tx - 1) / a.tx;
     const int ty = kThreads / a.tx;
     auto blocks = [&](int run) {
