@@ -45,17 +45,18 @@ constexpr int kMaxThreads = 128;
 constexpr int kUnroll = 4;      // tokens in flight per thread
 
 // NS: the states padded to a power of two (A = B = 0 beyond S: those states
-// stay zero).  Channels per thread: states and decay rates take half of 128
-// registers up to NS = 16, of 255 above.  (At NS = 16, 4000 x 6144: two
-// channels in four blocks per SM 137 us for the output pass, four channels in
-// two blocks 143, one channel in six blocks 176: B and C are read twice as
-// often.)
-// (In fp32 two at most: four would leave no shared memory for tiles ahead.)
-template <typename T, int NS>
-constexpr int kChannels = NS <= 8 && sizeof(T) == 2 ? 4 : NS <= 32 ? 2 : 1;
-template <int NS> constexpr int kResident = NS <= 16 ? 3 : 2;  // blocks of kMaxThreads per SM
+// stay zero).  Two channels per thread, one where a channel's states and
+// decay rates alone take 128 registers.  (4000 x 6144, 16 states, output pass:
+// two channels in three blocks per SM 113 us, four in two blocks 143, one in
+// six 176, where B and C are read twice as often.  1536 channels, 8 states:
+// two channels 42 us the whole call, four 54.)
+template <int NS> constexpr int kChannels = NS <= 32 ? 2 : 1;
+// Blocks of kMaxThreads per SM.  Three leave 168 registers, with which the
+// four tokens of a run overlap; four blocks (128 registers) took 8 % longer,
+// two 10 %.
+template <int NS> constexpr int kResident = NS <= 16 ? 3 : 2;
 // Tokens per shared-memory tile, and tiles: one is computed, the others are on
-// their way.  Three blocks' tiles fit an SM.
+// their way.
 template <typename T, int CH> constexpr int kTileOf = sizeof(T) * CH <= 4 ? 16 : 8;
 template <typename T, int CH> constexpr int kTilesOf = CH == 2 ? 2 : 3;
 
@@ -80,7 +81,7 @@ template <typename T> struct ScanArgs {
 
 // A thread's channels and all their states.
 template <typename T, int NS> struct ScanThread {
-    static constexpr int CH = kChannels<T, NS>;
+    static constexpr int CH = kChannels<NS>;
     static constexpr int NP = NS / 2;
     uint64_t A[CH][NP], h[CH][NP];
     float bias[CH], skip[CH], sum[CH];
@@ -262,7 +263,7 @@ __device__ __forceinline__ void copy_first(T *const (&dst)[K], int pitch, const 
 // they lie in global memory, and one of B (and C) as fp32, zero past the last
 // state.  ODD: rows of x, dt and z may start at odd 16-bit elements.
 template <typename T, int NS, bool OUT, bool ODD> struct ScanTiles {
-    static constexpr int CH = kChannels<T, NS>;
+    static constexpr int CH = kChannels<NS>;
     static constexpr int kTile = kTileOf<T, CH>, kTiles = kTilesOf<T, CH>;
     static constexpr int kIn = OUT ? 3 : 2, kBC = OUT ? 2 : 1;
     float *bc;     // [B, C][token][state]
@@ -312,30 +313,6 @@ template <typename T, int NS, bool OUT, bool ODD> struct ScanTiles {
     }
 };
 
-// CH elements of shared memory, aligned to CH.
-template <int CH> __device__ __forceinline__ void load_own(const float *p, float *r) {
-    Vec<float, CH>::load(p).to(r);
-}
-template <int CH> __device__ __forceinline__ void load_own(const __nv_bfloat16 *p, float *r) {
-    if constexpr (CH == 4) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p);
-        Vec<__nv_bfloat16, 2>{w.x}.to(r);
-        Vec<__nv_bfloat16, 2>{w.y}.to(r + 2);
-    } else {
-        Vec<__nv_bfloat16, CH>::load(p).to(r);
-    }
-}
-// The same to global memory.
-template <int CH> __device__ __forceinline__ void store_own(float *p, const float *r) {
-    Vec<float, CH>::from(r).store(p);
-}
-template <int CH> __device__ __forceinline__ void store_own(__nv_bfloat16 *p, const float *r) {
-    if constexpr (CH == 4)
-        *reinterpret_cast<uint2 *>(p) = make_uint2(Vec<__nv_bfloat16, 2>::from(r).w,
-                                                   Vec<__nv_bfloat16, 2>::from(r + 2).w);
-    else
-        Vec<__nv_bfloat16, CH>::from(r).store(p);
-}
 
 // U tokens from t of tile `buf`, whose first token is t0.  `odds`: whether
 // the tile's first rows of x, dt and z are odd, in bits 0 to 2, and whether
@@ -344,7 +321,7 @@ template <typename T, int NS, bool OUT, bool ODD, int U>
 __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS> &th,
                                          const ScanTiles<T, NS, OUT, ODD> &tl, int buf, int t0,
                                          int t, int odds) {
-    constexpr int CH = kChannels<T, NS>, kTile = kTileOf<T, CH>;
+    constexpr int CH = kChannels<NS>, kTile = kTileOf<T, CH>;
     float y[U][CH];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -357,7 +334,7 @@ __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS>
 #pragma unroll
                 for (int c = 0; c < CH; ++c) v[c] = to_f32(p[c + ((o >> k) & 1)]);
             } else {
-                load_own<CH>(p, v);
+                Vec<T, CH>::load(p).to(v);
             }
         };
         float xv[CH], dv[CH];
@@ -379,7 +356,7 @@ __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS>
     if (!ODD && a.out_own) {
 #pragma unroll
         for (int u = 0; u < U; ++u, out += a.os)
-            if (th.valid) store_own<CH>(out, y[u]);
+            if (th.valid) Vec<T, CH>::from(y[u]).store(out);
     } else {
 #pragma unroll
         for (int u = 0; u < U; ++u, out += a.os)
@@ -405,7 +382,7 @@ __device__ void copy_empty(const ScanArgs<T> &a, int first, int step, int d0, in
 
 template <typename T, int NS, bool OUT, bool ODD>
 __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(const ScanArgs<T> a) {
-    constexpr int CH = kChannels<T, NS>, kTile = kTileOf<T, CH>, kTiles = kTilesOf<T, CH>;
+    constexpr int CH = kChannels<NS>, kTile = kTileOf<T, CH>, kTiles = kTilesOf<T, CH>;
     extern __shared__ __align__(16) char smem[];
     const ScanTiles<T, NS, OUT, ODD> tl(smem, blockDim.x);
     const int group = blockIdx.x / a.tiles, in_group0 = (blockIdx.x % a.tiles) * tl.width;
@@ -700,16 +677,15 @@ struct ScanPlan {
 // The shortest window.
 constexpr int kMinWindow = 16;
 
-// kChannels, kResident of the variant that runs.
-int channels_per_thread(int dtype, int ns) {
-    return ns <= 8 && dtype == GDN_BF16 ? 4 : ns <= 32 ? 2 : 1;
-}
+// kChannels and kResident of the variant that runs.
+int channels_per_thread(int ns) { return ns <= 32 ? 2 : 1; }
+int resident_blocks(int ns) { return ns <= 16 ? 3 : 2; }
 
 ScanPlan scan_plan(const gdn_ssm_problem &p) {
     ScanPlan s;
     s.ns = 4;
     while (s.ns < p.state_dim) s.ns *= 2;
-    const int ch = channels_per_thread(p.dtype, s.ns), resident = s.ns <= 16 ? 3 : 2;
+    const int ch = channels_per_thread(s.ns), resident = resident_blocks(s.ns);
     const int per_group = p.channels / p.num_groups;
     const int warps = (per_group + 32 * ch - 1) / (32 * ch), most = kMaxThreads / 32;
     s.threads = 32 * (warps < most ? warps : most);
@@ -850,7 +826,7 @@ gdn_status scan_typed(const gdn_ssm_problem &p, const void *x, const void *dt, c
     a.in_word = word({x, dt, z}, {p.x_stride, p.dt_stride, z ? p.z_stride : 0, a.per_group});
     a.bc_word = word({B, C}, {p.b_stride, p.c_stride, p.state_dim});
     a.state_words = p.state_dim % 4 == 0 && aligned16(A) && aligned16(init) && aligned16(fin);
-    const int ch = channels_per_thread(p.dtype, pl.ns);
+    const int ch = channels_per_thread(pl.ns);
     a.out_own = (reinterpret_cast<uintptr_t>(out) | (uint64_t)p.out_stride * sizeof(T)) %
                         (ch * sizeof(T)) == 0 && a.per_group % ch == 0;
     // Only a batch of several sequences (or of no tokens) has empty ones.
