@@ -5,6 +5,8 @@ one shared library with the CUDA runtime linked statically, so the library
 loads on a machine without a GPU (only the C ABI symbols are exported).  A
 second variant, libgdn_debug, is built with GDN_DEBUG: the same kernels plus
 device-side checks of the inputs' preconditions and of the kernels' indices.
+The host compiler builds the extension module that marshals the block
+operators' tensors.
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import os
 import platform
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -32,6 +35,35 @@ def library_path(debug: bool = False) -> str:
     return os.path.join(BUILD, f"{name}_{platform.machine()}.so")
 
 
+def binding_path() -> str:
+    """The extension module that marshals the block operators' tensors."""
+    return os.path.join(BUILD, f"gdn_block_binding_{platform.machine()}.so")
+
+
+def _binding_command(out: str):
+    """Compiles csrc/block_binding.cpp against this Python and PyTorch; their
+    libraries are those that `import torch` has already loaded."""
+    import torch
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", os.path.join(home, "include"), "-I", sysconfig.get_paths()["include"],
+            "-I", os.path.join(cuda, "include"), "-I", INCLUDE,
+            os.path.join(CSRC, "block_binding.cpp"), "-o", out,
+            "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda"]
+
+
+def _build_binding() -> None:
+    out = binding_path()
+    tmp = out + ".tmp"
+    r = subprocess.run(_binding_command(tmp), capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on block_binding.cpp:\n{r.stderr}")
+    os.replace(tmp, out)
+
+
 def _nvcc() -> str:
     for cand in (shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -44,7 +76,7 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
@@ -57,11 +89,14 @@ def _stale(out: str) -> bool:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), debug=None) -> str:
     """Compile every CUDA source and link the library: debug=None builds the
-    release and the GDN_DEBUG variants (their sources compiled in one
-    parallel pool), True or False one of them.  Returns the path of the
+    release and the GDN_DEBUG variants and the binding (their sources compiled
+    in one parallel pool), True or False one of the variants.  Returns the path of the
     release library (or of the one variant asked for)."""
     variants = [False, True] if debug is None else [bool(debug)]
     todo = [v for v in variants if force or _stale(library_path(v))]
+    binding = debug is None and (force or _stale(binding_path()))
+    if binding and not todo:
+        _build_binding()
     if todo:
         nvcc = _nvcc()
         srcs = _sources()
@@ -84,8 +119,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug=None
         for dbg in todo:
             os.makedirs(obj_dir(dbg), exist_ok=True)
         jobs = [(dbg, src) for dbg in todo for src in srcs]
-        with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
+        with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
+            module = ex.submit(_build_binding) if binding else None
             objs = list(ex.map(compile_one, jobs))
+            if module:
+                module.result()
         for dbg in todo:
             out = library_path(dbg)
             mine = [o for (d, _), o in zip(jobs, objs) if d == dbg]

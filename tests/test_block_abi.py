@@ -159,32 +159,36 @@ def test_binding_refuses_host_tensors_and_wrong_types():
                                torch.zeros(4, 1, 2), torch.zeros(2, dtype=torch.int32))
 
 
-def test_binding_checks_rows():
-    """Strided rows pass, overlapping or scattered ones do not (the device is
-    checked first: here through the helper)."""
-    from gated_deltanet_linear_chunk_gb300 import block
-
-    class OnDevice:
-        """A tensor as the helper sees it, on device 0."""
-        def __new__(cls, t):
-            t = t.as_subclass(_Fake)
-            return t
-
-    class _Fake(torch.Tensor):
-        def get_device(self):
-            return 0
+def test_binding_checks_rows(lib):
+    """Strided rows pass, overlapping or scattered ones do not (types, shapes
+    and strides are checked before the device, so no GPU is needed to see it:
+    what passes is then refused for being on the host)."""
     f32 = torch.float32
 
-    def rows(t, shape=None):
-        return block._rows(OnDevice(t), "t", f32, shape or t.shape, 0)
-    assert rows(torch.zeros(4, 24)[:, 3:11]) == 24
-    assert rows(torch.zeros(4, 24)[:, 4:20].unflatten(1, (2, 8))) == 24
-    assert rows(torch.zeros(0, 8).as_strided((0, 8), (0, 0))) == 8
-    for bad in (torch.zeros(8, 4).t(), torch.zeros(1, 8).expand(4, 8), torch.zeros(4, 16)[:, ::2],
-                torch.zeros(4, 8, 2).transpose(1, 2)):
+    def conv(x):
+        gdn.gdn_short_conv_step(x, torch.zeros(8, 4), torch.zeros(4, 3, 8))
+
+    def scan(B):
+        x = torch.zeros(4, 8)
+        gdn.gdn_selective_scan_step(x, x, torch.zeros(8, 8), B, B, torch.zeros(4, 8, 8))
+    for good in (torch.zeros(4, 8), torch.zeros(4, 24)[:, 3:11]):
+        with pytest.raises(ValueError, match="one CUDA device"):
+            conv(good)
+    for bad in (torch.zeros(8, 4).t(), torch.zeros(1, 8).expand(4, 8), torch.zeros(4, 16)[:, ::2]):
         with pytest.raises(ValueError, match="contiguous within"):
-            rows(bad)
-    with pytest.raises(ValueError, match="shape"):
-        rows(torch.zeros(4, 8), (4, 9))
+            conv(bad)
+    # Rows of B are not reached before x: it is refused for its device.
+    with pytest.raises(ValueError, match="one CUDA device"):
+        scan(torch.zeros(4, 24)[:, 4:20].unflatten(1, (2, 8)))
     with pytest.raises(TypeError):
-        rows(torch.zeros(4, 8, dtype=torch.float64))
+        conv(torch.zeros(4, 8, dtype=torch.float64))
+    with pytest.raises(ValueError, match="dimensions"):
+        conv(torch.zeros(4, 2, 8))
+    with pytest.raises(ValueError, match="taps|tap"):
+        gdn.gdn_short_conv_step(torch.zeros(4, 8, dtype=f32), torch.zeros(8, 0),
+                                torch.zeros(4, 0, 8))
+    with pytest.raises(TypeError, match="must be a tensor"):
+        gdn.gdn_short_conv_step([1.0], torch.zeros(8, 4), torch.zeros(4, 3, 8))
+    with pytest.raises(ValueError, match="activation"):
+        gdn.gdn_short_conv_step(torch.zeros(4, 8), torch.zeros(8, 4), torch.zeros(4, 3, 8),
+                                activation="tanh")
