@@ -149,6 +149,7 @@ template <> struct Vec<__nv_bfloat16, 2> {
         const __nv_bfloat162 h = __floats2bfloat162_rn(r[0], r[1]);
         return Vec{*reinterpret_cast<const uint32_t *>(&h)};
     }
+    __device__ __forceinline__ static Vec zero() { return Vec{0u}; }
 };
 template <> struct Vec<float, 2> {
     float2 w;
@@ -161,6 +162,10 @@ template <> struct Vec<float, 2> {
         return Vec{make_float2(r[0], r[1])};
     }
 };
+// Whether element p lies in the upper half of its 4-byte word.
+template <typename T> __device__ __forceinline__ int odd(const T *p) {
+    return (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & 1;
+}
 template <typename T> constexpr int kWide = 16 / (int)sizeof(T);
 
 // Whether rows at p, `stride` elements apart, start on 16-byte boundaries.

@@ -222,11 +222,6 @@ __device__ __forceinline__ void copy_rows(T *dst, int pitch, const T *src, int64
     }
 }
 
-// Whether element p lies in the upper half of its 4-byte word.
-template <typename T> __device__ __forceinline__ int odd(const T *p) {
-    return (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & 1;
-}
-
 // The same for 16-bit rows that may start at odd elements: element c of a
 // row goes to place c + odd(row), so that both sides of the copies are whole
 // 4-byte words.  A row's first element, where odd, is left to copy_first.

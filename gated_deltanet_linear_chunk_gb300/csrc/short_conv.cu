@@ -8,12 +8,15 @@
 // element) against 2 K flops, so both kernels are bound by HBM bandwidth and,
 // for few tokens, by the latency of one load and one store.
 //
-// A thread takes one 16-byte word of channels (one element where the rows are
-// not 16-byte aligned) through a run of consecutive tokens.  The last K - 1
+// A thread takes one 16-byte word of channels (two 16-bit elements or one
+// element where the rows' alignment allows no more) through a run of
+// consecutive tokens.  The last K - 1
 // inputs stay in registers, so only a run's start reads rows again (K - 1
 // rows per run, from L2).  The run's rows come through a ring in shared memory
 // by asynchronous copies, 8 tokens ahead: 16 KB in flight per block without
 // a register.  Channels go in pairs through the packed fp32 instructions.
+#include <type_traits>
+
 #include "block.cuh"
 
 namespace gdn {
@@ -116,28 +119,34 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 5 : 2) gdn_short_conv_kerne
 
     // A ring of this thread's words: kAhead groups of kStep tokens on their
     // way while one is computed.  A thread reads only what it copied itself,
-    // so its own wait is all the synchronisation needed.
+    // so its own wait is all the synchronisation needed.  (A single 16-bit
+    // element comes as the aligned 4-byte word that holds it, without the
+    // upper half where that is not needed.)
     using Word = Vec<T, V>;
-    Word *ring = reinterpret_cast<Word *>(sw + a.tx * V * K) + threadIdx.x;
-    // (Single 16-bit elements are too small for that: their loads are started
-    // together and stored.)
+    using Slot = std::conditional_t<sizeof(Word) == 2, uint32_t, Word>;
+    Slot *ring = reinterpret_cast<Slot *>(sw + a.tx * V * K) + threadIdx.x;
     auto issue = [&](int t) {
         const T *from = a.x + t * a.xs + c;
-        Word *to = ring + ((t - t0) % kRing) * kThreads;
-        if constexpr (sizeof(Word) >= 4) {
+        Slot *to = ring + ((t - t0) % kRing) * kThreads;
 #pragma unroll
-            for (int u = 0; u < kStep; ++u)
-                if (t + u < t1) copy_async<sizeof(Word)>(to + u * kThreads, from + u * a.xs);
-        } else {
-            Word word[kStep];
-#pragma unroll
-            for (int u = 0; u < kStep; ++u)
-                if (t + u < t1) word[u] = Word::load(from + u * a.xs);
-#pragma unroll
-            for (int u = 0; u < kStep; ++u)
-                if (t + u < t1) to[u * kThreads] = word[u];
+        for (int u = 0; u < kStep; ++u, from += a.xs) {
+            if (t + u >= t1) break;
+            if constexpr (sizeof(Word) == 2)
+                copy_async_part(to + u * kThreads, from - odd(from), odd(from) ? 4 : 2);
+            else
+                copy_async<sizeof(Word)>(to + u * kThreads, from);
         }
         copies_commit();
+    };
+    auto arrived = [&](int t) {
+        const Slot v = ring[((t - t0) % kRing) * kThreads];
+        if constexpr (sizeof(Word) == 2) {
+            const T *from = a.x + t * a.xs + c;
+            const uint16_t half = (uint16_t)(odd(from) ? v >> 16 : v);
+            return *reinterpret_cast<const Word *>(&half);
+        } else {
+            return v;
+        }
     };
 #pragma unroll
     for (int g = 0; g < kAhead; ++g) issue(t0 + g * kStep);
@@ -168,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 5 : 2) gdn_short_conv_kerne
     }
     T *to = a.out + t0 * a.os + c;
     auto token = [&](int t) {
-        pairs(ring[((t - t0) % kRing) * kThreads], in[K - 1]);
+        pairs(arrived(t), in[K - 1]);
         float y[2 * P];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -224,15 +233,22 @@ __global__ void __launch_bounds__(kThreads) gdn_short_conv_step_kernel(const Ste
     const int tx = threadIdx.x & (a.tx - 1), ty = threadIdx.x / a.tx;
     const int c0 = (blockIdx.x % a.n_chan) * a.tx * V, c = c0 + tx * V;
     const int64_t first = ((int64_t)(blockIdx.x / a.n_chan) * (kThreads / a.tx) + ty) * a.run;
-    stage_weights<K>(sw, a.weight, c0, a.C, a.tx * V);
-    if (c >= a.C) return;
-    const int last = (int)min(first + a.run, (int64_t)a.N);
-    for (int n = (int)first; n < last; ++n) {
-        Vec<T, V> rows[K];
+    const int last = c < a.C ? (int)min(first + a.run, (int64_t)a.N) : 0;
+    // The next sequence's rows are loaded before the one at hand is computed,
+    // the first one's before the weights.
+    using Word = Vec<T, V>;
+    Word rows[K];
+    auto fetch = [&](Word (&into)[K], int64_t n) {
 #pragma unroll
         for (int j = 0; j < K - 1; ++j)
-            rows[j] = Vec<T, V>::load(a.state + ((int64_t)n * (K - 1) + j) * a.C + c);
-        rows[K - 1] = Vec<T, V>::load(a.x + n * a.xs + c);
+            into[j] = Word::load(a.state + (n * (K - 1) + j) * a.C + c);
+        into[K - 1] = Word::load(a.x + n * a.xs + c);
+    };
+    if (first < last) fetch(rows, first);
+    stage_weights<K>(sw, a.weight, c0, a.C, a.tx * V);
+    for (int n = (int)first; n < last; ++n) {
+        Word ahead[K];
+        if (n + 1 < last) fetch(ahead, n + 1);
         float y[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) y[v] = a.bias ? a.bias[c + v] : 0.f;
@@ -247,10 +263,13 @@ __global__ void __launch_bounds__(kThreads) gdn_short_conv_step_kernel(const Ste
         if (a.act)
 #pragma unroll
             for (int v = 0; v < V; ++v) y[v] = silu(y[v]);
-        Vec<T, V>::from(y).store(a.out + n * a.os + c);
+        Word::from(y).store(a.out + n * a.os + c);
 #pragma unroll
         for (int j = 0; j < K - 1; ++j)
             rows[j + 1].store(a.next + ((int64_t)n * (K - 1) + j) * a.C + c);
+        if (n + 1 < last)
+#pragma unroll
+            for (int j = 0; j < K; ++j) rows[j] = ahead[j];
     }
 }
 
@@ -302,7 +321,7 @@ gdn_status run_conv(const gdn_conv_problem &p, const void *x, const float *weigh
         fin ? ((int64_t)p.num_seqs * words + kThreads - 1) / kThreads : 0;
     if (n_main + n_state > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     a.n_main = (int)n_main;
-    const size_t smem = (size_t)a.tx * V * K * sizeof(float) + kRing * kThreads * sizeof(Vec<T, V>);
+    const size_t smem = (size_t)a.tx * V * K * sizeof(float) + kRing * kThreads * (sizeof(T) * V < 4 ? 4 : sizeof(T) * V);
     // A state written in place must not replace what another block still
     // reads: its blocks then run as a launch of their own.
     const bool apart = fin && fin == init;
@@ -347,28 +366,47 @@ gdn_status run_step(const gdn_conv_problem &p, const void *x, const float *weigh
     return launch_status();
 }
 
-// f(V, K) of one element type: the word width by `wide`, K by the width.
-#define GDN_CONV_DISPATCH(run, T)                                                              \
-    switch (p.width) {                                                                         \
-        case 2: return wide ? run<T, kWide<T>, 2>(GDN_CONV_ARGS) : run<T, 1, 2>(GDN_CONV_ARGS); \
-        case 3: return wide ? run<T, kWide<T>, 3>(GDN_CONV_ARGS) : run<T, 1, 3>(GDN_CONV_ARGS); \
-        case 4: return wide ? run<T, kWide<T>, 4>(GDN_CONV_ARGS) : run<T, 1, 4>(GDN_CONV_ARGS); \
-        case 5: return wide ? run<T, kWide<T>, 5>(GDN_CONV_ARGS) : run<T, 1, 5>(GDN_CONV_ARGS); \
-        case 6: return wide ? run<T, kWide<T>, 6>(GDN_CONV_ARGS) : run<T, 1, 6>(GDN_CONV_ARGS); \
-        case 7: return wide ? run<T, kWide<T>, 7>(GDN_CONV_ARGS) : run<T, 1, 7>(GDN_CONV_ARGS); \
-        case 8: return wide ? run<T, kWide<T>, 8>(GDN_CONV_ARGS) : run<T, 1, 8>(GDN_CONV_ARGS); \
-    }                                                                                          \
+// f<V>(K): the word by the rows' alignment, K by the width.
+#define GDN_CONV_WIDTHS(run, T, V)                        \
+    switch (p.width) {                                    \
+        case 2: return run<T, V, 2>(GDN_CONV_ARGS);       \
+        case 3: return run<T, V, 3>(GDN_CONV_ARGS);       \
+        case 4: return run<T, V, 4>(GDN_CONV_ARGS);       \
+        case 5: return run<T, V, 5>(GDN_CONV_ARGS);       \
+        case 6: return run<T, V, 6>(GDN_CONV_ARGS);       \
+        case 7: return run<T, V, 7>(GDN_CONV_ARGS);       \
+        case 8: return run<T, V, 8>(GDN_CONV_ARGS);       \
+    }                                                     \
     return GDN_ERR_UNSUPPORTED;
+#define GDN_CONV_DISPATCH(run, T, word)                   \
+    if (word == kWide<T>) {                               \
+        GDN_CONV_WIDTHS(run, T, kWide<T>)                 \
+    }                                                     \
+    if constexpr (sizeof(T) == 2)                         \
+        if (word == 2) {                                  \
+            GDN_CONV_WIDTHS(run, T, 2)                    \
+        }                                                 \
+    GDN_CONV_WIDTHS(run, T, 1)
+
+// The widest word of rows of x and out, and of contiguous states: whole 16
+// bytes, two 16-bit elements, or one element.
+template <typename T>
+int conv_word(const gdn_conv_problem &p, const void *x, const void *out, const void *a,
+              const void *b) {
+    const uint64_t bits = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out) |
+                          reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
+                          (uint64_t)p.x_stride * sizeof(T) | (uint64_t)p.out_stride * sizeof(T) |
+                          (uint64_t)p.channels * sizeof(T);
+    return bits % 16 == 0 ? kWide<T> : sizeof(T) == 2 && bits % 4 == 0 ? 2 : 1;
+}
 
 template <typename T>
 gdn_status conv_typed(const gdn_conv_problem &p, const void *x, const float *weight,
                       const float *bias, const int32_t *cu, const void *init, void *out,
                       void *fin, cudaStream_t stream) {
-    const bool wide = p.channels % kWide<T> == 0 && rows_aligned16<T>(x, p.x_stride) &&
-                      rows_aligned16<T>(out, p.out_stride) && rows_aligned16<T>(init, 0) &&
-                      rows_aligned16<T>(fin, 0);
+    const int word = conv_word<T>(p, x, out, init, fin);
 #define GDN_CONV_ARGS p, x, weight, bias, cu, init, out, fin, stream
-    GDN_CONV_DISPATCH(run_conv, T)
+    GDN_CONV_DISPATCH(run_conv, T, word)
 #undef GDN_CONV_ARGS
 }
 
@@ -376,11 +414,9 @@ template <typename T>
 gdn_status step_typed(const gdn_conv_problem &p, const void *x, const float *weight,
                       const float *bias, const void *state, void *out, void *next,
                       cudaStream_t stream) {
-    const bool wide = p.channels % kWide<T> == 0 && rows_aligned16<T>(x, p.x_stride) &&
-                      rows_aligned16<T>(out, p.out_stride) && rows_aligned16<T>(state, 0) &&
-                      rows_aligned16<T>(next, 0);
+    const int word = conv_word<T>(p, x, out, state, next);
 #define GDN_CONV_ARGS p, x, weight, bias, state, out, next, stream
-    GDN_CONV_DISPATCH(run_step, T)
+    GDN_CONV_DISPATCH(run_step, T, word)
 #undef GDN_CONV_ARGS
 }
 
