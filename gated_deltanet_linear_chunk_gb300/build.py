@@ -90,11 +90,12 @@ def _stale(out: str) -> bool:
 def build(force: bool = False, verbose: bool = False, extra_flags=(), debug=None) -> str:
     """Compile every CUDA source and link the library: debug=None builds the
     release and the GDN_DEBUG variants and the binding (their sources compiled
-    in one parallel pool), True or False one of the variants.  Returns the path of the
+    in one parallel pool), False the release variant and the binding, True the
+    GDN_DEBUG one.  Returns the path of the
     release library (or of the one variant asked for)."""
     variants = [False, True] if debug is None else [bool(debug)]
     todo = [v for v in variants if force or _stale(library_path(v))]
-    binding = debug is None and (force or _stale(binding_path()))
+    binding = debug is not True and (force or _stale(binding_path()))
     if binding and not todo:
         _build_binding()
     if todo:

@@ -669,8 +669,9 @@ struct ScanPlan {
     int ns, threads, tiles, W, len;
 };
 
-// The shortest window.
-constexpr int kMinWindow = 16;
+// The shortest window.  (128 tokens of 1024 channels, us by windows: 1 35, 4 21,
+// 8 14, 16 12.5, 24 12.2, 48 18; 64 tokens of 6144: 1 19.5, 4 21, 8 18, 24 24.)
+constexpr int kMinWindow = 8;
 
 // kChannels and kResident of the variant that runs.
 int channels_per_thread(int ns) { return ns <= 32 ? 2 : 1; }
@@ -690,7 +691,10 @@ ScanPlan scan_plan(const gdn_ssm_problem &p) {
     int64_t W = (int64_t)resident * kGridSms * (kMaxThreads / s.threads) / blocks;
     const int64_t short_enough = p.total_tokens / kMinWindow;
     W = W < short_enough ? W : short_enough;
-    W = W < 1 ? 1 : W;
+    // Two windows do 1.4 times the work of one for twice the blocks, with two
+    // more launches: not worth it (2000 x 128: 440 us against 538, 128 x 1024
+    // 33 against 35, 4000 x 6144 1249 against 987).
+    W = W < 3 ? 1 : W;
     const int64_t len = (p.total_tokens + W - 1) / W;
     s.len = (int)(len > 0 ? len : 1);
     s.W = (int)((p.total_tokens + s.len - 1) / s.len);

@@ -358,7 +358,7 @@ gdn_status run_step(const gdn_conv_problem &p, const void *x, const float *weigh
     auto blocks = [&](int run) {
         return (int64_t)a.n_chan * ((p.num_seqs + (int64_t)run * ty - 1) / ((int64_t)run * ty));
     };
-    a.run = 4;
+    a.run = 8;
     while (a.run > 1 && blocks(a.run) < 4 * kGridSms) a.run /= 2;
     if (blocks(a.run) > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     gdn_short_conv_step_kernel<T, V, K>
