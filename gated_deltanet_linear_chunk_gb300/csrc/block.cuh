@@ -182,6 +182,18 @@ template <int BYTES> __device__ __forceinline__ void copy_async(void *smem, cons
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(gmem) : "memory");
 }
+// 16 bytes that are not read again soon.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
+}
+__device__ __forceinline__ void copy_async_once(void *smem, const void *gmem, uint64_t policy) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(to), "l"(gmem),
+                 "l"(policy)
+                 : "memory");
+}
 // The first `bytes` (2 or 4) of a 4-byte word; the rest of it becomes zero.
 __device__ __forceinline__ void copy_async_part(void *smem, const void *gmem, int bytes) {
     const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));

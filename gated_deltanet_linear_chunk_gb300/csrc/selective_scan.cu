@@ -525,6 +525,14 @@ __global__ void __launch_bounds__(kCombineThreads) gdn_scan_deferred_kernel(cons
 }
 
 // ------------------------------------------------------------ single tokens
+// One step reads and writes 8 bytes per state for one exponential and four
+// fp32 operations: bound by HBM bandwidth.  A block takes tiles of 128
+// channels, a thread per channel, and walks (tile, sequence) pairs; a pair's
+// states are contiguous in memory whatever S is.  They come into a ring in
+// shared memory by asynchronous copies, some pairs ahead and without
+// registers; each thread updates its channel's states there, and the block
+// writes them back in order.  The decay rates stay in registers while the tile
+// does.  Every block of one wave takes the same number of pairs.
 constexpr int kStepThreads = 128;
 
 template <typename T> struct ScanStepArgs {
@@ -533,132 +541,174 @@ template <typename T> struct ScanStepArgs {
     T *out;
     float *next;
     int N, D, S, per_group;
-    int tiles, run;                 // warps' channel tiles per group, sequences per warp
+    int tiles;               // of kStepThreads channels per group
+    int64_t pairs, run;      // (tile, sequence) pairs, and how many per block
     int64_t xs, dts, bs, cs, zs, os;
-    bool softplus, bc_words;        // bc_words: B and C allow four elements at a time
+    bool softplus, words;    // words: every pair's states are whole 16-byte words
 };
 
-// Four elements, aligned to four.
-__device__ __forceinline__ void load4(const float *p, float *r) { Vec<float, 4>::load(p).to(r); }
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float *r) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    Vec<__nv_bfloat16, 2>{w.x}.to(r);
-    Vec<__nv_bfloat16, 2>{w.y}.to(r + 2);
+// NS: the states padded to a power of two, at least 4.
+// Stages of the ring, and blocks per SM: 64 KB in flight or more.  (256 x 6144,
+// 16 states: four stages of six blocks 42 us, three of eight 46, six of four
+// 48, two of ten 45; 32 states: three of four 41, four of three 44; 64
+// states: two of three 41, three of two 47.)
+template <int NS> constexpr int kStepStages = NS <= 16 ? 4 : NS == 32 ? 3 : 2;
+template <int NS> constexpr int kStepBlocks = NS <= 8 ? 8 : NS == 16 ? 6 : NS == 32 ? 4 : 3;
+template <int NS> constexpr size_t step_bytes() {
+    return (size_t)kStepStages<NS> * kStepThreads * NS * sizeof(float) + 4 * NS * sizeof(float);
 }
 
-// A warp takes Q R channels of one group through `run` sequences.  L lanes
-// share a channel, each with V consecutive states (J times L V apart); the
-// channels pass in Q rounds of R = 32 / L.  Lane i forms the step of channel
-// i, the rounds fetch it from there, and return their sums there.  The decay
-// rates stay in registers for all sequences; the next sequence's states and
-// inputs are loaded before the one at hand is computed, so that half the
-// state traffic is in flight at all times.
-template <typename T, int V, int L, int J> struct StepTile {
-    static constexpr int R = 32 / L;
-    static constexpr int Q = L < 4 ? L : 4;
-    static constexpr int kChannelsPerWarp = Q * R;
-};
+// QUADS: S is a multiple of four, A aligned to it: states four at a time.
+template <typename T, int NS, bool QUADS>
+__global__ void __launch_bounds__(kStepThreads, kStepBlocks<NS>)
+gdn_scan_step_kernel(const ScanStepArgs<T> a) {
+    constexpr int STAGES = kStepStages<NS>;
+    extern __shared__ __align__(16) float ring[];  // [stage][channel][S]
+    float *bc = ring + STAGES * kStepThreads * NS;  // [pair parity][B, C][NS]
+    const int t = threadIdx.x;
+    const int64_t first = (int64_t)blockIdx.x * a.run, last = min(first + a.run, a.pairs);
 
-template <typename T, int V, int L, int J>
-__global__ void __launch_bounds__(kStepThreads) gdn_scan_step_kernel(const ScanStepArgs<T> a) {
-    using Tile = StepTile<T, V, L, J>;
-    constexpr int R = Tile::R, Q = Tile::Q, W = Tile::kChannelsPerWarp;
-    const int lane = threadIdx.x & 31, part = lane % L;
-    const int g = blockIdx.x / a.tiles, in_group = (blockIdx.x % a.tiles) * W;
-    const int d0 = g * a.per_group + in_group, count = min(W, a.per_group - in_group);
-    const int dl = d0 + min(lane, count - 1);  // this lane's channel
-    const int64_t first = ((int64_t)blockIdx.y * (kStepThreads / 32) + threadIdx.x / 32) * a.run;
-    const int64_t last = min(first + a.run, (int64_t)a.N);
-    if (first >= last) return;
-    const float bias = a.bias ? a.bias[dl] : 0.f, skip = a.skip ? a.skip[dl] : 0.f;
-
-    // What a sequence brings: loaded one ahead.
+    // A pair's place: pairs go through all sequences of a tile in turn.
+    struct Place {
+        int64_t n;
+        int tile, g, d0, count;
+    };
+    auto place = [&](int64_t n, int tile) {
+        const int in_group = (tile % a.tiles) * kStepThreads, g = tile / a.tiles;
+        return Place{n, tile, g, g * a.per_group + in_group,
+                     min(kStepThreads, a.per_group - in_group)};
+    };
+    auto after = [&](Place p) {
+        if (p.n + 1 == a.N) return place(0, p.tile + 1);
+        ++p.n;
+        return p;
+    };
+    // The states of pair i, at p, on their way to its stage.  (They are read
+    // and written once: neither should push anything out of L2.)
+    const uint64_t once = evict_first_policy();
+    auto copy = [&](int64_t i, const Place &p) {
+        if (i < last) {
+            const float *from = a.state + (p.n * a.D + p.d0) * a.S;
+            float *to = ring + (i % STAGES) * (kStepThreads * NS);
+            const int n = p.count * a.S;
+            if (a.words) {
+                for (int k = 4 * t; k < n; k += 4 * kStepThreads)
+                    copy_async_once(to + k, from + k, once);
+            } else {
+                for (int k = t; k < n; k += kStepThreads) copy_async<4>(to + k, from + k);
+            }
+        }
+        copies_commit();
+    };
+    // A pair's other inputs: this thread's channel's, and one B or C.
     struct Inputs {
-        float dt, x, z, B[J][V], C[J][V];
-        Vec<float, V> h[Q][J];
+        float dt, x, z, bc;
     };
-    auto fetch = [&](Inputs &f, int64_t n) {
+    auto fetch = [&](Inputs &f, const Place &p) {
+        const int d = p.d0 + min(t, p.count - 1);
+        f.dt = to_f32(a.dt[p.n * a.dts + d]);
+        f.x = to_f32(a.x[p.n * a.xs + d]);
+        f.z = a.z ? to_f32(a.z[p.n * a.zs + d]) : 0.f;
+        // Threads 0 .. NS - 1 take B, the next NS take C.
+        const int k = t % NS;
+        f.bc = 0.f;
+        if (t < 2 * NS && k < a.S)
+            f.bc = to_f32(t < NS ? a.B[p.n * a.bs + p.g * a.S + k]
+                                    : a.C[p.n * a.cs + p.g * a.S + k]);
+    };
+
+    Place at = place(first % a.N, (int)(first / a.N)), ahead = at;
 #pragma unroll
-        for (int q = 0; q < Q; ++q)
+    for (int k = 0; k < STAGES - 1; ++k) {
+        copy(first + k, ahead);
+        ahead = after(ahead);
+    }
+    Inputs in;
+    fetch(in, at);
+    const int quads = a.S / 4;
+    // Where a thread starts in its channel's quads, so that the eight threads
+    // of a 16-byte access phase hit distinct banks whatever power of two
+    // divides the channels' distance.
+    const int share = min(quads & -quads, 8);
+    const int turn = QUADS ? t / (8 / share) % share : 0;
+    auto quad = [&](int j) { return j + turn < quads ? j + turn : j + turn - quads; };
+    float A[NS], bias = 0.f, skip = 0.f;
+    int tile = -1;
+    for (int64_t i = first; i < last; ++i) {
+        const bool mine = t < at.count;
+        if (at.tile != tile) {
+            tile = at.tile;
+            const int d = at.d0 + min(t, at.count - 1);
+            const float *from = a.A + (int64_t)d * a.S;
+            bias = a.bias ? a.bias[d] : 0.f;
+            skip = a.skip ? a.skip[d] : 0.f;
+            if (QUADS) {
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int ch = q * R + lane / L, k = (j * L + part) * V;
-                f.h[q][j] = Vec<float, V>::zero();
-                if (ch < count && k < a.S)
-                    f.h[q][j] = Vec<float, V>::load(a.state + (n * a.D + d0 + ch) * a.S + k);
-            }
-        f.dt = to_f32(a.dt[n * a.dts + dl]);
-        f.x = to_f32(a.x[n * a.xs + dl]);
-        f.z = a.z ? to_f32(a.z[n * a.zs + dl]) : 0.f;
+                for (int j = 0; j < NS / 4; ++j)
+                    if (j < quads) Vec<float, 4>::load(from + 4 * quad(j)).to(A + 4 * j);
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int k = (j * L + part) * V;
+                for (int k = 0; k < NS; ++k) A[k] *= kLog2e;
+            } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) f.B[j][i] = f.C[j][i] = 0.f;
-            if (k < a.S) {
-                const T *b = a.B + n * a.bs + g * a.S + k, *c = a.C + n * a.cs + g * a.S + k;
-                if (V == 4 && a.bc_words) {
-                    load4(b, f.B[j]);
-                    load4(c, f.C[j]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        f.B[j][i] = to_f32(b[i]);
-                        f.C[j][i] = to_f32(c[i]);
-                    }
-                }
+                for (int k = 0; k < NS; ++k) A[k] = k < a.S ? kLog2e * from[k] : 0.f;
             }
         }
-    };
-    Inputs cur, ahead;
-    fetch(cur, first);
-    float A[Q][J][V];
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int ch = q * R + lane / L, k = (j * L + part) * V;
-            Vec<float, V> w = Vec<float, V>::zero();
-            if (ch < count && k < a.S)
-                w = Vec<float, V>::load(a.A + (int64_t)(d0 + ch) * a.S + k);
-            w.to(A[q][j]);
-#pragma unroll
-            for (int i = 0; i < V; ++i) A[q][j][i] *= kLog2e;
-        }
-    for (int64_t n = first; n < last; ++n) {
-        if (n + 1 < last) fetch(ahead, n + 1);
-        float s = cur.dt + bias;
+        float *both = bc + (i & 1) * (2 * NS);
+        if (t < 2 * NS) both[t] = in.bc;
+        const Inputs now = in;
+        copies_wait<STAGES - 2>();
+        __syncthreads();  // the pair's states are here, the pair before is written back
+        copy(i + STAGES - 1, ahead);
+        ahead = after(ahead);
+        const Place next = after(at);
+        if (i + 1 < last) fetch(in, next);
+
+        float s = now.dt + bias;
         if (a.softplus) s = softplus(s);
-        float sum = 0.f;  // this lane's channel's
+        const float u = s * now.x;
+        float y = 0.f;
+        float *stage = ring + (i % STAGES) * (kStepThreads * NS);
+        float *own = stage + t * a.S;
+        if (mine) {
+            if (QUADS) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const int ch = q * R + lane / L;
-            const float sc = __shfl_sync(0xffffffffu, s, ch);
-            const float uc = sc * __shfl_sync(0xffffffffu, cur.x, ch);
-            float y = 0.f;
+                for (int j = 0; j < NS / 4; ++j) {
+                    if (j >= quads) break;
+                    const int k = 4 * quad(j);
+                    float h[4], b[4], c[4];
+                    Vec<float, 4>::load(own + k).to(h);
+                    Vec<float, 4>::load(both + k).to(b);
+                    Vec<float, 4>::load(both + NS + k).to(c);
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int k = (j * L + part) * V;
-                float h[V];
-                cur.h[q][j].to(h);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    h[i] = fmaf(ex2(sc * A[q][j][i]), h[i], uc * cur.B[j][i]);
-                    y = fmaf(cur.C[j][i], h[i], y);
+                    for (int v = 0; v < 4; ++v) {
+                        h[v] = fmaf(ex2(s * A[4 * j + v]), h[v], u * b[v]);
+                        y = fmaf(c[v], h[v], y);
+                    }
+                    Vec<float, 4>::from(h).store(own + k);
                 }
-                if (ch < count && k < a.S)
-                    Vec<float, V>::from(h).store(a.next + (n * a.D + d0 + ch) * a.S + k);
-            }
+            } else {
 #pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-            // Channel ch's sum goes to lane ch.
-            const float back = __shfl_sync(0xffffffffu, y, (lane % R) * L);
-            if (lane / R == q) sum = back;
+                for (int k = 0; k < NS; ++k) {
+                    if (k >= a.S) break;
+                    const float h = fmaf(ex2(s * A[k]), own[k], u * both[k]);
+                    y = fmaf(both[NS + k], h, y);
+                    own[k] = h;
+                }
+            }
+            y = fmaf(skip, now.x, y);
+            if (a.z) y *= silu(now.z);
+            a.out[at.n * a.os + at.d0 + t] = from_f32<T>(y);
         }
-        sum = fmaf(skip, cur.x, sum);
-        if (a.z) sum *= silu(cur.z);
-        if (lane < count) a.out[n * a.os + dl] = from_f32<T>(sum);
-        cur = ahead;
+        __syncthreads();
+        float *to = a.next + (at.n * a.D + at.d0) * a.S;
+        const int n = at.count * a.S;
+        if (a.words) {
+            for (int k = 4 * t; k < n; k += 4 * kStepThreads)
+                __stcs(reinterpret_cast<float4 *>(to + k), Vec<float, 4>::load(stage + k).w);
+        } else {
+            for (int k = t; k < n; k += kStepThreads) __stcs(to + k, stage[k]);
+        }
+        at = next;
     }
 }
 
@@ -724,19 +774,19 @@ template <typename T> ScanArgs<T> scan_args(const gdn_ssm_problem &p, const Scan
     return a;
 }
 
-// Blocks of full size need more shared memory than a kernel has by default;
+// Blocks of full size need more shared memory than a kernel has by default:
 // the limit is raised once per device and variant.
-template <typename T, int NS, bool ODD> bool scan_shared_memory() {
-    static std::atomic<bool> done[kMaxDevices];
+bool raise_shared_memory(std::atomic<bool> (&done)[kMaxDevices],
+                         std::initializer_list<const void *> kernels,
+                         std::initializer_list<size_t> bytes) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
     if (done[dev].load(std::memory_order_acquire)) return true;
-    const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    if (cudaFuncSetAttribute(gdn_scan_kernel<T, NS, true, ODD>, attr,
-                             (int)ScanTiles<T, NS, true, ODD>::bytes(kMaxThreads)) != cudaSuccess ||
-        cudaFuncSetAttribute(gdn_scan_kernel<T, NS, false, ODD>, attr,
-                             (int)ScanTiles<T, NS, false, ODD>::bytes(kMaxThreads)) != cudaSuccess)
-        return false;
+    auto size = bytes.begin();
+    for (const void *k : kernels)
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)*size++) != cudaSuccess)
+            return false;
     done[dev].store(true, std::memory_order_release);
     return true;
 }
@@ -747,7 +797,14 @@ gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cuda
     const int64_t ds = (int64_t)a.D * a.S;
     const size_t in_bytes = ScanTiles<T, NS, false, ODD>::bytes(pl.threads);
     const size_t out_bytes = ScanTiles<T, NS, true, ODD>::bytes(pl.threads);
-    if (!scan_shared_memory<T, NS, ODD>()) return GDN_ERR_CUDA;
+    static std::atomic<bool> done[kMaxDevices];
+    if (!raise_shared_memory(
+            done,
+            {reinterpret_cast<const void *>(gdn_scan_kernel<T, NS, false, ODD>),
+             reinterpret_cast<const void *>(gdn_scan_kernel<T, NS, true, ODD>)},
+            {ScanTiles<T, NS, false, ODD>::bytes(kMaxThreads),
+             ScanTiles<T, NS, true, ODD>::bytes(kMaxThreads)}))
+        return GDN_ERR_CUDA;
     // With several windows the second and third launch may start while the
     // one before ends; they wait for it before they touch the carries.
     cudaLaunchAttribute attr;
@@ -840,22 +897,25 @@ gdn_status scan_typed(const gdn_ssm_problem &p, const void *x, const void *dt, c
     return GDN_ERR_UNSUPPORTED;
 }
 
-template <typename T, int V, int L, int J>
-void run_scan_step(ScanStepArgs<T> &a, cudaStream_t stream) {
-    constexpr int W = StepTile<T, V, L, J>::kChannelsPerWarp;
-    a.tiles = (a.per_group + W - 1) / W;
-    const int64_t tiles = (int64_t)a.tiles * (a.D / a.per_group);
-    auto rows = [&](int run) {
-        const int per = run * (kStepThreads / 32);
-        return ((int64_t)a.N + per - 1) / per;
-    };
-    // Up to four sequences per warp, while two waves of five blocks per SM
-    // are left.
-    a.run = 4;
-    while (a.run > 1 && tiles * rows(a.run) < 10 * kGridSms) a.run /= 2;
-    while (rows(a.run) > 65535) a.run *= 2;
-    gdn_scan_step_kernel<T, V, L, J>
-        <<<dim3((unsigned)tiles, (unsigned)rows(a.run)), kStepThreads, 0, stream>>>(a);
+template <typename T, int NS, bool QUADS>
+gdn_status run_scan_step(ScanStepArgs<T> &a, cudaStream_t stream) {
+    static std::atomic<bool> done[kMaxDevices];
+    if (!raise_shared_memory(done, {reinterpret_cast<const void *>(
+                                       gdn_scan_step_kernel<T, NS, QUADS>)},
+                             {step_bytes<NS>()}))
+        return GDN_ERR_CUDA;
+    a.tiles = (a.per_group + kStepThreads - 1) / kStepThreads;
+    a.pairs = (int64_t)a.tiles * (a.D / a.per_group) * a.N;
+    const int64_t blocks = kStepBlocks<NS> * kGridSms;
+    a.run = (a.pairs + blocks - 1) / blocks;
+    gdn_scan_step_kernel<T, NS, QUADS>
+        <<<(unsigned)((a.pairs + a.run - 1) / a.run), kStepThreads, step_bytes<NS>(), stream>>>(a);
+    return launch_status();
+}
+
+template <typename T, int NS> gdn_status run_scan_step(ScanStepArgs<T> &a, cudaStream_t stream) {
+    return a.S % 4 == 0 && aligned16(a.A) ? run_scan_step<T, NS, true>(a, stream)
+                                          : run_scan_step<T, NS, false>(a, stream);
 }
 
 template <typename T>
@@ -886,26 +946,15 @@ gdn_status scan_step_typed(const gdn_ssm_problem &p, const void *x, const void *
     a.zs = p.z_stride;
     a.os = p.out_stride;
     a.softplus = p.dt_softplus != 0;
-    const bool wide = p.state_dim % 4 == 0 && aligned16(state) && aligned16(next) && aligned16(A);
-    a.bc_words = ((reinterpret_cast<uintptr_t>(B) | reinterpret_cast<uintptr_t>(C) |
-                   (uint64_t)p.b_stride * sizeof(T) | (uint64_t)p.c_stride * sizeof(T)) %
-                  (4 * sizeof(T))) == 0;
+    // Tiles start at multiples of 128 channels in a group: whole words where
+    // a group's states are.
+    a.words = (int64_t)a.per_group * a.S % 4 == 0 && aligned16(state) && aligned16(next);
     const int S = p.state_dim;
-    if (wide) {
-        if (S <= 4) run_scan_step<T, 4, 1, 1>(a, stream);
-        else if (S <= 8) run_scan_step<T, 4, 2, 1>(a, stream);
-        else if (S <= 16) run_scan_step<T, 4, 4, 1>(a, stream);
-        else if (S <= 32) run_scan_step<T, 4, 8, 1>(a, stream);
-        else run_scan_step<T, 4, 16, 1>(a, stream);
-    } else {
-        if (S <= 1) run_scan_step<T, 1, 1, 1>(a, stream);
-        else if (S <= 4) run_scan_step<T, 1, 4, 1>(a, stream);
-        else if (S <= 8) run_scan_step<T, 1, 8, 1>(a, stream);
-        else if (S <= 16) run_scan_step<T, 1, 16, 1>(a, stream);
-        else if (S <= 32) run_scan_step<T, 1, 16, 2>(a, stream);
-        else run_scan_step<T, 1, 16, 4>(a, stream);
-    }
-    return launch_status();
+    if (S <= 4) return run_scan_step<T, 4>(a, stream);
+    if (S <= 8) return run_scan_step<T, 8>(a, stream);
+    if (S <= 16) return run_scan_step<T, 16>(a, stream);
+    if (S <= 32) return run_scan_step<T, 32>(a, stream);
+    return run_scan_step<T, 64>(a, stream);
 }
 
 }  // namespace
