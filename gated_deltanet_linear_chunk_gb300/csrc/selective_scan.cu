@@ -73,7 +73,7 @@ template <typename T> struct ScanArgs {
     int per_group, tiles;  // channels per group, blocks per group
     int W, len;            // windows, tokens per window
     int64_t xs, dts, bs, cs, zs, os;
-    int in_word, bc_word;  // CopyWord of x, dt, z and of B, C
+    int bc_word;  // CopyWord of B and C
     bool softplus, defer;
     bool out_own;      // out's rows are aligned to a thread's channels
     bool state_words;  // A, the states and the workspace allow 16-byte words
@@ -222,19 +222,33 @@ __device__ __forceinline__ void copy_rows(T *dst, int pitch, const T *src, int64
     }
 }
 
-// The same for 16-bit rows that may start at odd elements: element c of a
-// row goes to place c + odd(row), so that both sides of the copies are whole
-// 4-byte words.  A row's first element, where odd, is left to copy_first.
+// Elements between p and the 16-byte word that holds it.
+template <typename T> __device__ __forceinline__ int shift_of(const T *p) {
+    return (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & (kWide<T> - 1);
+}
+
+// The same for rows at any alignment: element c of a row goes to place
+// c + shift_of(row), so that all but the row's ends are copied in whole
+// 16-byte words, the ends in 4-byte ones.  (A first 16-bit element in the
+// upper half of its 4-byte word is left to copy_first.)
 template <typename T>
-__device__ __forceinline__ void copy_rows_odd(T *dst, int pitch, const T *src, int64_t stride,
-                                              int rows, int cols) {
+__device__ __forceinline__ void copy_rows_shifted(T *dst, int pitch, const T *src, int64_t stride,
+                                                  int rows, int cols) {
+    constexpr int V = kWide<T>, E = 4 / (int)sizeof(T);  // elements per word
     const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
     for (int r = threadIdx.x / 32; r < rows; r += warps) {
         const T *from = src + r * stride;
-        const int o = odd(from);
+        const int o = shift_of(from), lead = min((V - o) % V, cols);
         T *to = dst + r * pitch + o;
-        for (int c = o + 2 * lane; c < cols; c += 64)
-            copy_async_part(to + c, from + c, c + 1 < cols ? 4 : 2);
+        const int words = (cols - lead) / V, tail = lead + words * V;
+        for (int k = lane; k < words; k += 32)
+            copy_async<16>(to + lead + k * V, from + lead + k * V);
+        // Lanes 0 to 3 take the row's start, 4 to 7 its end.
+        const int c = lane < 4 ? o % E + lane * E : tail + (lane - 4) * E;
+        if (lane < 8 && c < (lane < 4 ? lead : cols)) {
+            if constexpr (E == 1) copy_async<4>(to + c, from + c);
+            else copy_async_part(to + c, from + c, c + 1 < cols ? 4 : 2);
+        }
     }
 }
 template <typename T, int K>
@@ -250,14 +264,14 @@ __device__ __forceinline__ void copy_first(T *const (&dst)[K], int pitch, const 
         }
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (is[k]) dst[k][r * pitch + 1] = v[k];
+            if (is[k]) dst[k][r * pitch + shift_of(src[k] + r * stride[k])] = v[k];
     }
 }
 
 // Shared memory of a block: kTiles tiles of x, dt (and z) and of B (and C) as
 // they lie in global memory, and one of B (and C) as fp32, zero past the last
-// state.  ODD: rows of x, dt and z may start at odd 16-bit elements.
-template <typename T, int NS, bool OUT, bool ODD> struct ScanTiles {
+// state.  SHIFT: rows of x, dt and z start anywhere.
+template <typename T, int NS, bool OUT, bool SHIFT> struct ScanTiles {
     static constexpr int CH = kChannels<NS>;
     static constexpr int kTile = kTileOf<T, CH>, kTiles = kTilesOf<T, CH>;
     static constexpr int kIn = OUT ? 3 : 2, kBC = OUT ? 2 : 1;
@@ -267,7 +281,7 @@ template <typename T, int NS, bool OUT, bool ODD> struct ScanTiles {
     int width;     // channels per block
     int pitch;     // elements between rows of `ins`
     __device__ ScanTiles(char *smem, int threads) : width(threads * CH) {
-        pitch = width + (ODD ? 2 : 0);
+        pitch = width + (SHIFT ? kWide<T> : 0);
         bc = reinterpret_cast<float *>(smem);
         raws = reinterpret_cast<T *>(bc + kBC * kTile * NS);
         ins = raws + kTiles * kBC * kTile * NS;
@@ -278,7 +292,7 @@ template <typename T, int NS, bool OUT, bool ODD> struct ScanTiles {
     __device__ __forceinline__ T *in(int buf) const { return ins + buf * (kIn * kTile * pitch); }
     static size_t bytes(int threads) {
         return kBC * kTile * NS * (sizeof(float) + kTiles * sizeof(T)) +
-               kTiles * kIn * kTile * (threads * CH + (ODD ? 2 : 0)) * sizeof(T);
+               kTiles * kIn * kTile * (threads * CH + (SHIFT ? kWide<T> : 0)) * sizeof(T);
     }
     // Starts the copies of tokens [t, te) (one tile at most) of the block's
     // channels, d the first of `cols`.
@@ -292,14 +306,14 @@ template <typename T, int NS, bool OUT, bool ODD> struct ScanTiles {
 #pragma unroll
         for (int k = 0; k < kIn; ++k) {
             if (k == 2 && !a.z) break;
-            if (ODD) copy_rows_odd(dst[k], pitch, src[k], stride[k], rows, cols);
-            else copy_rows(dst[k], pitch, src[k], stride[k], rows, cols, a.in_word);
+            if (SHIFT) copy_rows_shifted(dst[k], pitch, src[k], stride[k], rows, cols);
+            else copy_rows(dst[k], pitch, src[k], stride[k], rows, cols, kCopy16);
         }
         copy_rows(raw(buf), NS, a.B + t * a.bs + group * a.S, a.bs, rows, a.S, a.bc_word);
         if (OUT)
             copy_rows(raw(buf) + kTile * NS, NS, a.C + t * a.cs + group * a.S, a.cs, rows, a.S,
                       a.bc_word);
-        if (ODD) copy_first(dst, pitch, src, stride, rows);
+        if (SHIFT && sizeof(T) == 2) copy_first(dst, pitch, src, stride, rows);
     }
     // B and C of the tile that has arrived, to fp32.
     __device__ __forceinline__ void widen(const ScanArgs<T> &a, int buf) const {
@@ -309,25 +323,24 @@ template <typename T, int NS, bool OUT, bool ODD> struct ScanTiles {
 };
 
 
-// U tokens from t of tile `buf`, whose first token is t0.  `odds`: whether
-// the tile's first rows of x, dt and z are odd, in bits 0 to 2, and whether
-// their strides are, in bits 4 to 6.
-template <typename T, int NS, bool OUT, bool ODD, int U>
+// U tokens from t of tile `buf`, whose first token is t0.  A byte each for x,
+// dt and z: how far the tile's first row is shifted, and what a row adds.
+template <typename T, int NS, bool OUT, bool SHIFT, int U>
 __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS> &th,
-                                         const ScanTiles<T, NS, OUT, ODD> &tl, int buf, int t0,
-                                         int t, int odds) {
+                                         const ScanTiles<T, NS, OUT, SHIFT> &tl, int buf, int t0,
+                                         int t, uint32_t shifts, uint32_t steps) {
     constexpr int CH = kChannels<NS>, kTile = kTileOf<T, CH>;
     float y[U][CH];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int r = t - t0 + u;
         const T *in = tl.in(buf) + r * tl.pitch + th.col;
-        const int o = ODD ? odds ^ ((odds >> 4) & -(r & 1)) : 0;
+        const uint32_t o = SHIFT ? shifts + r * steps : 0;
         auto own = [&](int k, float *v) {
             const T *p = in + k * kTile * tl.pitch;
-            if (ODD) {
+            if (SHIFT) {
 #pragma unroll
-                for (int c = 0; c < CH; ++c) v[c] = to_f32(p[c + ((o >> k) & 1)]);
+                for (int c = 0; c < CH; ++c) v[c] = to_f32(p[c + (o >> (8 * k) & (kWide<T> - 1))]);
             } else {
                 Vec<T, CH>::load(p).to(v);
             }
@@ -348,7 +361,7 @@ __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS>
     }
     if (!OUT) return;
     T *out = a.out + t * a.os + th.d;
-    if (!ODD && a.out_own) {
+    if (!SHIFT && a.out_own) {
 #pragma unroll
         for (int u = 0; u < U; ++u, out += a.os)
             if (th.valid) Vec<T, CH>::from(y[u]).store(out);
@@ -375,11 +388,11 @@ __device__ void copy_empty(const ScanArgs<T> &a, int first, int step, int d0, in
     }
 }
 
-template <typename T, int NS, bool OUT, bool ODD>
+template <typename T, int NS, bool OUT, bool SHIFT>
 __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(const ScanArgs<T> a) {
     constexpr int CH = kChannels<NS>, kTile = kTileOf<T, CH>, kTiles = kTilesOf<T, CH>;
     extern __shared__ __align__(16) char smem[];
-    const ScanTiles<T, NS, OUT, ODD> tl(smem, blockDim.x);
+    const ScanTiles<T, NS, OUT, SHIFT> tl(smem, blockDim.x);
     const int group = blockIdx.x / a.tiles, in_group0 = (blockIdx.x % a.tiles) * tl.width;
     const int w = blockIdx.y, d0 = group * a.per_group + in_group0;
     const int cols = min(tl.width, a.per_group - in_group0);
@@ -421,18 +434,20 @@ __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(co
         __syncthreads();  // the tile has arrived, and the one before is done with
         tl.widen(a, buf);
         fetch(tile + kTiles - 1);
-        int odds = 0;
-        if (ODD)
-            odds = odd(a.x + tt * a.xs + d0) | odd(a.dt + tt * a.dts + d0) << 1 |
-                   odd(a.z + tt * a.zs + d0) << 2 | (int)(a.xs & 1) << 4 |
-                   (int)(a.dts & 1) << 5 | (int)(a.zs & 1) << 6;
+        uint32_t shifts = 0, steps = 0;
+        if (SHIFT) {
+            constexpr int M = kWide<T> - 1;
+            shifts = shift_of(a.x + tt * a.xs + d0) | shift_of(a.dt + tt * a.dts + d0) << 8 |
+                     shift_of(a.z + tt * a.zs + d0) << 16;
+            steps = (a.xs & M) | (a.dts & M) << 8 | (a.zs & M) << 16;
+        }
         __syncthreads();
         int t = tt;
         while (t < te) {
             const int e = min(te, s.end);
             for (; t + kUnroll <= e; t += kUnroll)
-                scan_run<T, NS, OUT, ODD, kUnroll>(a, th, tl, buf, tt, t, odds);
-            for (; t < e; ++t) scan_run<T, NS, OUT, ODD, 1>(a, th, tl, buf, tt, t, odds);
+                scan_run<T, NS, OUT, SHIFT, kUnroll>(a, th, tl, buf, tt, t, shifts, steps);
+            for (; t < e; ++t) scan_run<T, NS, OUT, SHIFT, 1>(a, th, tl, buf, tt, t, shifts, steps);
             if (OUT && t == s.end) {
                 // A final state written over the initial one must wait for
                 // the windows that read it: it takes the place of the state
@@ -791,19 +806,19 @@ bool raise_shared_memory(std::atomic<bool> (&done)[kMaxDevices],
     return true;
 }
 
-template <typename T, int NS, bool ODD>
+template <typename T, int NS, bool SHIFT>
 gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cudaStream_t stream) {
     const unsigned blocks = (unsigned)(a.G * pl.tiles);
     const int64_t ds = (int64_t)a.D * a.S;
-    const size_t in_bytes = ScanTiles<T, NS, false, ODD>::bytes(pl.threads);
-    const size_t out_bytes = ScanTiles<T, NS, true, ODD>::bytes(pl.threads);
+    const size_t in_bytes = ScanTiles<T, NS, false, SHIFT>::bytes(pl.threads);
+    const size_t out_bytes = ScanTiles<T, NS, true, SHIFT>::bytes(pl.threads);
     static std::atomic<bool> done[kMaxDevices];
     if (!raise_shared_memory(
             done,
-            {reinterpret_cast<const void *>(gdn_scan_kernel<T, NS, false, ODD>),
-             reinterpret_cast<const void *>(gdn_scan_kernel<T, NS, true, ODD>)},
-            {ScanTiles<T, NS, false, ODD>::bytes(kMaxThreads),
-             ScanTiles<T, NS, true, ODD>::bytes(kMaxThreads)}))
+            {reinterpret_cast<const void *>(gdn_scan_kernel<T, NS, false, SHIFT>),
+             reinterpret_cast<const void *>(gdn_scan_kernel<T, NS, true, SHIFT>)},
+            {ScanTiles<T, NS, false, SHIFT>::bytes(kMaxThreads),
+             ScanTiles<T, NS, true, SHIFT>::bytes(kMaxThreads)}))
         return GDN_ERR_CUDA;
     // With several windows the second and third launch may start while the
     // one before ends; they wait for it before they touch the carries.
@@ -815,7 +830,7 @@ gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cuda
     cfg.attrs = &attr;
     cfg.numAttrs = pl.W > 1 ? 1 : 0;
     if (pl.W > 1) {
-        gdn_scan_kernel<T, NS, false, ODD>
+        gdn_scan_kernel<T, NS, false, SHIFT>
             <<<dim3(blocks, pl.W - 1), pl.threads, in_bytes, stream>>>(a);
         if (launch_status() != GDN_OK) return GDN_ERR_CUDA;
         // Eight windows are loaded at once: more than a few rounds of them
@@ -834,7 +849,7 @@ gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cuda
         cfg.gridDim = dim3(blocks, rows);
         cfg.blockDim = dim3(pl.threads);
         cfg.dynamicSmemBytes = out_bytes;
-        if (cudaLaunchKernelEx(&cfg, gdn_scan_kernel<T, NS, true, ODD>, a) != cudaSuccess)
+        if (cudaLaunchKernelEx(&cfg, gdn_scan_kernel<T, NS, true, SHIFT>, a) != cudaSuccess)
             return GDN_ERR_CUDA;
     }
     if (a.defer && pl.W > 1)
@@ -845,10 +860,10 @@ gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cuda
 }
 
 template <typename T, int NS>
-gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cudaStream_t stream) {
-    if constexpr (sizeof(T) == 2)
-        if (a.in_word == kCopyElement) return run_scan<T, NS, true>(pl, a, empties, stream);
-    return run_scan<T, NS, false>(pl, a, empties, stream);
+gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool shifted, bool empties,
+                    cudaStream_t stream) {
+    return shifted ? run_scan<T, NS, true>(pl, a, empties, stream)
+                   : run_scan<T, NS, false>(pl, a, empties, stream);
 }
 
 template <typename T>
@@ -879,7 +894,8 @@ gdn_status scan_typed(const gdn_ssm_problem &p, const void *x, const void *dt, c
         for (int64_t n : sizes) bits |= (uint64_t)n * sizeof(T);
         return bits % 16 == 0 ? kCopy16 : bits % 4 == 0 ? kCopy4 : kCopyElement;
     };
-    a.in_word = word({x, dt, z}, {p.x_stride, p.dt_stride, z ? p.z_stride : 0, a.per_group});
+    const bool shifted =
+        word({x, dt, z}, {p.x_stride, p.dt_stride, z ? p.z_stride : 0, a.per_group}) != kCopy16;
     a.bc_word = word({B, C}, {p.b_stride, p.c_stride, p.state_dim});
     a.state_words = p.state_dim % 4 == 0 && aligned16(A) && aligned16(init) && aligned16(fin);
     const int ch = channels_per_thread(pl.ns);
@@ -888,11 +904,11 @@ gdn_status scan_typed(const gdn_ssm_problem &p, const void *x, const void *dt, c
     // Only a batch of several sequences (or of no tokens) has empty ones.
     const bool empties = fin && fin != init && (p.num_seqs > 1 || p.total_tokens == 0);
     switch (pl.ns) {
-        case 4: return run_scan<T, 4>(pl, a, empties, stream);
-        case 8: return run_scan<T, 8>(pl, a, empties, stream);
-        case 16: return run_scan<T, 16>(pl, a, empties, stream);
-        case 32: return run_scan<T, 32>(pl, a, empties, stream);
-        case 64: return run_scan<T, 64>(pl, a, empties, stream);
+        case 4: return run_scan<T, 4>(pl, a, shifted, empties, stream);
+        case 8: return run_scan<T, 8>(pl, a, shifted, empties, stream);
+        case 16: return run_scan<T, 16>(pl, a, shifted, empties, stream);
+        case 32: return run_scan<T, 32>(pl, a, shifted, empties, stream);
+        case 64: return run_scan<T, 64>(pl, a, shifted, empties, stream);
     }
     return GDN_ERR_UNSUPPORTED;
 }
