@@ -260,15 +260,26 @@ gdn_status launch_short_conv_step(const gdn_conv_problem &p, const void *x, cons
                                   const float *bias, const void *state, void *out, void *next,
                                   cudaStream_t stream);
 size_t scan_workspace_size(const gdn_ssm_problem &p);
-gdn_status launch_selective_scan(const gdn_ssm_problem &p, const void *x, const void *dt,
-                                 const float *A, const void *B, const void *C, const float *skip,
-                                 const void *z, const float *bias, const int32_t *cu,
-                                 const float *init, void *out, float *fin, cudaStream_t stream);
-gdn_status launch_selective_scan_step(const gdn_ssm_problem &p, const void *x, const void *dt,
+gdn_status launch_selective_scan_bf16(const gdn_ssm_problem &p, const void *x, const void *dt,
                                       const float *A, const void *B, const void *C,
                                       const float *skip, const void *z, const float *bias,
-                                      const float *state, void *out, float *next,
+                                      const int32_t *cu, const float *init, void *out, float *fin,
                                       cudaStream_t stream);
+gdn_status launch_selective_scan_f32(const gdn_ssm_problem &p, const void *x, const void *dt,
+                                     const float *A, const void *B, const void *C,
+                                     const float *skip, const void *z, const float *bias,
+                                     const int32_t *cu, const float *init, void *out, float *fin,
+                                     cudaStream_t stream);
+gdn_status launch_selective_scan_step_bf16(const gdn_ssm_problem &p, const void *x,
+                                           const void *dt, const float *A, const void *B,
+                                           const void *C, const float *skip, const void *z,
+                                           const float *bias, const float *state, void *out,
+                                           float *next, cudaStream_t stream);
+gdn_status launch_selective_scan_step_f32(const gdn_ssm_problem &p, const void *x, const void *dt,
+                                          const float *A, const void *B, const void *C,
+                                          const float *skip, const void *z, const float *bias,
+                                          const float *state, void *out, float *next,
+                                          cudaStream_t stream);
 gdn_status launch_norm_gate_residual(const gdn_norm_problem &p, const void *y,
                                      const float *weight, const void *gate, const void *residual,
                                      const float *next_weight, void *out, void *next,

@@ -128,8 +128,10 @@ GDN_API gdn_status gdn_selective_scan(const gdn_ssm_problem *problem, const void
     const size_t need = scan_workspace_size(p);
     if (need > 0 && (!p.workspace || p.workspace_bytes < need || !aligned16(p.workspace)))
         return GDN_ERR_WORKSPACE;
-    return launch_selective_scan(p, x, dt, A, B, C, skip, z, dt_bias, cu_seqlens, initial_state,
-                                 out, final_state, reinterpret_cast<cudaStream_t>(stream));
+    const auto launch =
+        p.dtype == GDN_BF16 ? launch_selective_scan_bf16 : launch_selective_scan_f32;
+    return launch(p, x, dt, A, B, C, skip, z, dt_bias, cu_seqlens, initial_state, out, final_state,
+                  reinterpret_cast<cudaStream_t>(stream));
 }
 
 GDN_API gdn_status gdn_selective_scan_step(const gdn_ssm_problem *problem, const void *x,
@@ -149,8 +151,10 @@ GDN_API gdn_status gdn_selective_scan_step(const gdn_ssm_problem *problem, const
     if (out == x || out == dt || out == z || out == B || out == C || out == state ||
         out == new_state)
         return GDN_ERR_INVALID_ARG;
-    return launch_selective_scan_step(p, x, dt, A, B, C, skip, z, dt_bias, state, out, new_state,
-                                      reinterpret_cast<cudaStream_t>(stream));
+    const auto launch =
+        p.dtype == GDN_BF16 ? launch_selective_scan_step_bf16 : launch_selective_scan_step_f32;
+    return launch(p, x, dt, A, B, C, skip, z, dt_bias, state, out, new_state,
+                  reinterpret_cast<cudaStream_t>(stream));
 }
 
 GDN_API gdn_status gdn_norm_gate_residual(const gdn_norm_problem *problem, const void *y,

@@ -1,5 +1,7 @@
-// selective_scan.cu -- selective state space scan over packed sequences, and
-// its single-token step (gdn_selective_scan, gdn_selective_scan_step).
+// selective_scan.cuh -- selective state space scan over packed sequences, and
+// its single-token step (gdn_selective_scan, gdn_selective_scan_step): the
+// kernels of one element type, instantiated in selective_scan_bf16.cu and
+// selective_scan_f32.cu.
 //
 // Per sequence and channel d, with S states and s_t = softplus(dt_t + bias):
 //
@@ -31,6 +33,8 @@
 //   3. the outputs of every window.
 // Windows of a fixed length balance exactly, and a window whose end falls
 // between two sequences skips step 1.
+#pragma once
+
 #include <atomic>
 #include <initializer_list>
 
@@ -739,10 +743,10 @@ struct ScanPlan {
 constexpr int kMinWindow = 8;
 
 // kChannels and kResident of the variant that runs.
-int channels_per_thread(int ns) { return ns <= 32 ? 2 : 1; }
-int resident_blocks(int ns) { return ns <= 16 ? 3 : 2; }
+inline int channels_per_thread(int ns) { return ns <= 32 ? 2 : 1; }
+inline int resident_blocks(int ns) { return ns <= 16 ? 3 : 2; }
 
-ScanPlan scan_plan(const gdn_ssm_problem &p) {
+inline ScanPlan scan_plan(const gdn_ssm_problem &p) {
     ScanPlan s;
     s.ns = 4;
     while (s.ns < p.state_dim) s.ns *= 2;
@@ -791,7 +795,7 @@ template <typename T> ScanArgs<T> scan_args(const gdn_ssm_problem &p, const Scan
 
 // Blocks of full size need more shared memory than a kernel has by default:
 // the limit is raised once per device and variant.
-bool raise_shared_memory(std::atomic<bool> (&done)[kMaxDevices],
+inline bool raise_shared_memory(std::atomic<bool> (&done)[kMaxDevices],
                          std::initializer_list<const void *> kernels,
                          std::initializer_list<size_t> bytes) {
     int dev = 0;
@@ -974,33 +978,4 @@ gdn_status scan_step_typed(const gdn_ssm_problem &p, const void *x, const void *
 }
 
 }  // namespace
-
-size_t scan_workspace_size(const gdn_ssm_problem &p) {
-    const ScanPlan pl = scan_plan(p);
-    if (pl.W <= 1) return 0;
-    return (size_t)(pl.W - 1) * p.channels * (p.state_dim + 1) * sizeof(float);
-}
-
-gdn_status launch_selective_scan(const gdn_ssm_problem &p, const void *x, const void *dt,
-                                 const float *A, const void *B, const void *C, const float *skip,
-                                 const void *z, const float *bias, const int32_t *cu,
-                                 const float *init, void *out, float *fin, cudaStream_t stream) {
-    return p.dtype == GDN_BF16
-               ? scan_typed<__nv_bfloat16>(p, x, dt, A, B, C, skip, z, bias, cu, init, out, fin,
-                                           stream)
-               : scan_typed<float>(p, x, dt, A, B, C, skip, z, bias, cu, init, out, fin, stream);
-}
-
-gdn_status launch_selective_scan_step(const gdn_ssm_problem &p, const void *x, const void *dt,
-                                      const float *A, const void *B, const void *C,
-                                      const float *skip, const void *z, const float *bias,
-                                      const float *state, void *out, float *next,
-                                      cudaStream_t stream) {
-    return p.dtype == GDN_BF16
-               ? scan_step_typed<__nv_bfloat16>(p, x, dt, A, B, C, skip, z, bias, state, out,
-                                                next, stream)
-               : scan_step_typed<float>(p, x, dt, A, B, C, skip, z, bias, state, out, next,
-                                        stream);
-}
-
 }  // namespace gdn
