@@ -12,6 +12,13 @@
 // on the fp32 sum of the first's result and the residual, before that sum is
 // rounded to out's type.  Rows of up to 32 lanes' words share a warp (a
 // power of two of lanes each, reduced by shuffles); longer rows take a block.
+// The grid is one wave that walks the rows, so the weights are read once per
+// block and a row's loads are on their way while the row before is reduced.
+//
+// Measured: 4000 rows of 6144, bf16 y and gate, fp32 residual, both norms, 58 us,
+// 87 % of the copy bandwidth (a block per row, weights read again for each: 90
+// us); 192000 rows of 128 with a SiLU gate 28 us, 77 % (39 us with a block per
+// eight rows: half of its instructions were addresses and weights).
 #include "block.cuh"
 
 namespace gdn {

@@ -33,6 +33,14 @@
 //   3. the outputs of every window.
 // Windows of a fixed length balance exactly, and a window whose end falls
 // between two sequences skips step 1.
+//
+// Measured, 4000 tokens of 6144 channels and 16 states in bf16: 77 us for step 1,
+// 10 for step 2, 112 for step 3, 188 in all (they overlap at their ends): 393 M
+// (token, channel, state) elements at 9 per clock and SM in step 3.  Issue
+// slots are 62 % busy, the fp32 pipe 53 %, the exponentials' pipe 56 and 43 %
+// (it takes 32 per clock and SM, fp32 128), memory 20 %: 223 instructions per
+// token of two channels, 96 of them the recurrence.  The bytes alone would
+// take 29 us, step 3's fp32 operations 42.
 #pragma once
 
 #include <atomic>
@@ -552,6 +560,9 @@ __global__ void __launch_bounds__(kCombineThreads) gdn_scan_deferred_kernel(cons
 // registers; each thread updates its channel's states there, and the block
 // writes them back in order.  The decay rates stay in registers while the tile
 // does.  Every block of one wave takes the same number of pairs.
+//
+// Measured: 256 sequences of 6144 channels and 16 states, 42 us, 75 % of the
+// copy bandwidth; 13 states 40 us (65 %), where lanes sharing a channel took 131.
 constexpr int kStepThreads = 128;
 
 template <typename T> struct ScanStepArgs {

@@ -15,6 +15,14 @@
 // rows per run, from L2).  The run's rows come through a ring in shared memory
 // by asynchronous copies, 8 tokens ahead: 16 KB in flight per block without
 // a register.  Channels go in pairs through the packed fp32 instructions.
+//
+// Measured: 4000 tokens of 10240 bf16 channels, width 4, SiLU, 34 us, 71 % of
+// the copy bandwidth; issue slots 46 % and memory 48 % busy, each group of
+// tokens waiting for its copies and then computing.  (Rows loaded into
+// registers four ahead took 49 us: 136 registers, 24 KB in flight per SM.  With
+// runs of 32 tokens, 1.6 waves of blocks, 39 us; of 53, one wave, 34.)
+// The step of 256 sequences takes 13 us for 42 MB, half of it the launch, the
+// weights and the first loads.
 #include <type_traits>
 
 #include "block.cuh"

@@ -11,9 +11,9 @@
  *   - rows of the token-major tensors may be strided (a slice of a wider
  *     projection): strides are given in elements, the elements of a row are
  *     contiguous.  Rows of an output must not overlap.
- *   - pointers need only the alignment of their elements.  Rows that are
- *     16-byte aligned (pointer, stride and channel count) load and store
- *     whole 16-byte words.
+ *   - pointers need only the alignment of their elements.  Whole 16-byte
+ *     words are loaded and stored where the rows allow it (pointer, stride and
+ *     channel count); other alignments take narrower accesses.
  * dtype is GDN_BF16 or GDN_F32.  Sums, states and statistics are fp32;
  * results are rounded once, to nearest even.
  *
@@ -22,7 +22,9 @@
  * on the host; a malformed one gives unspecified values, and no access
  * outside the tensors.
  *
- * These operators have no device-side waits and no device status.
+ * These operators have no device-side waits and no device status.  The only
+ * process-wide state they add is, per device and variant of a kernel, whether
+ * its shared-memory limit has been raised (set once).
  */
 #ifndef GDN_BLOCK_H
 #define GDN_BLOCK_H
@@ -132,11 +134,14 @@ GDN_API size_t gdn_selective_scan_workspace_size(const gdn_ssm_problem *problem)
  *                  initial_state (in-place resume)
  * out must not alias an input.
  *
- * The tokens are cut into windows of equal length, enough of them for every
- * window's channels to fill the GPU.  With more than one, three launches run:
- * the state that each window adds on its own (from a zero state, or from the
- * sequence's start inside it), the states entering the windows, and the
- * outputs of all windows.  With one window the last launch runs alone.
+ * The packed tokens are cut into windows of equal length (at least 8 tokens),
+ * as many as make one wave of blocks.  With more than one, three launches
+ * run: the state that each window adds on its own (from a zero state, or from
+ * the sequence's start inside it), the states entering the windows, and the
+ * outputs of all windows; the later ones may start while the one before ends
+ * (programmatic launches on `stream`).  Few tokens run as one window, with
+ * the last launch alone and no workspace.  The order of the fp32 sums depends
+ * on the sizes alone, so a call gives the same bits every time.
  */
 GDN_API gdn_status gdn_selective_scan(const gdn_ssm_problem *problem, const void *x,
                                       const void *dt, const float *A, const void *B,
