@@ -253,13 +253,16 @@ __global__ void __launch_bounds__(kThreads) gdn_short_conv_step_kernel(const Ste
         into[K - 1] = Word::load(a.x + n * a.xs + c);
     };
     if (first < last) fetch(rows, first);
+    float bias[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) bias[v] = a.bias && first < last ? a.bias[c + v] : 0.f;
     stage_weights<K>(sw, a.weight, c0, a.C, a.tx * V);
     for (int n = (int)first; n < last; ++n) {
         Word ahead[K];
         if (n + 1 < last) fetch(ahead, n + 1);
         float y[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) y[v] = a.bias ? a.bias[c + v] : 0.f;
+        for (int v = 0; v < V; ++v) y[v] = bias[v];
 #pragma unroll
         for (int j = 0; j < K; ++j) {
             float r[V];

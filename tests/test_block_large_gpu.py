@@ -193,3 +193,33 @@ def test_refusals_of_the_binding():
         gdn.gdn_norm_gate_residual(x, next_out=x)
     with pytest.raises(gdn.GDNError):
         gdn.gdn_norm_gate_residual(x, eps=-1.0)
+
+
+@pytest.mark.parametrize("states", [16, 13, 64])
+def test_scan_step_of_many_pairs(states):
+    """More (channel tile, sequence) pairs than blocks, so that a block passes
+    from one tile to the next: the same bits as the sequences in small
+    batches, in place and apart."""
+    n, d, groups = 900, 700, 2
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+
+    def normal(*shape, dtype=torch.bfloat16):
+        return torch.randn(*shape, generator=gen, device="cuda").to(dtype)
+    x, dt, z = normal(n, d), normal(n, d), normal(n, d)
+    B, C = normal(n, groups, states), normal(n, groups, states)
+    A = -torch.rand(d, states, generator=gen, device="cuda") * 4
+    D, bias = normal(d, dtype=torch.float32), normal(d, dtype=torch.float32)
+    state = normal(n, d, states, dtype=torch.float32)
+    kw = dict(D=D, dt_bias=bias, dt_softplus=True)
+    want, want_state = [], []
+    for i in range(0, n, 60):
+        at = slice(i, i + 60)
+        s = state[at].clone()
+        want.append(gdn.gdn_selective_scan_step(x[at], dt[at], A, B[at], C[at], s, z=z[at], **kw))
+        want_state.append(s)
+    new = torch.empty_like(state)
+    out = gdn.gdn_selective_scan_step(x, dt, A, B, C, state, z=z, new_state=new, **kw)
+    assert torch.equal(out, torch.cat(want)) and torch.equal(new, torch.cat(want_state))
+    out = gdn.gdn_selective_scan_step(x, dt, A, B, C, state, z=z, **kw)
+    assert torch.equal(out, torch.cat(want)) and torch.equal(state, torch.cat(want_state))
