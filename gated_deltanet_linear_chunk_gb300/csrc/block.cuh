@@ -81,8 +81,7 @@ __device__ __forceinline__ uint64_t silu2(uint64_t v) {
 }
 
 // ------------------------------------------------------------- vector access
-// V consecutive elements: one 16-byte word (16 / sizeof(T) elements) or one
-// element (V = 1).
+// V consecutive elements in one word of up to 16 bytes.
 template <typename T, int V> struct Vec;
 template <typename T> struct Vec<T, 1> {
     T w;
@@ -133,6 +132,28 @@ template <> struct Vec<__nv_bfloat16, 8> {
         return Vec{make_uint4(u[0], u[1], u[2], u[3])};
     }
 };
+template <> struct Vec<__nv_bfloat16, 4> {
+    uint2 w;
+    __device__ __forceinline__ static Vec load(const __nv_bfloat16 *p) {
+        return Vec{*reinterpret_cast<const uint2 *>(p)};
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
+        *reinterpret_cast<uint2 *>(p) = w;
+    }
+    __device__ __forceinline__ static Vec zero() { return Vec{make_uint2(0, 0)}; }
+    __device__ __forceinline__ void to(float *r) const {
+        r[0] = __uint_as_float(w.x << 16);
+        r[1] = __uint_as_float(w.x & 0xffff0000u);
+        r[2] = __uint_as_float(w.y << 16);
+        r[3] = __uint_as_float(w.y & 0xffff0000u);
+    }
+    __device__ __forceinline__ static Vec from(const float *r) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(r[0], r[1]);
+        const __nv_bfloat162 g = __floats2bfloat162_rn(r[2], r[3]);
+        return Vec{make_uint2(*reinterpret_cast<const uint32_t *>(&h),
+                              *reinterpret_cast<const uint32_t *>(&g))};
+    }
+};
 template <> struct Vec<__nv_bfloat16, 2> {
     uint32_t w;
     __device__ __forceinline__ static Vec load(const __nv_bfloat16 *p) {
@@ -180,7 +201,8 @@ template <int BYTES> __device__ __forceinline__ void copy_async(void *smem, cons
     if constexpr (BYTES == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(gmem) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(gmem) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(gmem), "n"(BYTES)
+                     : "memory");
 }
 // 16 bytes that are not read again soon.
 __device__ __forceinline__ uint64_t evict_first_policy() {

@@ -334,7 +334,6 @@ template <typename T, int NS, bool OUT, bool SHIFT> struct ScanTiles {
     }
 };
 
-
 // U tokens from t of tile `buf`, whose first token is t0.  A byte each for x,
 // dt and z: how far the tile's first row is shifted, and what a row adds.
 template <typename T, int NS, bool OUT, bool SHIFT, int U>

@@ -8,21 +8,22 @@
 // element) against 2 K flops, so both kernels are bound by HBM bandwidth and,
 // for few tokens, by the latency of one load and one store.
 //
-// A thread takes one 16-byte word of channels (two 16-bit elements or one
-// element where the rows' alignment allows no more) through a run of
-// consecutive tokens.  The last K - 1
-// inputs stay in registers, so only a run's start reads rows again (K - 1
-// rows per run, from L2).  The run's rows come through a ring in shared memory
-// by asynchronous copies, 8 tokens ahead: 16 KB in flight per block without
-// a register.  Channels go in pairs through the packed fp32 instructions.
+// Over packed sequences a thread takes one word of four channels (two 16-bit
+// elements or one element where the rows' alignment allows no more) through a
+// run of consecutive tokens.  The last K - 1 inputs stay in registers, so only
+// a run's start reads rows again (K - 1 rows per run, from L2).  The run's rows
+// come through a ring in shared memory by asynchronous copies, 16 tokens ahead
+// (8 with 16-byte words): 16 KB in flight per block without a register.
+// Channels go in pairs through the packed fp32 instructions.
 //
-// Measured: 4000 tokens of 10240 bf16 channels, width 4, SiLU, 34 us, 71 % of
-// the copy bandwidth; issue slots 46 % and memory 48 % busy, each group of
-// tokens waiting for its copies and then computing.  (Rows loaded into
-// registers four ahead took 49 us: 136 registers, 24 KB in flight per SM.  With
-// runs of 32 tokens, 1.6 waves of blocks, 39 us; of 53, one wave, 34.)
-// The step of 256 sequences takes 13 us for 42 MB, half of it the launch, the
-// weights and the first loads.
+// Measured: 4000 tokens of 10240 bf16 channels, width 4, SiLU, 31 us, 79 % of
+// the copy bandwidth.  What was tried beside it at this size: bf16 in words of
+// 16 bytes, five blocks per SM, 8 tokens ahead, 35 us (98 registers a thread
+// leave too few warps to cover a group's wait); 8-byte words with five, four
+// and three blocks 33, 35 and 37; rows loaded into registers four ahead 49;
+// runs of up to 96 tokens in place of 64, 33 (a longer last wave).
+// The step keeps 16-byte words: 256 sequences take 12 us for 42 MB, half of it
+// the launch, the weights and the first loads.
 #include <type_traits>
 
 #include "block.cuh"
@@ -32,8 +33,12 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kStep = 4;   // tokens per group of copies
-constexpr int kAhead = 2;  // groups in flight
-constexpr int kRing = (kAhead + 1) * kStep;
+// Groups in flight: 24 KB of ring per block with 16-byte words, 20 KB with
+// 8-byte ones, so that six blocks' rings stay on an SM.
+template <int Bytes> constexpr int kAhead = Bytes == 16 ? 2 : 4;
+template <int Bytes> constexpr int kRing = (kAhead<Bytes> + 1) * kStep;
+// Blocks per SM that the registers of a width's weights and inputs allow.
+template <int K> constexpr int kBlocks = K <= 4 ? 6 : 2;
 
 template <typename T> struct ConvArgs {
     const T *x;
@@ -110,7 +115,7 @@ __device__ __forceinline__ void write_state(const ConvArgs<T> &a, int64_t i) {
 }
 
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(kThreads, K <= 4 ? 5 : 2) gdn_short_conv_kernel(const ConvArgs<T> a) {
+__global__ void __launch_bounds__(kThreads, kBlocks<K>) gdn_short_conv_kernel(const ConvArgs<T> a) {
     constexpr int P = (V + 1) / 2;  // pairs of channels
     extern __shared__ __align__(16) float sw[];
     const int blk = blockIdx.x + a.first;
@@ -125,29 +130,35 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 5 : 2) gdn_short_conv_kerne
     const int t0 = live ? (int)first : 0;
     const int t1 = live ? (int)min(first + a.run, (int64_t)a.T_) : 0;
 
-    // A ring of this thread's words: kAhead groups of kStep tokens on their
+    // A ring of this thread's words: kGroups groups of kStep tokens on their
     // way while one is computed.  A thread reads only what it copied itself,
     // so its own wait is all the synchronisation needed.  (A single 16-bit
     // element comes as the aligned 4-byte word that holds it, without the
     // upper half where that is not needed.)
     using Word = Vec<T, V>;
     using Slot = std::conditional_t<sizeof(Word) == 2, uint32_t, Word>;
+    constexpr int kGroups = kAhead<sizeof(Slot)>, kSlots = kRing<sizeof(Slot)>;
     Slot *ring = reinterpret_cast<Slot *>(sw + a.tx * V * K) + threadIdx.x;
-    auto issue = [&](int t) {
-        const T *from = a.x + t * a.xs + c;
-        Slot *to = ring + ((t - t0) % kRing) * kThreads;
-#pragma unroll
-        for (int u = 0; u < kStep; ++u, from += a.xs) {
-            if (t + u >= t1) break;
+    const T *ahead = a.x + t0 * a.xs + c;  // where copies go on
+    int ahead_t = t0, ahead_slot = 0;
+    auto issue = [&] {
+        Slot *to = ring + ahead_slot * kThreads;
+        auto copy = [&](int u) {
             if constexpr (sizeof(Word) == 2)
-                copy_async_part(to + u * kThreads, from - odd(from), odd(from) ? 4 : 2);
+                copy_async_part(to + u * kThreads, ahead - odd(ahead), odd(ahead) ? 4 : 2);
             else
-                copy_async<sizeof(Word)>(to + u * kThreads, from);
-        }
+                copy_async<sizeof(Word)>(to + u * kThreads, ahead);
+            ahead += a.xs;
+        };
+#pragma unroll
+        for (int u = 0; u < kStep; ++u)
+            if (ahead_t + u < t1) copy(u);
+        ahead_t += kStep;
+        ahead_slot = ahead_slot + kStep == kSlots ? 0 : ahead_slot + kStep;
         copies_commit();
     };
-    auto arrived = [&](int t) {
-        const Slot v = ring[((t - t0) % kRing) * kThreads];
+    auto arrived = [&](int t, int slot) {
+        const Slot v = ring[slot * kThreads];
         if constexpr (sizeof(Word) == 2) {
             const T *from = a.x + t * a.xs + c;
             const uint16_t half = (uint16_t)(odd(from) ? v >> 16 : v);
@@ -157,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 5 : 2) gdn_short_conv_kerne
         }
     };
 #pragma unroll
-    for (int g = 0; g < kAhead; ++g) issue(t0 + g * kStep);
+    for (int g = 0; g < kGroups; ++g) issue();
 
     // Then, while they come: the sequence, the inputs before the run, the weights.
     Span s{};
@@ -184,8 +195,8 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 5 : 2) gdn_short_conv_kerne
         b[i] = a.bias ? pack2f(a.bias[c + 2 * i], V > 1 ? a.bias[c + 2 * i + 1] : 0.f) : 0;
     }
     T *to = a.out + t0 * a.os + c;
-    auto token = [&](int t) {
-        pairs(arrived(t), in[K - 1]);
+    auto token = [&](int t, int slot) {
+        pairs(arrived(t, slot), in[K - 1]);
         float y[2 * P];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -202,11 +213,12 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 5 : 2) gdn_short_conv_kerne
         Word::from(y).store(to);
         to += a.os;
     };
+    int slot = 0;
     for (int t = t0; t < t1; t += kStep) {
-        copies_wait<kAhead - 1>();
+        copies_wait<kGroups - 1>();
         if (t + kStep <= min(s.end, t1)) {
 #pragma unroll
-            for (int u = 0; u < kStep; ++u) token(t + u);
+            for (int u = 0; u < kStep; ++u) token(t + u, slot + u);
         } else {
             const int te = min(t + kStep, t1);
 #pragma unroll 1
@@ -217,10 +229,11 @@ __global__ void __launch_bounds__(kThreads, K <= 4 ? 5 : 2) gdn_short_conv_kerne
                     for (int j = 0; j < K - 1; ++j)
                         pairs(tap<T, V, K>(a, s.n, s.start, tok - (K - 1) + j, c), in[j]);
                 }
-                token(tok);
+                token(tok, slot + tok - t);
             }
         }
-        issue(t + kAhead * kStep);
+        slot = slot + kStep == kSlots ? 0 : slot + kStep;
+        issue();
     }
 }
 
@@ -310,9 +323,7 @@ gdn_status run_conv(const gdn_conv_problem &p, const void *x, const float *weigh
     a.os = p.out_stride;
     a.act = p.activation == GDN_ACT_SILU;
     const int words = p.channels / V;
-    // (Half a block along the channels where all of it would need more than
-    // the 48 KB of shared memory that a kernel has by default.)
-    a.tx = threads_along(words, V * K > 48 ? kThreads / 2 : kThreads);
+    a.tx = threads_along(words, kThreads);
     a.n_chan = (words + a.tx - 1) / a.tx;
     const int ty = kThreads / a.tx;
     // Tokens per thread: long runs read fewer rows twice (K - 1 of each
@@ -322,7 +333,7 @@ gdn_status run_conv(const gdn_conv_problem &p, const void *x, const float *weigh
     };
     // One wave of blocks with runs of up to 64 tokens, or so many full waves;
     // at least 8 tokens while four blocks per SM are left.
-    const int64_t slots = (K <= 4 ? 5 : 2) * kGridSms;
+    const int64_t slots = kBlocks<K> * kGridSms;
     const int64_t each = (p.total_tokens * a.n_chan + slots * ty - 1) / (slots * ty);
     const int64_t waves = (each + 63) / 64;
     a.run = (int)((each + waves - 1) / (waves > 0 ? waves : 1));
@@ -332,7 +343,10 @@ gdn_status run_conv(const gdn_conv_problem &p, const void *x, const float *weigh
         fin ? ((int64_t)p.num_seqs * words + kThreads - 1) / kThreads : 0;
     if (n_main + n_state > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     a.n_main = (int)n_main;
-    const size_t smem = (size_t)a.tx * V * K * sizeof(float) + kRing * kThreads * (sizeof(T) * V < 4 ? 4 : sizeof(T) * V);
+    // (36 KB at most, at width 8.)
+    constexpr int kSlot = sizeof(T) * V < 4 ? 4 : sizeof(T) * V;
+    static_assert((kThreads * V * K * 4 + kRing<kSlot> * kThreads * kSlot) <= 48 * 1024);
+    const size_t smem = (size_t)a.tx * V * K * sizeof(float) + kRing<kSlot> * kThreads * kSlot;
     // A state written in place must not replace what another block still
     // reads: its blocks then run as a launch of their own.
     const bool apart = fin && fin == init;
@@ -377,7 +391,7 @@ gdn_status run_step(const gdn_conv_problem &p, const void *x, const float *weigh
     return launch_status();
 }
 
-// f<V>(K): the word by the rows' alignment, K by the width.
+// run<T, V, K>: the word by the rows' alignment, K by the width.
 #define GDN_CONV_WIDTHS(run, T, V)                        \
     switch (p.width) {                                    \
         case 2: return run<T, V, 2>(GDN_CONV_ARGS);       \
@@ -389,9 +403,9 @@ gdn_status run_step(const gdn_conv_problem &p, const void *x, const float *weigh
         case 8: return run<T, V, 8>(GDN_CONV_ARGS);       \
     }                                                     \
     return GDN_ERR_UNSUPPORTED;
-#define GDN_CONV_DISPATCH(run, T, word)                   \
-    if (word == kWide<T>) {                               \
-        GDN_CONV_WIDTHS(run, T, kWide<T>)                 \
+#define GDN_CONV_DISPATCH(run, T, wide, word)             \
+    if (word == wide) {                                   \
+        GDN_CONV_WIDTHS(run, T, wide)                     \
     }                                                     \
     if constexpr (sizeof(T) == 2)                         \
         if (word == 2) {                                  \
@@ -399,25 +413,27 @@ gdn_status run_step(const gdn_conv_problem &p, const void *x, const float *weigh
         }                                                 \
     GDN_CONV_WIDTHS(run, T, 1)
 
-// The widest word of rows of x and out, and of contiguous states: whole 16
-// bytes, two 16-bit elements, or one element.
+// The word of rows of x and out, and of contiguous states: `wide` elements
+// where the alignment allows, two 16-bit elements, or one element.
 template <typename T>
-int conv_word(const gdn_conv_problem &p, const void *x, const void *out, const void *a,
+int conv_word(int wide, const gdn_conv_problem &p, const void *x, const void *out, const void *a,
               const void *b) {
     const uint64_t bits = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out) |
                           reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) |
                           (uint64_t)p.x_stride * sizeof(T) | (uint64_t)p.out_stride * sizeof(T) |
                           (uint64_t)p.channels * sizeof(T);
-    return bits % 16 == 0 ? kWide<T> : sizeof(T) == 2 && bits % 4 == 0 ? 2 : 1;
+    return bits % (wide * sizeof(T)) == 0 ? wide : sizeof(T) == 2 && bits % 4 == 0 ? 2 : 1;
 }
 
 template <typename T>
 gdn_status conv_typed(const gdn_conv_problem &p, const void *x, const float *weight,
                       const float *bias, const int32_t *cu, const void *init, void *out,
                       void *fin, cudaStream_t stream) {
-    const int word = conv_word<T>(p, x, out, init, fin);
+    // Four elements, so 8 bytes of bf16: their few registers let six blocks
+    // stay on an SM.
+    const int word = conv_word<T>(4, p, x, out, init, fin);
 #define GDN_CONV_ARGS p, x, weight, bias, cu, init, out, fin, stream
-    GDN_CONV_DISPATCH(run_conv, T, word)
+    GDN_CONV_DISPATCH(run_conv, T, 4, word)
 #undef GDN_CONV_ARGS
 }
 
@@ -425,9 +441,9 @@ template <typename T>
 gdn_status step_typed(const gdn_conv_problem &p, const void *x, const float *weight,
                       const float *bias, const void *state, void *out, void *next,
                       cudaStream_t stream) {
-    const int word = conv_word<T>(p, x, out, state, next);
+    const int word = conv_word<T>(kWide<T>, p, x, out, state, next);
 #define GDN_CONV_ARGS p, x, weight, bias, state, out, next, stream
-    GDN_CONV_DISPATCH(run_step, T, word)
+    GDN_CONV_DISPATCH(run_step, T, kWide<T>, word)
 #undef GDN_CONV_ARGS
 }
 
