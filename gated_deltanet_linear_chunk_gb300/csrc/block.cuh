@@ -32,17 +32,17 @@ __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 // [0, 1] (3e-8; 1.4e-7 in fp32 arithmetic, 5e-8 on average): relative accuracy
 // is kept for the small steps of very negative v, where log1p(e) is e.  (NaN:
 // e is NaN, and so is the result.)
+__device__ __forceinline__ constexpr float softplus_coefficient(int power) {
+    constexpr float c[9] = {0.9999999403953552f,  -0.4999949336051941f,  0.3331909775733948f,
+                            -0.2484298199415207f, 0.19106008112430573f,  -0.13663247227668762f,
+                            0.07822594791650772f, -0.029505232349038124f, 0.005232691299170256f};
+    return c[power];
+}
 __device__ __forceinline__ float softplus(float v) {
     const float e = ex2(-kLog2e * fabsf(v));
-    float p = 0.005232691299170256f;
-    p = fmaf(p, e, -0.029505232349038124f);
-    p = fmaf(p, e, 0.07822594791650772f);
-    p = fmaf(p, e, -0.13663247227668762f);
-    p = fmaf(p, e, 0.19106008112430573f);
-    p = fmaf(p, e, -0.2484298199415207f);
-    p = fmaf(p, e, 0.3331909775733948f);
-    p = fmaf(p, e, -0.4999949336051941f);
-    p = fmaf(p, e, 0.9999999403953552f);
+    float p = softplus_coefficient(8);
+#pragma unroll
+    for (int k = 7; k >= 0; --k) p = fmaf(p, e, softplus_coefficient(k));
     return fmaf(p, e, fmaxf(v, 0.f));
 }
 
@@ -73,7 +73,16 @@ __device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
-// silu of both.
+// softplus and silu of both.
+__device__ __forceinline__ uint64_t softplus2(uint64_t v) {
+    const float2 w = unpack2f(v);
+    const uint64_t e = pack2f(ex2(-kLog2e * fabsf(w.x)), ex2(-kLog2e * fabsf(w.y)));
+    uint64_t p = pack2f(softplus_coefficient(8), softplus_coefficient(8));
+#pragma unroll
+    for (int k = 7; k >= 0; --k)
+        p = ffma2(p, e, pack2f(softplus_coefficient(k), softplus_coefficient(k)));
+    return ffma2(p, e, pack2f(fmaxf(w.x, 0.f), fmaxf(w.y, 0.f)));
+}
 __device__ __forceinline__ uint64_t silu2(uint64_t v) {
     const float2 e = unpack2f(fmul2(v, pack2f(-kLog2e, -kLog2e)));
     const float2 f = unpack2f(fadd2(pack2f(ex2(e.x), ex2(e.y)), pack2f(1.f, 1.f)));

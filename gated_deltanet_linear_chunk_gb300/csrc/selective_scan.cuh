@@ -96,7 +96,7 @@ template <typename T, int NS> struct ScanThread {
     static constexpr int CH = kChannels<NS>;
     static constexpr int NP = NS / 2;
     uint64_t A[CH][NP], h[CH][NP];
-    float bias[CH], skip[CH], sum[CH];
+    uint64_t bias, skip, sum;  // of both channels; of one and zero where CH = 1
     int d, col;  // first channel: in the tensors, in the block
     int valid;   // channels that exist
 
@@ -104,12 +104,12 @@ template <typename T, int NS> struct ScanThread {
         col = threadIdx.x * CH;
         d = group * a.per_group + in_group0 + col;
         valid = min(max(a.per_group - in_group0 - col, 0), CH);
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            bias[c] = c < valid && a.bias ? a.bias[d + c] : 0.f;
-            skip[c] = c < valid && a.skip ? a.skip[d + c] : 0.f;
-            sum[c] = 0.f;
-        }
+        auto both = [&](const float *p) {
+            return pack2f(p && valid > 0 ? p[d] : 0.f, p && valid > 1 ? p[d + 1] : 0.f);
+        };
+        bias = both(a.bias);
+        skip = both(a.skip);
+        sum = 0;
         read(a, a.A, 0, kLog2e, A);
     }
     // This thread's part of row `row` of a [rows, D, S] array (zeros where it
@@ -156,19 +156,20 @@ template <typename T, int NS> struct ScanThread {
             }
         }
     }
-    // One token: xv, dv of the channels, B and C of the group; y = C . h.
+    // One token: x and dt of the channels, B and C of the group; returns C . h.
     template <bool OUT>
-    __device__ __forceinline__ void token(bool softplus_on, const float *xv, const float *dv,
-                                          const float *sB, const float *sC, float *y) {
+    __device__ __forceinline__ uint64_t token(bool softplus_on, uint64_t x, uint64_t dt,
+                                              const float *sB, const float *sC) {
+        // (A choice, not a branch: the tokens of a run are one basic block,
+        // which the compiler can interleave.)
+        const uint64_t v = fadd2(dt, bias), sp = softplus2(v), s = softplus_on ? sp : v;
+        if (!OUT) sum = fadd2(sum, s);
+        const float2 s1 = unpack2f(s), u1 = unpack2f(fmul2(s, x));
         uint64_t s2[CH], u2[CH], y2[CH];
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            // (A choice, not a branch: the tokens of a run are one basic block,
-            // which the compiler can interleave.)
-            const float v = dv[c] + bias[c], sp = softplus(v), s = softplus_on ? sp : v;
-            if (!OUT) sum[c] += s;
-            s2[c] = pack2f(s, s);
-            u2[c] = pack2f(s * xv[c], s * xv[c]);
+            s2[c] = c ? pack2f(s1.y, s1.y) : pack2f(s1.x, s1.x);
+            u2[c] = c ? pack2f(u1.y, u1.y) : pack2f(u1.x, u1.x);
             y2[c] = 0;
         }
 #pragma unroll
@@ -187,12 +188,8 @@ template <typename T, int NS> struct ScanThread {
                     if (OUT) y2[c] = ffma2(cc[i], h[c][p], y2[c]);
                 }
         }
-        if (OUT)
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const float2 v = unpack2f(y2[c]);
-                y[c] = v.x + v.y;
-            }
+        const float2 y0 = unpack2f(y2[0]), y1 = unpack2f(y2[CH - 1]);
+        return pack2f(y0.x + y0.y, CH > 1 ? y1.x + y1.y : 0.f);
     }
 };
 
@@ -347,27 +344,25 @@ __device__ __forceinline__ void scan_run(const ScanArgs<T> &a, ScanThread<T, NS>
         const int r = t - t0 + u;
         const T *in = tl.in(buf) + r * tl.pitch + th.col;
         const uint32_t o = SHIFT ? shifts + r * steps : 0;
-        auto own = [&](int k, float *v) {
+        auto own = [&](int k) {
             const T *p = in + k * kTile * tl.pitch;
+            float v[2] = {0.f, 0.f};
             if (SHIFT) {
 #pragma unroll
                 for (int c = 0; c < CH; ++c) v[c] = to_f32(p[c + (o >> (8 * k) & (kWide<T> - 1))]);
             } else {
                 Vec<T, CH>::load(p).to(v);
             }
+            return pack2f(v[0], v[1]);
         };
-        float xv[CH], dv[CH];
-        own(0, xv);
-        own(1, dv);
-        th.template token<OUT>(a.softplus, xv, dv, tl.bc + r * NS, tl.bc + (kTile + r) * NS, y[u]);
+        const uint64_t x = own(0);
+        const uint64_t sums = th.template token<OUT>(a.softplus, x, own(1), tl.bc + r * NS,
+                                                     tl.bc + (kTile + r) * NS);
         if (OUT) {
-            float zv[CH];
-            own(2, zv);
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const float gate = silu(zv[c]);
-                y[u][c] = fmaf(th.skip[c], xv[c], y[u][c]) * (a.z ? gate : 1.f);
-            }
+            const uint64_t gate = silu2(own(2)), v = ffma2(th.skip, x, sums);
+            const float2 f = unpack2f(a.z ? fmul2(v, gate) : v);
+            y[u][0] = f.x;
+            if (CH > 1) y[u][CH - 1] = f.y;
         }
     }
     if (!OUT) return;
@@ -477,9 +472,10 @@ __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(co
     if (!OUT) {
         ptx::griddep_launch_dependents();
         th.store(a, a.carry, w);
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-            if (c < th.valid) a.steps[(int64_t)w * a.D + th.d + c] = th.sum[c];
+        const float2 sum = unpack2f(th.sum);
+        float *steps = a.steps + (int64_t)w * a.D + th.d;
+        if (th.valid > 0) steps[0] = sum.x;
+        if (th.valid > 1) steps[1] = sum.y;
     }
 }
 
