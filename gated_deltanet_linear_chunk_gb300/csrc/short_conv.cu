@@ -16,13 +16,13 @@
 // (8 with 16-byte words): 16 KB in flight per block without a register.
 // Channels go in pairs through the packed fp32 instructions.
 //
-// Measured: 4000 tokens of 10240 bf16 channels, width 4, SiLU, 31 us, 79 % of
+// Measured: 4000 tokens of 10240 bf16 channels, width 4, SiLU, 30 us, 82 % of
 // the copy bandwidth.  What was tried beside it at this size: bf16 in words of
 // 16 bytes, five blocks per SM, 8 tokens ahead, 35 us (98 registers a thread
 // leave too few warps to cover a group's wait); 8-byte words with five, four
 // and three blocks 33, 35 and 37; rows loaded into registers four ahead 49;
-// runs of up to 96 tokens in place of 64, 33 (a longer last wave).
-// The step keeps 16-byte words: 256 sequences take 12 us for 42 MB, half of it
+// runs of up to 96 tokens in place of 64, 33 (a longer last wave); weights staged in single floats 31.
+// The step keeps 16-byte words: 256 sequences take 11 us for 42 MB, half of it
 // the launch, the weights and the first loads.
 #include <type_traits>
 
@@ -58,22 +58,34 @@ template <typename T> struct ConvArgs {
 
 // The weights of this block's channels as [K][channels] in shared memory:
 // read from [C, K] in order, so that the threads' own columns are not a
-// strided walk over global memory, eight loads before their stores.
+// strided walk over global memory, eight loads before their stores: all of
+// them up to 32 weights a thread in 16-byte words.
+template <int K, int V>
+__device__ __forceinline__ void stage_words(float *sw, const float *from, int i0, int n, int width) {
+    using Word = Vec<float, V>;
+    for (i0 += threadIdx.x * V; i0 < n; i0 += 8 * kThreads * V) {
+        Word w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i0 + k * kThreads * V < n) w[k] = Word::load(from + i0 + k * kThreads * V);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k * kThreads * V;
+            float v[V];
+            w[k].to(v);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (i < n) sw[(i + e) % K * width + (i + e) / K] = v[e];
+        }
+    }
+}
 template <int K>
 __device__ __forceinline__ void stage_weights(float *sw, const float *w, int c0, int C, int width) {
     const int n = min(width, C - c0) * K;
     const float *from = w + (int64_t)c0 * K;
-    for (int i0 = threadIdx.x; i0 < n; i0 += 8 * kThreads) {
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (i0 + k * kThreads < n) v[k] = from[i0 + k * kThreads];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int i = i0 + k * kThreads;
-            if (i < n) sw[(i % K) * width + i / K] = v[k];
-        }
-    }
+    const int whole = reinterpret_cast<uintptr_t>(from) % 16 == 0 ? n & ~3 : 0;
+    stage_words<K, 4>(sw, from, 0, whole, width);
+    if (whole < n) stage_words<K, 1>(sw, from, whole, n, width);
     __syncthreads();
 }
 
