@@ -2,6 +2,9 @@
 // of the ABI): vector loads, elementary functions, the sequence of a token.
 #pragma once
 
+#include <atomic>
+#include <initializer_list>
+
 #include "common.cuh"
 #include "gdn_block.h"
 
@@ -73,7 +76,7 @@ __device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
 }
-// softplus and silu of both.
+// softplus, sigmoid and silu of both.
 __device__ __forceinline__ uint64_t softplus2(uint64_t v) {
     const float2 w = unpack2f(v);
     const uint64_t e = pack2f(ex2(-kLog2e * fabsf(w.x)), ex2(-kLog2e * fabsf(w.y)));
@@ -83,11 +86,12 @@ __device__ __forceinline__ uint64_t softplus2(uint64_t v) {
         p = ffma2(p, e, pack2f(softplus_coefficient(k), softplus_coefficient(k)));
     return ffma2(p, e, pack2f(fmaxf(w.x, 0.f), fmaxf(w.y, 0.f)));
 }
-__device__ __forceinline__ uint64_t silu2(uint64_t v) {
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t v) {
     const float2 e = unpack2f(fmul2(v, pack2f(-kLog2e, -kLog2e)));
     const float2 f = unpack2f(fadd2(pack2f(ex2(e.x), ex2(e.y)), pack2f(1.f, 1.f)));
-    return fmul2(v, pack2f(rcp(f.x), rcp(f.y)));
+    return pack2f(rcp(f.x), rcp(f.y));
 }
+__device__ __forceinline__ uint64_t silu2(uint64_t v) { return fmul2(v, sigmoid2(v)); }
 
 // ------------------------------------------------------------- vector access
 // V consecutive elements in one word of up to 16 bytes.
@@ -196,6 +200,24 @@ template <> struct Vec<float, 2> {
 template <typename T> __device__ __forceinline__ int odd(const T *p) {
     return (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & 1;
 }
+// V elements of a word as pairs (an element alone: with a zero), and back.
+template <int V, typename Word>
+__device__ __forceinline__ void to_pairs(const Word &w, uint64_t (&p)[(V + 1) / 2]) {
+    float r[V + 1];
+    r[V] = 0.f;
+    w.to(r);
+#pragma unroll
+    for (int i = 0; i < V; i += 2) p[i / 2] = pack2f(r[i], r[i + 1]);
+}
+template <int V>
+__device__ __forceinline__ void from_pairs(const uint64_t (&p)[(V + 1) / 2], float (&r)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+        const float2 v = unpack2f(p[i / 2]);
+        r[i] = v.x;
+        if (i + 1 < V) r[i + 1] = v.y;
+    }
+}
 template <typename T> constexpr int kWide = 16 / (int)sizeof(T);
 
 // Whether rows at p, `stride` elements apart, start on 16-byte boundaries.
@@ -205,9 +227,12 @@ template <typename T> inline bool rows_aligned16(const void *p, int64_t stride) 
 
 // ------------------------------------------------------- asynchronous copies
 // From global to shared memory, 4 or 16 bytes, both sides aligned to them.
-template <int BYTES> __device__ __forceinline__ void copy_async(void *smem, const void *gmem) {
+// (PART: the rest of a 32-byte sector is copied by this thread's next copy, which
+// finds it in L1.)
+template <int BYTES, bool PART = false>
+__device__ __forceinline__ void copy_async(void *smem, const void *gmem) {
     const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    if constexpr (BYTES == 16)
+    if constexpr (BYTES == 16 && !PART)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(gmem) : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(gmem), "n"(BYTES)
@@ -235,6 +260,24 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 // Waits until at most N committed groups of this thread's copies are on their way.
 template <int N> __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A kernel has 48 KB of shared memory by default: for more the limit is raised
+// once per device and variant.
+constexpr int kMaxDevices = 64;
+inline bool raise_shared_memory(std::atomic<bool> (&done)[kMaxDevices],
+                                std::initializer_list<const void *> kernels,
+                                std::initializer_list<size_t> bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    if (done[dev].load(std::memory_order_acquire)) return true;
+    auto size = bytes.begin();
+    for (const void *k : kernels)
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)*size++) != cudaSuccess)
+            return false;
+    done[dev].store(true, std::memory_order_release);
+    return true;
 }
 
 // ---------------------------------------------------- packed sequences

@@ -13,7 +13,8 @@
 // rounded to out's type.  Rows of up to 32 lanes' words share a warp (a
 // power of two of lanes each, reduced by shuffles); longer rows take a block.
 // The grid is one wave that walks the rows, so the weights are read once per
-// block and a row's loads are on their way while the row before is reduced.
+// block and a row's loads are on their way while the row before is reduced:
+// in registers, or for long rows in shared memory.
 //
 // Measured: 4000 rows of 6144, bf16 y and gate, fp32 residual, both norms, 58 us,
 // 87 % of the copy bandwidth (a block per row, weights read again for each: 90
@@ -25,6 +26,7 @@ namespace gdn {
 namespace {
 
 constexpr int kWarpThreads = 128;  // block of the rows that share warps
+constexpr int64_t kRingBudget = 220 * 1024;  // of an SM's shared memory, for the rings
 
 template <typename T, typename R> struct NormArgs {
     const T *y, *gate;
@@ -34,14 +36,16 @@ template <typename T, typename R> struct NormArgs {
     T *next;
     int64_t rows;
     int dim, lanes, act;
+    int ahead, row_bytes;  // rows in the ring, and the size of one
+    bool staged;   // the weights are in shared memory
     bool gate_first;
     float eps, scale, inv_dim;
     int64_t ys, gs, rs, os, ns;
 };
 
-// V elements: one, two, or whole 16-byte words.
+// V elements: in words of up to 16 bytes.
 template <typename T, int V> struct Words {
-    static constexpr int W = V <= 2 ? V : kWide<T>;
+    static constexpr int W = V < kWide<T> ? V : kWide<T>;
     Vec<T, W> w[V / W];
     __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
@@ -77,23 +81,71 @@ template <bool BLOCK> __device__ __forceinline__ float row_sum(float v, int lane
     return warp_sum(v);
 }
 
-// Elements of a row that a lane may hold with the weights and the next row's
-// words beside them.
-template <int V, int I> constexpr bool kAhead = V <= 2 ? I <= 4 : V * I <= 16;
-// Threads of a block that shares one row: as many as leave a thread those
-// registers.
-template <int V, int I> constexpr int kRowThreads = V <= 2 || V * I <= 8 ? 1024 : 512;
+// Where a lane's next rows wait.  In registers, one row ahead, where its part
+// is up to 8 elements in 4 words (16 for rows within a warp); else in a ring in
+// shared memory, up to four rows ahead, through asynchronous copies: 16 elements with
+// the weights and another row's words leave no registers.  (us without rows
+// ahead and with the ring: 2436 rows of 10088 46 and 31, 2590 of 9488 53 and
+// 35, 791 of 11624 in fp32 42 and 22, 2552 of 9629 163 and 123.  Few narrow
+// words are bound by their instructions: 9965 rows of 2466 take 38 in
+// registers and 50 with a ring.)
+template <int V, int I, bool BLOCK> constexpr bool kRing = BLOCK && (V * I > 8 || I > 4);
+// Blocks per SM of the rows that share warps, by the elements of a lane.
+template <int N> constexpr int kWarpBlocks = N <= 8 ? 8 : 4;
+// A block that shares one row has at most this many threads.
+constexpr int kRowThreads = 1024;
+
+// A lane's part of one row in the ring: I words of V elements in pieces of up
+// to 16 bytes, a single 16-bit element in the 4-byte word that holds it.
+template <typename E, int V, int I> struct RowSlots {
+    static constexpr int kWord = V * (int)sizeof(E) < 4 ? 4 : V * (int)sizeof(E);
+    static constexpr int kPiece = kWord < 16 ? kWord : 16, kPieces = kWord / kPiece;
+    static constexpr int kBytes = I * kWord;  // per thread
+    __device__ __forceinline__ static char *piece(char *base, int threads, int i, int k) {
+        return base + ((i * kPieces + k) * threads + threadIdx.x) * kPiece;
+    }
+    // high: whether a single 16-bit element lies in its 4-byte word's upper half.
+    __device__ __forceinline__ static void copy(char *base, int threads, int i, const E *from,
+                                                int high) {
+        if constexpr (V * sizeof(E) == 2) {
+            copy_async_part(piece(base, threads, i, 0), from - high, high ? 4 : 2);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k)
+                copy_async<kPiece, (kPieces > 1)>(piece(base, threads, i, k),
+                                                  from + k * (kPiece / sizeof(E)));
+        }
+    }
+    __device__ __forceinline__ static void read(char *base, int threads, int i, int high,
+                                                float *to) {
+        if constexpr (V * sizeof(E) == 2) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(piece(base, threads, i, 0));
+            const uint16_t half = (uint16_t)(high ? w >> 16 : w);
+            to[0] = to_f32(*reinterpret_cast<const E *>(&half));
+        } else {
+            constexpr int W = kPiece / (int)sizeof(E);
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k)
+                Vec<E, W>::load(reinterpret_cast<const E *>(piece(base, threads, i, k))).to(to + k * W);
+        }
+    }
+};
+
 
 // I words of V elements per lane.  BLOCK: the block's threads share a row;
-// otherwise a.lanes lanes do.  Each walks rows a grid apart with the weights
-// in registers, and starts the next row's loads before the first reduction
-// of the one at hand.  Lanes past the row's end load its first word and leave
-// it out of sums and stores.  The gate commutes with the norm's factor, so a
-// lane keeps only y times the gate and the residual.
+// otherwise a.lanes lanes do.  Each walks rows a grid apart, the weights in
+// registers or shared memory, and starts the loads of the next rows before the
+// first reduction of the one at hand.  Words past the row's end hold anything
+// and are left out of sums and stores.  The gate commutes with the norm's
+// factor, so a lane keeps only y times the gate and the residual.
 template <typename T, typename R, int V, int I, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? kRowThreads<V, I> : kWarpThreads)
+__global__ void __launch_bounds__(BLOCK ? kRowThreads : kWarpThreads)
 gdn_norm_kernel(const NormArgs<T, R> a) {
-    constexpr bool AHEAD = kAhead<V, I>;
+    constexpr bool RING = kRing<V, I, BLOCK>;
+    using SlotT = RowSlots<T, V, I>;
+    using SlotR = RowSlots<R, V, I>;
+    using SlotW = RowSlots<float, V, I>;
+    extern __shared__ __align__(16) char ring[];  // [row ahead][y, gate, residual], weights
     // Two sums per pass, in turn for odd and even passes: with only one of
     // them there is one barrier between a pass's reads and the next's writes.
     __shared__ float sums[2][2][32];
@@ -104,48 +156,110 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
     int64_t row = (int64_t)blockIdx.x * groups + (BLOCK ? 0 : threadIdx.x / lanes);
     const int64_t step = (int64_t)gridDim.x * groups;
 
-    int c[I];
-    bool ok[I];
-    float w[AHEAD ? I : 1][V], nw[AHEAD ? I : 1][V];
+    // Whether the row has word i of this lane, and its first element (of a word
+    // that it has not, the row's first: the words held in registers are loaded
+    // all).  Many words' places are computed each time, a few are kept.
+    const int c0 = lane * V, span = lanes * V;
+    int column[RING ? 1 : I];
+    bool exists[RING ? 1 : I];
+    auto ok = [&](int i) { return RING ? c0 + i * span < a.dim : exists[RING ? 0 : i]; };
+    auto c = [&](int i) { return RING ? c0 + i * span : column[RING ? 0 : i]; };
+    if (!RING)
 #pragma unroll
-    for (int i = 0; i < I; ++i) {
-        c[i] = (lane + i * lanes) * V;
-        ok[i] = c[i] < a.dim;
-        if (!ok[i]) c[i] = 0;
-    }
+        for (int i = 0; i < I; ++i) {
+            exists[RING ? 0 : i] = c0 + i * span < a.dim;
+            column[RING ? 0 : i] = exists[RING ? 0 : i] ? c0 + i * span : 0;
+        }
+    // Whether word i of a row is in the upper half of 4 bytes (a block's words
+    // lie an even number of elements apart).
+    auto high = [&](const auto *r, int i) { return odd(r + c0) ^ (BLOCK ? 0 : i & span & 1); };
+    const int threads = blockDim.x;
+    auto in_gate = [&](char *stage) { return stage + SlotT::kBytes * threads; };
+    auto in_residual = [&](char *stage) {
+        return stage + (a.gate ? 2 : 1) * SlotT::kBytes * threads;
+    };
+    char *const staged = ring + a.ahead * a.row_bytes;  // weights
     Words<T, V> yw[I], gw[I];
     Words<R, V> rw[I];
-    auto fetch = [&](int64_t r) {
+    // Row r's loads; in the ring's place `stage`, if it exists.
+    auto fetch = [&](int64_t r, char *stage) {
+        if (!RING) {
+            r = min(r, a.rows - 1);
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            yw[i].load(a.y + r * a.ys + c[i]);
-            if (a.gate) gw[i].load(a.gate + r * a.gs + c[i]);
-            if (a.residual) rw[i].load(a.residual + r * a.rs + c[i]);
+            for (int i = 0; i < I; ++i) {
+                yw[i].load(a.y + r * a.ys + c(i));
+                if (a.gate) gw[i].load(a.gate + r * a.gs + c(i));
+                if (a.residual) rw[i].load(a.residual + r * a.rs + c(i));
+            }
+            return;
         }
+        if (r < a.rows) {
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                if (!ok(i)) break;
+                SlotT::copy(stage, threads, i, a.y + r * a.ys + c(i), high(a.y + r * a.ys, i));
+                if (a.gate)
+                    SlotT::copy(in_gate(stage), threads, i, a.gate + r * a.gs + c(i),
+                                high(a.gate + r * a.gs, i));
+                if (a.residual)
+                    SlotR::copy(in_residual(stage), threads, i, a.residual + r * a.rs + c(i),
+                                high(a.residual + r * a.rs, i));
+            }
+        }
+        copies_commit();
     };
-    fetch(min(row, a.rows - 1));
-    if (AHEAD)
+    float w[RING ? 1 : I][V], nw[RING ? 1 : I][V];
+    if (RING && a.staged)
 #pragma unroll
         for (int i = 0; i < I; ++i) {
-            if (a.weight) load_f<V>(a.weight + c[i], w[i]);
-            if (a.next_weight) load_f<V>(a.next_weight + c[i], nw[i]);
+            if (!ok(i)) break;
+            if (a.weight) SlotW::copy(staged, threads, i, a.weight + c(i), 0);
+            if (a.next_weight)
+                SlotW::copy(staged + SlotW::kBytes * threads, threads, i, a.next_weight + c(i), 0);
         }
+    if (RING)
+        for (int k = 0; k < a.ahead; ++k)
+            fetch(row + k * step, ring + k * a.row_bytes);
+    else
+        fetch(row, nullptr);
+    if (!RING)
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            if (a.weight) load_f<V>(a.weight + c(i), w[i]);
+            if (a.next_weight) load_f<V>(a.next_weight + c(i), nw[i]);
+        }
+    auto weight = [&](const float *all, int second, int i, float *to) {
+        if (a.staged)
+            SlotW::read(staged + second * SlotW::kBytes * threads, threads, i, 0, to);
+        else
+            load_f<V>(all + (ok(i) ? c(i) : 0), to);
+    };
     // All groups of a block make the same number of passes: the sums need
     // every lane of a warp.
+    int place = 0;  // of this row in the ring
     for (int64_t first = (int64_t)blockIdx.x * groups; first < a.rows;
          first += step, row += step, turn ^= 1) {
         const bool live = row < a.rows;
+        char *const stage = ring + place * a.row_bytes;
+        if (RING) {
+            if (a.ahead == 1) copies_wait<0>();
+            else if (a.ahead == 2) copies_wait<1>();
+            else copies_wait<3>();
+            place = place + 1 == a.ahead ? 0 : place + 1;
+        }
         float m[I][V], r[I][V], sum = 0.f;
 #pragma unroll
         for (int i = 0; i < I; ++i) {
-            yw[i].to(m[i]);
+            if (RING) SlotT::read(stage, threads, i, high(a.y + row * a.ys, i), m[i]);
+            else yw[i].to(m[i]);
             float part = 0.f;
             if (!a.gate_first)
 #pragma unroll
                 for (int v = 0; v < V; ++v) part = fmaf(m[i][v], m[i][v], part);
             if (a.gate) {
                 float g[V];
-                gw[i].to(g);
+                if (RING) SlotT::read(in_gate(stage), threads, i, high(a.gate + row * a.gs, i), g);
+                else gw[i].to(g);
                 if (a.act == GDN_ACT_SILU) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) m[i][v] *= silu(g[v]);
@@ -160,15 +274,17 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
             if (a.gate_first)
 #pragma unroll
                 for (int v = 0; v < V; ++v) part = fmaf(m[i][v], m[i][v], part);
-            if (ok[i]) sum += part;
-            if (a.residual) {
-                rw[i].to(r[i]);
-            } else {
+            if (ok(i)) sum += part;
+            if (!a.residual) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) r[i][v] = 0.f;
+            } else if (RING) {
+                SlotR::read(in_residual(stage), threads, i, high(a.residual + row * a.rs, i), r[i]);
+            } else {
+                rw[i].to(r[i]);
             }
         }
-        if (AHEAD) fetch(min(row + step, a.rows - 1));
+        fetch(row + (RING ? a.ahead : 1) * step, stage);
         float inv = a.scale;
         if (a.weight)
             inv *= rsqrtf(fmaf(row_sum<BLOCK>(sum, lanes, sums[turn][0]), a.inv_dim, a.eps));
@@ -177,20 +293,20 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
         for (int i = 0; i < I; ++i) {
             if (a.weight) {
                 float u[V];
-                if (!AHEAD) load_f<V>(a.weight + c[i], u);
+                if (RING) weight(a.weight, 0, i, u);
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    r[i][v] = fmaf(m[i][v] * inv, AHEAD ? w[AHEAD ? i : 0][v] : u[v], r[i][v]);
+                    r[i][v] = fmaf(m[i][v] * inv, !RING ? w[RING ? 0 : i][v] : u[v], r[i][v]);
             } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v) r[i][v] = fmaf(m[i][v], inv, r[i][v]);
             }
-            if (live && ok[i]) store_f<V>(a.out + row * a.os + c[i], r[i]);
+            if (live && ok(i)) store_f<V>(a.out + row * a.os + c(i), r[i]);
             if (a.next_weight) {
                 float part = 0.f;
 #pragma unroll
                 for (int v = 0; v < V; ++v) part = fmaf(r[i][v], r[i][v], part);
-                if (ok[i]) sum += part;
+                if (ok(i)) sum += part;
             }
         }
         if (a.next_weight) {
@@ -198,41 +314,81 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
 #pragma unroll
             for (int i = 0; i < I; ++i) {
                 float u[V];
-                if (!AHEAD) load_f<V>(a.next_weight + c[i], u);
+                if (RING) weight(a.next_weight, 1, i, u);
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    r[i][v] *= inv * (AHEAD ? nw[AHEAD ? i : 0][v] : u[v]);
-                if (live && ok[i]) store_f<V>(a.next + row * a.ns + c[i], r[i]);
+                    r[i][v] *= inv * (!RING ? nw[RING ? 0 : i][v] : u[v]);
+                if (live && ok(i)) store_f<V>(a.next + row * a.ns + c(i), r[i]);
             }
         }
-        if (!AHEAD) fetch(min(row + step, a.rows - 1));
     }
+    if (RING) copies_wait<0>();
 }
 
 // The grid holds what is resident at once (64 registers per thread, 128 in
 // blocks of few words): more blocks would load the weights again.  Measured
 // on 24000 rows of 1024 (128 threads): 6 blocks per SM 55 us, 4 61, 8 59.
 
+// Starts blocks of `threads` for rows of `per` each; `most` is how many run at
+// once as far as registers go.
+template <typename T, typename R, int V, int I, bool BLOCK>
+gdn_status launch_norm(NormArgs<T, R> &a, int threads, int64_t per, int resident,
+                       cudaStream_t stream) {
+    const int64_t blocks = (a.rows + per - 1) / per, most = (int64_t)resident * kGridSms;
+    const int64_t grid = blocks < most ? blocks : most;
+    int64_t bytes = 0;
+    a.ahead = 0;
+    a.staged = false;
+    if (kRing<V, I, BLOCK>) {
+        // As many rows ahead as the passes can use and an SM's shared memory
+        // holds for its blocks, after the weights where one row fits beside them.
+        const int64_t budget = kRingBudget / resident;
+        const int64_t row = (int64_t)threads * ((a.gate ? 2 : 1) * RowSlots<T, V, I>::kBytes +
+                                                (a.residual ? RowSlots<R, V, I>::kBytes : 0));
+        const int64_t weights = (int64_t)threads * 2 * RowSlots<float, V, I>::kBytes;
+        a.row_bytes = (int)row;
+        a.staged = weights + row <= budget;
+        bytes = a.staged ? weights : 0;
+        const int64_t passes = (blocks + grid - 1) / grid;
+        a.ahead = 4;
+        while (a.ahead > 1 && (a.ahead > passes || bytes + a.ahead * row > budget)) a.ahead /= 2;
+        bytes += a.ahead * row;
+        static std::atomic<bool> done[kMaxDevices];
+        if (!raise_shared_memory(
+                done, {reinterpret_cast<const void *>(gdn_norm_kernel<T, R, V, I, BLOCK>)},
+                {(size_t)kRingBudget}))
+            return GDN_ERR_CUDA;
+    }
+    gdn_norm_kernel<T, R, V, I, BLOCK><<<(unsigned)grid, threads, (size_t)bytes, stream>>>(a);
+    return launch_status();
+}
+
 // Rows that share warps.
 template <typename T, typename R, int V, int I>
 gdn_status run_norm_warps(NormArgs<T, R> &a, int words, cudaStream_t stream) {
     a.lanes = 1;
     while (a.lanes * I < words) a.lanes *= 2;
-    const int64_t per = kWarpThreads / a.lanes, blocks = (a.rows + per - 1) / per;
-    const int64_t most = (V * I <= 8 ? 8 : 4) * kGridSms;
-    gdn_norm_kernel<T, R, V, I, false>
-        <<<(unsigned)(blocks < most ? blocks : most), kWarpThreads, 0, stream>>>(a);
-    return launch_status();
+    return launch_norm<T, R, V, I, false>(a, kWarpThreads, kWarpThreads / a.lanes,
+                                          kWarpBlocks<V * I>, stream);
 }
 
 // Blocks that share a row.
 template <typename T, typename R, int V, int I>
 gdn_status run_norm_block(NormArgs<T, R> &a, int words, cudaStream_t stream) {
     const int threads = 32 * ((words + 32 * I - 1) / (32 * I));
-    const int64_t most = (threads <= 384 ? 768 / threads : 1) * kGridSms;
-    gdn_norm_kernel<T, R, V, I, true>
-        <<<(unsigned)(a.rows < most ? a.rows : most), threads, 0, stream>>>(a);
-    return launch_status();
+    const int most = kRing<V, I, true> ? 1024 : 768;
+    return launch_norm<T, R, V, I, true>(a, threads, 1, threads <= most ? most / threads : 1,
+                                         stream);
+}
+
+// Rows in words of four or eight elements.
+template <typename T, typename R, int V>
+gdn_status run_norm(NormArgs<T, R> &a, cudaStream_t stream) {
+    const int words = a.dim / V;
+    if (words <= 32) return run_norm_warps<T, R, V, 1>(a, words, stream);
+    if (words <= 64) return run_norm_warps<T, R, V, 2>(a, words, stream);
+    if (words <= (V == 8 ? 1024 : 768)) return run_norm_block<T, R, V, 1>(a, words, stream);
+    return run_norm_block<T, R, V, 16 / V>(a, words, stream);
 }
 
 template <typename T, typename R>
@@ -274,14 +430,9 @@ gdn_status norm_typed(const gdn_norm_problem &p, const void *y, const float *wei
                whole(d, next_weight, 0, 4);
     };
     constexpr int V = kWide<T>;
-    if (words_of(V)) {
-        const int words = p.dim / V;
-        if (words <= 32) return run_norm_warps<T, R, V, 1>(a, words, stream);
-        if (words <= 64) return run_norm_warps<T, R, V, 2>(a, words, stream);
-        if (words <= (V == 8 ? 1024 : 768)) return run_norm_block<T, R, V, 1>(a, words, stream);
-        if (words <= 2048) return run_norm_block<T, R, V, 4>(a, words, stream);
-        if constexpr (V == 4) return run_norm_block<T, R, V, 8>(a, words, stream);
-    }
+    if (words_of(V)) return run_norm<T, R, V>(a, stream);
+    if constexpr (V == 8)
+        if (words_of(4)) return run_norm<T, R, 4>(a, stream);
     if constexpr (sizeof(T) == 2) {
         const int words = p.dim / 2;
         if (words_of(2)) {

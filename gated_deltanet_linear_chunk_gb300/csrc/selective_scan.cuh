@@ -43,16 +43,12 @@
 // take 29 us, step 3's fp32 operations 42.
 #pragma once
 
-#include <atomic>
-#include <initializer_list>
-
 #include "block.cuh"
 #include "sm103.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr int kMaxThreads = 128;
 constexpr int kUnroll = 4;      // tokens in flight per thread
 
@@ -797,23 +793,6 @@ template <typename T> ScanArgs<T> scan_args(const gdn_ssm_problem &p, const Scan
     a.carry = static_cast<float *>(p.workspace);
     a.steps = a.carry + (int64_t)(pl.W > 1 ? pl.W - 1 : 0) * a.D * a.S;
     return a;
-}
-
-// Blocks of full size need more shared memory than a kernel has by default:
-// the limit is raised once per device and variant.
-inline bool raise_shared_memory(std::atomic<bool> (&done)[kMaxDevices],
-                         std::initializer_list<const void *> kernels,
-                         std::initializer_list<size_t> bytes) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
-    if (done[dev].load(std::memory_order_acquire)) return true;
-    auto size = bytes.begin();
-    for (const void *k : kernels)
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)*size++) != cudaSuccess)
-            return false;
-    done[dev].store(true, std::memory_order_release);
-    return true;
 }
 
 template <typename T, int NS, bool SHIFT>

@@ -21,7 +21,8 @@
 // 16 bytes, five blocks per SM, 8 tokens ahead, 35 us (98 registers a thread
 // leave too few warps to cover a group's wait); 8-byte words with five, four
 // and three blocks 33, 35 and 37; rows loaded into registers four ahead 49;
-// runs of up to 96 tokens in place of 64, 33 (a longer last wave); weights staged in single floats 31.
+// runs of up to 96 tokens in place of 64, 33 (a longer last wave); weights
+// staged in single floats 31.
 // The step keeps 16-byte words: 256 sequences take 11 us for 42 MB, half of it
 // the launch, the weights and the first loads.
 #include <type_traits>
@@ -97,16 +98,6 @@ __device__ __forceinline__ Vec<T, V> tap(const ConvArgs<T> &a, int n, int start,
     const int r = K - 1 + pos - start;
     if (!a.init || r < 0) return Vec<T, V>::zero();
     return Vec<T, V>::load(a.init + ((int64_t)n * (K - 1) + r) * a.C + c);
-}
-
-// A word's elements as pairs (an element alone: with a zero).
-template <typename T, int V, int P>
-__device__ __forceinline__ void pairs(const Vec<T, V> &x, uint64_t (&p)[P]) {
-    float r[2 * P];
-    r[2 * P - 1] = 0.f;
-    x.to(r);
-#pragma unroll
-    for (int i = 0; i < P; ++i) p[i] = pack2f(r[2 * i], r[2 * i + 1]);
 }
 
 // The states after the sequences' last tokens.  One thread per sequence and
@@ -192,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<K>) gdn_short_conv_kernel(co
         for (int j = 0; j < K - 1; ++j)
             word[j] = tap<T, V, K>(a, s.n, s.start, t0 - (K - 1) + j, c);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) pairs(word[j], in[j]);
+        for (int j = 0; j < K - 1; ++j) to_pairs<V>(word[j], in[j]);
     }
     stage_weights<K>(sw, a.weight, c0, a.C, a.tx * V);
     if (!live) return;
@@ -208,20 +199,19 @@ __global__ void __launch_bounds__(kThreads, kBlocks<K>) gdn_short_conv_kernel(co
     }
     T *to = a.out + t0 * a.os + c;
     auto token = [&](int t, int slot) {
-        pairs(arrived(t, slot), in[K - 1]);
-        float y[2 * P];
+        to_pairs<V>(arrived(t, slot), in[K - 1]);
+        uint64_t sum[P];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            uint64_t sum = b[i];
+            sum[i] = b[i];
 #pragma unroll
-            for (int j = 0; j < K; ++j) sum = ffma2(w[j][i], in[j][i], sum);
-            if (a.act) sum = silu2(sum);
-            const float2 v = unpack2f(sum);
-            y[2 * i] = v.x;
-            y[2 * i + 1] = v.y;
+            for (int j = 0; j < K; ++j) sum[i] = ffma2(w[j][i], in[j][i], sum[i]);
+            if (a.act) sum[i] = silu2(sum[i]);
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) in[j][i] = in[j + 1][i];
         }
+        float y[V];
+        from_pairs<V>(sum, y);
         Word::from(y).store(to);
         to += a.os;
     };
@@ -239,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<K>) gdn_short_conv_kernel(co
                     s = next_span(a.cu, a.N, a.T_, s);
 #pragma unroll
                     for (int j = 0; j < K - 1; ++j)
-                        pairs(tap<T, V, K>(a, s.n, s.start, tok - (K - 1) + j, c), in[j]);
+                        to_pairs<V>(tap<T, V, K>(a, s.n, s.start, tok - (K - 1) + j, c), in[j]);
                 }
                 token(tok, slot + tok - t);
             }

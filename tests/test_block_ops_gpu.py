@@ -105,6 +105,13 @@ def test_conv_widths(K, C):
     check_conv(LENS["ragged"], C, K, torch.float32, True, K % 2 == 1, "silu", False)
 
 
+@pytest.mark.parametrize("C", [2, 4, 6, 12, 20, 516, 1028])
+@pytest.mark.parametrize("K", [3, 4, 8])
+def test_conv_narrow_words(K, C):
+    """Rows of 16-bit elements at 4- and 8-byte boundaries."""
+    check_conv(LENS["ragged"], C, K, torch.bfloat16, True, True, "silu", False)
+
+
 @pytest.mark.parametrize("wide", ["even", "odd"])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_conv_strided_rows(wide, dtype):
@@ -368,6 +375,38 @@ def test_norm_parts(gate, first, weight, residual, nxt):
 def test_norm_rows_and_strides(rows, wide):
     check_norm(rows, 128, torch.bfloat16, torch.float32, True, True, True, True, True, wide=wide)
     check_norm(rows, 600, torch.bfloat16, torch.bfloat16, True, True, False, True, True, wide=wide)
+
+
+@pytest.mark.parametrize("dim", [4, 12, 100, 260, 1028, 3788, 4100])
+@pytest.mark.parametrize("types", ["bf16-bf16", "bf16-f32"])
+@pytest.mark.parametrize("wide", [False, "even"])
+def test_norm_words_of_four(dim, types, wide):
+    """Rows of 16-bit elements at 8-byte boundaries only."""
+    dt, rdt = (TYPES[k] for k in types.split("-"))
+    check_norm(7, dim, dt, rdt, True, True, True, True, True, wide=wide)
+
+
+@pytest.mark.parametrize("rows,dim", [(700, 8200), (500, 8203), (500, 9002), (2000, 4100),
+                                      (1300, 4101), (200, 16384)])
+@pytest.mark.parametrize("types", ["bf16-bf16", "bf16-f32", "f32-f32"])
+@pytest.mark.parametrize("parts", ["all", "residual", "gate"])
+def test_norm_long_rows_in_turn(rows, dim, types, parts):
+    """Blocks that take several long rows, the next ones on their way."""
+    dt, rdt = (TYPES[k] for k in types.split("-"))
+    check_norm(rows, dim, dt, rdt, True, parts != "residual", False, parts != "gate",
+               parts != "residual", wide="odd" if parts == "gate" else False)
+
+
+def test_norm_long_rows_in_place():
+    """out over y, next over the gate, where later rows are copied ahead."""
+    d = Draw(4)
+    for rows, dim in ((700, 8200), (700, 9001), (400, 9002)):
+        y, g, r = (d(rows, dim, dtype=torch.bfloat16) for _ in range(3))
+        w, v = d(dim), d(dim)
+        out, nxt = gdn.gdn_norm_gate_residual(y, w, g, r, v)
+        y2, g2 = y.clone(), g.clone()
+        o, n = gdn.gdn_norm_gate_residual(y2, w, g2, r, v, out=y2, next_out=g2)
+        assert torch.equal(o, out) and torch.equal(n, nxt)
 
 
 def test_norm_in_place():
