@@ -81,15 +81,18 @@ template <bool BLOCK> __device__ __forceinline__ float row_sum(float v, int lane
     return warp_sum(v);
 }
 
-// Where a lane's next rows wait.  In registers, one row ahead, where its part
-// is up to 8 elements in 4 words (16 for rows within a warp); else in a ring in
-// shared memory, up to four rows ahead, through asynchronous copies: 16 elements with
-// the weights and another row's words leave no registers.  (us without rows
-// ahead and with the ring: 2436 rows of 10088 46 and 31, 2590 of 9488 53 and
-// 35, 791 of 11624 in fp32 42 and 22, 2552 of 9629 163 and 123.  Few narrow
-// words are bound by their instructions: 9965 rows of 2466 take 38 in
-// registers and 50 with a ring.)
-template <int V, int I, bool BLOCK> constexpr bool kRing = BLOCK && (V * I > 8 || I > 4);
+// Where a lane's next rows wait.  In registers, one row ahead, or (RING) in a
+// ring in shared memory, up to four rows ahead, through asynchronous copies:
+//  - Long rows, a lane's 16 elements, with the weights and another row's words
+//    leave no registers (us without rows ahead and with the ring: 2436 rows of
+//    10088 46 and 31, 2590 of 9488 53 and 35, 791 of 11624 in fp32 42 and 22,
+//    2552 of 9629 163 and 123).
+//  - Words of four elements ahead in registers are few bytes in flight (in
+//    registers and in the ring: 20617 rows of 1192 in fp32 57 and 36, 23630 of
+//    1040 80 and 73), if a block takes several rows (31 rows of 2016 2.6 and 2.9).
+//  - Words of eight are enough in registers (12047 rows of 2040 36.5 and 38),
+//    and narrower ones are bound by their instructions (9965 of 2466 38 and 50).
+template <int V, int I> constexpr bool kLongRow = V * I > 8 || I > 4;
 // Blocks per SM of the rows that share warps, by the elements of a lane.
 template <int N> constexpr int kWarpBlocks = N <= 8 ? 8 : 4;
 // A block that shares one row has at most this many threads.
@@ -138,10 +141,10 @@ template <typename E, int V, int I> struct RowSlots {
 // first reduction of the one at hand.  Words past the row's end hold anything
 // and are left out of sums and stores.  The gate commutes with the norm's
 // factor, so a lane keeps only y times the gate and the residual.
-template <typename T, typename R, int V, int I, bool BLOCK>
+template <typename T, typename R, int V, int I, bool BLOCK, bool RING>
 __global__ void __launch_bounds__(BLOCK ? kRowThreads : kWarpThreads)
 gdn_norm_kernel(const NormArgs<T, R> a) {
-    constexpr bool RING = kRing<V, I, BLOCK>;
+    constexpr bool HELD = !BLOCK || !kLongRow<V, I>;  // the weights are in registers
     using SlotT = RowSlots<T, V, I>;
     using SlotR = RowSlots<R, V, I>;
     using SlotW = RowSlots<float, V, I>;
@@ -208,8 +211,8 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
         }
         copies_commit();
     };
-    float w[RING ? 1 : I][V], nw[RING ? 1 : I][V];
-    if (RING && a.staged)
+    float w[HELD ? I : 1][V], nw[HELD ? I : 1][V];
+    if (!HELD && a.staged)
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             if (!ok(i)) break;
@@ -222,11 +225,12 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
             fetch(row + k * step, ring + k * a.row_bytes);
     else
         fetch(row, nullptr);
-    if (!RING)
+    if (HELD)
 #pragma unroll
         for (int i = 0; i < I; ++i) {
-            if (a.weight) load_f<V>(a.weight + c(i), w[i]);
-            if (a.next_weight) load_f<V>(a.next_weight + c(i), nw[i]);
+            const int at = ok(i) ? c(i) : 0;
+            if (a.weight) load_f<V>(a.weight + at, w[i]);
+            if (a.next_weight) load_f<V>(a.next_weight + at, nw[i]);
         }
     auto weight = [&](const float *all, int second, int i, float *to) {
         if (a.staged)
@@ -293,10 +297,10 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
         for (int i = 0; i < I; ++i) {
             if (a.weight) {
                 float u[V];
-                if (RING) weight(a.weight, 0, i, u);
+                if (!HELD) weight(a.weight, 0, i, u);
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    r[i][v] = fmaf(m[i][v] * inv, !RING ? w[RING ? 0 : i][v] : u[v], r[i][v]);
+                    r[i][v] = fmaf(m[i][v] * inv, HELD ? w[HELD ? i : 0][v] : u[v], r[i][v]);
             } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v) r[i][v] = fmaf(m[i][v], inv, r[i][v]);
@@ -314,10 +318,10 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
 #pragma unroll
             for (int i = 0; i < I; ++i) {
                 float u[V];
-                if (RING) weight(a.next_weight, 1, i, u);
+                if (!HELD) weight(a.next_weight, 1, i, u);
 #pragma unroll
                 for (int v = 0; v < V; ++v)
-                    r[i][v] *= inv * (!RING ? nw[RING ? 0 : i][v] : u[v]);
+                    r[i][v] *= inv * (HELD ? nw[HELD ? i : 0][v] : u[v]);
                 if (live && ok(i)) store_f<V>(a.next + row * a.ns + c(i), r[i]);
             }
         }
@@ -329,9 +333,9 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
 // blocks of few words): more blocks would load the weights again.  Measured
 // on 24000 rows of 1024 (128 threads): 6 blocks per SM 55 us, 4 61, 8 59.
 
-// Starts blocks of `threads` for rows of `per` each; `most` is how many run at
-// once as far as registers go.
-template <typename T, typename R, int V, int I, bool BLOCK>
+// Starts blocks of `threads` for rows of `per` each, `resident` of them on an
+// SM as far as registers go.
+template <typename T, typename R, int V, int I, bool BLOCK, bool RING>
 gdn_status launch_norm(NormArgs<T, R> &a, int threads, int64_t per, int resident,
                        cudaStream_t stream) {
     const int64_t blocks = (a.rows + per - 1) / per, most = (int64_t)resident * kGridSms;
@@ -339,7 +343,7 @@ gdn_status launch_norm(NormArgs<T, R> &a, int threads, int64_t per, int resident
     int64_t bytes = 0;
     a.ahead = 0;
     a.staged = false;
-    if (kRing<V, I, BLOCK>) {
+    if (RING) {
         // As many rows ahead as the passes can use and an SM's shared memory
         // holds for its blocks, after the weights where one row fits beside them.
         const int64_t budget = kRingBudget / resident;
@@ -347,7 +351,7 @@ gdn_status launch_norm(NormArgs<T, R> &a, int threads, int64_t per, int resident
                                                 (a.residual ? RowSlots<R, V, I>::kBytes : 0));
         const int64_t weights = (int64_t)threads * 2 * RowSlots<float, V, I>::kBytes;
         a.row_bytes = (int)row;
-        a.staged = weights + row <= budget;
+        a.staged = kLongRow<V, I> && weights + row <= budget;
         bytes = a.staged ? weights : 0;
         const int64_t passes = (blocks + grid - 1) / grid;
         a.ahead = 4;
@@ -355,11 +359,12 @@ gdn_status launch_norm(NormArgs<T, R> &a, int threads, int64_t per, int resident
         bytes += a.ahead * row;
         static std::atomic<bool> done[kMaxDevices];
         if (!raise_shared_memory(
-                done, {reinterpret_cast<const void *>(gdn_norm_kernel<T, R, V, I, BLOCK>)},
+                done, {reinterpret_cast<const void *>(gdn_norm_kernel<T, R, V, I, BLOCK, RING>)},
                 {(size_t)kRingBudget}))
             return GDN_ERR_CUDA;
     }
-    gdn_norm_kernel<T, R, V, I, BLOCK><<<(unsigned)grid, threads, (size_t)bytes, stream>>>(a);
+    gdn_norm_kernel<T, R, V, I, BLOCK, RING>
+        <<<(unsigned)grid, threads, (size_t)bytes, stream>>>(a);
     return launch_status();
 }
 
@@ -368,17 +373,24 @@ template <typename T, typename R, int V, int I>
 gdn_status run_norm_warps(NormArgs<T, R> &a, int words, cudaStream_t stream) {
     a.lanes = 1;
     while (a.lanes * I < words) a.lanes *= 2;
-    return launch_norm<T, R, V, I, false>(a, kWarpThreads, kWarpThreads / a.lanes,
-                                          kWarpBlocks<V * I>, stream);
+    return launch_norm<T, R, V, I, false, false>(a, kWarpThreads, kWarpThreads / a.lanes,
+                                                 kWarpBlocks<V * I>, stream);
 }
 
 // Blocks that share a row.
 template <typename T, typename R, int V, int I>
 gdn_status run_norm_block(NormArgs<T, R> &a, int words, cudaStream_t stream) {
     const int threads = 32 * ((words + 32 * I - 1) / (32 * I));
-    const int most = kRing<V, I, true> ? 1024 : 768;
-    return launch_norm<T, R, V, I, true>(a, threads, 1, threads <= most ? most / threads : 1,
-                                         stream);
+    // Blocks per SM with a ring (64 registers a thread), and without.
+    const int ring = 1024 / threads, held = threads <= 768 ? 768 / threads : 1;
+    if constexpr (kLongRow<V, I>) {
+        return launch_norm<T, R, V, I, true, true>(a, threads, 1, ring, stream);
+    } else {
+        if constexpr (V == 4)
+            if (a.rows > ring * kGridSms)
+                return launch_norm<T, R, V, I, true, true>(a, threads, 1, ring, stream);
+        return launch_norm<T, R, V, I, true, false>(a, threads, 1, held, stream);
+    }
 }
 
 // Rows in words of four or eight elements.

@@ -387,7 +387,7 @@ def test_norm_words_of_four(dim, types, wide):
 
 
 @pytest.mark.parametrize("rows,dim", [(700, 8200), (500, 8203), (500, 9002), (2000, 4100),
-                                      (1300, 4101), (200, 16384)])
+                                      (1300, 4101), (200, 16384), (3000, 1028)])
 @pytest.mark.parametrize("types", ["bf16-bf16", "bf16-f32", "f32-f32"])
 @pytest.mark.parametrize("parts", ["all", "residual", "gate"])
 def test_norm_long_rows_in_turn(rows, dim, types, parts):
