@@ -238,6 +238,12 @@ __device__ __forceinline__ void copy_async(void *smem, const void *gmem) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(gmem), "n"(BYTES)
                      : "memory");
 }
+// The first `bytes` of 16; the rest becomes zero.
+__device__ __forceinline__ void copy_async_head(void *smem, const void *gmem, int bytes) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(gmem), "r"(bytes)
+                 : "memory");
+}
 // 16 bytes that are not read again soon.
 __device__ __forceinline__ uint64_t evict_first_policy() {
     uint64_t policy;

@@ -193,34 +193,38 @@ template <typename T, int NS> struct ScanThread {
 // words, or element by element (16-bit rows at odd elements).
 enum CopyWord : int { kCopy16 = 16, kCopy4 = 4, kCopyElement = 0 };
 
+// Lanes that share a row of `words` copies: a power of two, as its logarithm.
+__device__ __forceinline__ int row_lanes(int words) { return words > 16 ? 5 : 32 - __clz(words - 1); }
+
 // `rows` rows of `cols` elements from `src` (rows `stride` apart) to `dst`
-// (rows `pitch` apart): a warp takes every n-th row, its lanes the row's words.
+// (rows `pitch` apart): 2^lg lanes take a row's words.
 template <typename T>
 __device__ __forceinline__ void copy_rows(T *dst, int pitch, const T *src, int64_t stride,
-                                          int rows, int cols, int word) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+                                          int rows, int cols, int word, int lg) {
+    const int lane = threadIdx.x & ((1 << lg) - 1), first = threadIdx.x >> lg;
+    const int apart = blockDim.x >> lg;
     if (word == kCopyElement) {
         // Four rows' loads before the first store.
-        for (int c = lane; c < cols; c += 32)
-            for (int r0 = warp; r0 < rows; r0 += 4 * warps) {
+        for (int c = lane; c < cols; c += 1 << lg)
+            for (int r0 = first; r0 < rows; r0 += 4 * apart) {
                 T v[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (r0 + k * warps < rows) v[k] = src[(r0 + k * warps) * stride + c];
+                    if (r0 + k * apart < rows) v[k] = src[(r0 + k * apart) * stride + c];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (r0 + k * warps < rows) dst[(r0 + k * warps) * pitch + c] = v[k];
+                    if (r0 + k * apart < rows) dst[(r0 + k * apart) * pitch + c] = v[k];
             }
         return;
     }
     const int step = word == kCopy16 ? kWide<T> : 4 / (int)sizeof(T);
-    for (int c = lane * step; c < cols; c += 32 * step) {
-        int r = warp;
+    for (int c = lane * step; c < cols; c += step << lg) {
+        int r = first;
         const T *from = src + r * stride + c;
         T *to = dst + r * pitch + c;
-        const int64_t next = warps * stride;
+        const int64_t next = apart * stride;
 #pragma unroll 4
-        for (; r < rows; r += warps, from += next, to += warps * pitch) {
+        for (; r < rows; r += apart, from += next, to += apart * pitch) {
             if (word == kCopy16) copy_async<16>(to, from);
             else copy_async<4>(to, from);
         }
@@ -233,9 +237,30 @@ template <typename T> __device__ __forceinline__ int shift_of(const T *p) {
 }
 
 // The same for rows at any alignment: element c of a row goes to place
-// c + shift_of(row), so that all but the row's ends are copied in whole
-// 16-byte words, the ends in 4-byte ones.  (A first 16-bit element in the
-// upper half of its 4-byte word is left to copy_first.)
+// c + shift_of(row).  Whole 16-byte words from the one that holds the row's
+// first element on, the last one's first bytes: what comes before the row is
+// in the tensor too, the row before it or its own earlier columns.
+template <typename T>
+__device__ __forceinline__ void copy_rows_over(T *dst, int pitch, const T *src, int64_t stride,
+                                               int rows, int cols, int lg) {
+    constexpr int V = kWide<T>;
+    const int lane = threadIdx.x & ((1 << lg) - 1), apart = blockDim.x >> lg;
+    int r = threadIdx.x >> lg;
+    const T *from = src + r * stride;
+    T *to = dst + r * pitch;
+    const int64_t next = apart * stride;
+#pragma unroll 4
+    for (; r < rows; r += apart, from += next, to += apart * pitch) {
+        const int o = shift_of(from), n = o + cols;
+        for (int k = lane * V; k < n; k += V << lg)
+            copy_async_head(to + k, from - o + k, min(16, (n - k) * (int)sizeof(T)));
+    }
+}
+
+// The same for a tensor's first tokens and channels, where nothing comes before:
+// all but the row's ends in whole 16-byte words, the ends in 4-byte ones.  (A
+// first 16-bit element in the upper half of its 4-byte word is left to
+// copy_first.)
 template <typename T>
 __device__ __forceinline__ void copy_rows_shifted(T *dst, int pitch, const T *src, int64_t stride,
                                                   int rows, int cols) {
@@ -285,8 +310,14 @@ template <typename T, int NS, bool OUT, bool SHIFT> struct ScanTiles {
     T *ins;        // [x, dt, z][token][channel], of every tile
     int width;     // channels per block
     int pitch;     // elements between rows of `ins`
-    __device__ ScanTiles(char *smem, int threads) : width(threads * CH) {
+    int in_lanes, bc_lanes;  // that share a row, as logarithms
+    __device__ ScanTiles(char *smem, int threads, int cols, int states, int bc_word)
+        : width(threads * CH) {
         pitch = width + (SHIFT ? kWide<T> : 0);
+        in_lanes = row_lanes((cols - 1 + (SHIFT ? kWide<T> - 1 : 0)) / kWide<T> + 1);
+        bc_lanes = row_lanes(bc_word == kCopyElement ? states
+                             : bc_word == kCopy16    ? (states - 1) / kWide<T> + 1
+                                                     : (states - 1) / (4 / (int)sizeof(T)) + 1);
         bc = reinterpret_cast<float *>(smem);
         raws = reinterpret_cast<T *>(bc + kBC * kTile * NS);
         ins = raws + kTiles * kBC * kTile * NS;
@@ -308,17 +339,21 @@ template <typename T, int NS, bool OUT, bool SHIFT> struct ScanTiles {
                                  OUT && a.z ? a.z + t * a.zs + d : nullptr};
         const int64_t stride[3] = {a.xs, a.dts, a.zs};
         T *const dst[3] = {in(buf), in(buf) + kTile * pitch, in(buf) + 2 * kTile * pitch};
+        // Whether a word that holds a row's first element may begin before the tensor.
+        const bool start =
+            t * min(min(a.xs, a.dts), OUT && a.z ? a.zs : a.xs) + d < kWide<T> - 1;
 #pragma unroll
         for (int k = 0; k < kIn; ++k) {
             if (k == 2 && !a.z) break;
-            if (SHIFT) copy_rows_shifted(dst[k], pitch, src[k], stride[k], rows, cols);
-            else copy_rows(dst[k], pitch, src[k], stride[k], rows, cols, kCopy16);
+            if (!SHIFT) copy_rows(dst[k], pitch, src[k], stride[k], rows, cols, kCopy16, in_lanes);
+            else if (!start) copy_rows_over(dst[k], pitch, src[k], stride[k], rows, cols, in_lanes);
+            else copy_rows_shifted(dst[k], pitch, src[k], stride[k], rows, cols);
         }
-        copy_rows(raw(buf), NS, a.B + t * a.bs + group * a.S, a.bs, rows, a.S, a.bc_word);
+        copy_rows(raw(buf), NS, a.B + t * a.bs + group * a.S, a.bs, rows, a.S, a.bc_word, bc_lanes);
         if (OUT)
             copy_rows(raw(buf) + kTile * NS, NS, a.C + t * a.cs + group * a.S, a.cs, rows, a.S,
-                      a.bc_word);
-        if (SHIFT && sizeof(T) == 2) copy_first(dst, pitch, src, stride, rows);
+                      a.bc_word, bc_lanes);
+        if (SHIFT && start && sizeof(T) == 2) copy_first(dst, pitch, src, stride, rows);
     }
     // B and C of the tile that has arrived, to fp32.
     __device__ __forceinline__ void widen(const ScanArgs<T> &a, int buf) const {
@@ -394,10 +429,11 @@ template <typename T, int NS, bool OUT, bool SHIFT>
 __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(const ScanArgs<T> a) {
     constexpr int CH = kChannels<NS>, kTile = kTileOf<T, CH>, kTiles = kTilesOf<T, CH>;
     extern __shared__ __align__(16) char smem[];
-    const ScanTiles<T, NS, OUT, SHIFT> tl(smem, blockDim.x);
-    const int group = blockIdx.x / a.tiles, in_group0 = (blockIdx.x % a.tiles) * tl.width;
+    const int group = blockIdx.x / a.tiles;
+    const int in_group0 = (blockIdx.x % a.tiles) * (int)blockDim.x * CH;
     const int w = blockIdx.y, d0 = group * a.per_group + in_group0;
-    const int cols = min(tl.width, a.per_group - in_group0);
+    const int cols = min((int)blockDim.x * CH, a.per_group - in_group0);
+    const ScanTiles<T, NS, OUT, SHIFT> tl(smem, blockDim.x, cols, a.S, a.bc_word);
     if (OUT && w >= a.W) {
         copy_empty(a, w - a.W, gridDim.y - a.W, d0, cols);
         return;
