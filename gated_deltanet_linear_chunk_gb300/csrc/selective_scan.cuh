@@ -790,13 +790,26 @@ inline ScanPlan scan_plan(const gdn_ssm_problem &p) {
     while (s.ns < p.state_dim) s.ns *= 2;
     const int ch = channels_per_thread(s.ns), resident = resident_blocks(s.ns);
     const int per_group = p.channels / p.num_groups;
-    const int warps = (per_group + 32 * ch - 1) / (32 * ch), most = kMaxThreads / 32;
-    s.threads = 32 * (warps < most ? warps : most);
-    s.tiles = (per_group + s.threads * ch - 1) / (s.threads * ch);
-    // One wave of blocks.
-    const int64_t blocks = (int64_t)p.num_groups * s.tiles;
-    int64_t W = (int64_t)resident * kGridSms * (kMaxThreads / s.threads) / blocks;
+    const int warps = (per_group + 32 * ch - 1) / (32 * ch);
     const int64_t short_enough = p.total_tokens / kMinWindow;
+    // One wave of blocks of up to `most` warps.
+    auto cut = [&](int most) {
+        s.threads = 32 * (warps < most ? warps : most);
+        s.tiles = (per_group + s.threads * ch - 1) / (s.threads * ch);
+        return (int64_t)resident * kGridSms * (kMaxThreads / s.threads) /
+               ((int64_t)p.num_groups * s.tiles);
+    };
+    int64_t W = cut(kMaxThreads / 32);
+    // Two warps where that leaves fewer channels' threads idle and so gives
+    // more windows: 35879 x 1246 in 2 groups, 91 windows for 76, 441 us for
+    // 492; 48014 x 3232 in 4, 32 for 28, 815 for 919.  (Elsewhere they read B
+    // and C more often: 60 x 3496 19 for 20.5; with 64 states 847 for 955
+    // although 13 windows for 12.)
+    if (s.ns <= 16 && W < short_enough) {
+        const int64_t narrow = cut(2);
+        if (narrow > W) W = narrow;
+        else W = cut(kMaxThreads / 32);
+    }
     W = W < short_enough ? W : short_enough;
     // Two windows do 1.4 times the work of one for twice the blocks, with two
     // more launches: not worth it (2000 x 128: 440 us against 538, 128 x 1024
