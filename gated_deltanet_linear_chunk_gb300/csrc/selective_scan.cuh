@@ -779,6 +779,10 @@ struct ScanPlan {
 // The shortest window.  (128 tokens of 1024 channels, us by windows: 1 35, 4 21,
 // 8 14, 16 12.5, 24 12.2, 48 18; 64 tokens of 6144: 1 19.5, 4 21, 8 18, 24 24.)
 constexpr int kMinWindow = 8;
+// Windows whose states are joined in one run.  Up to twice as many windows of
+// less than 16 tokens are not worth the runs: 512 tokens of 2048 channels, 33
+// windows 25 us, 57 26; 512 of 1024, 33 windows 18.4, 64 20; 400 of 512 15, 50 17.
+constexpr int kFewWindows = 33;
 
 // kChannels and kResident of the variant that runs.
 inline int channels_per_thread(int ns) { return ns <= 32 ? 2 : 1; }
@@ -811,6 +815,7 @@ inline ScanPlan scan_plan(const gdn_ssm_problem &p) {
         else W = cut(kMaxThreads / 32);
     }
     W = W < short_enough ? W : short_enough;
+    if (W > kFewWindows && W <= 2 * kFewWindows && p.total_tokens < 16 * W) W = kFewWindows;
     // Two windows do 1.4 times the work of one for twice the blocks, with two
     // more launches: not worth it (2000 x 128: 440 us against 538, 128 x 1024
     // 33 against 35, 4000 x 6144 1249 against 987).
@@ -872,14 +877,17 @@ gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cuda
             <<<dim3(blocks, pl.W - 1), pl.threads, in_bytes, stream>>>(a);
         if (launch_status() != GDN_OK) return GDN_ERR_CUDA;
         // Eight windows are loaded at once: more than a few rounds of them
-        // are cut into runs.
-        const bool runs = pl.W - 1 > 32;
-        const int64_t each = kCombineThreads / (runs ? 16 : 1);
+        // are cut into runs.  (512 tokens of 2048 channels in 57 windows, the
+        // whole call: 16 runs 29 us, 4 runs 26; 8000 of 256 in 128 windows: 35
+        // and 33 us, 2000 of 128 in 128: 18.5 and 19.)
+        const int runs = pl.W <= kFewWindows ? 1 : pl.W <= 2 * kFewWindows ? 4 : 16;
+        const int64_t each = kCombineThreads / runs;
         cfg.gridDim = dim3((unsigned)((ds + each - 1) / each));
         cfg.blockDim = dim3(kCombineThreads);
         cfg.dynamicSmemBytes = pl.W - 1;
-        if (cudaLaunchKernelEx(&cfg, runs ? gdn_scan_combine_kernel<T, 16>
-                                          : gdn_scan_combine_kernel<T, 1>, a) != cudaSuccess)
+        if (cudaLaunchKernelEx(&cfg, runs == 16  ? gdn_scan_combine_kernel<T, 16>
+                                     : runs == 4 ? gdn_scan_combine_kernel<T, 4>
+                                                 : gdn_scan_combine_kernel<T, 1>, a) != cudaSuccess)
             return GDN_ERR_CUDA;
     }
     const unsigned rows = (unsigned)(pl.W + (empties ? (a.N < kEmptyRows ? a.N : kEmptyRows) : 0));
