@@ -244,6 +244,22 @@ def test_scan_strided_rows(wide, dtype):
     check_scan(LENS["tile"], 72, 7, 3, TYPES[dtype], wide=wide)
 
 
+@pytest.mark.parametrize("d,G", [(1, 1), (3, 1), (3, 3), (5, 1), (9, 3), (67, 1), (130, 2)])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("wide", [False, "even", "odd"])
+def test_scan_unaligned_rows(d, G, dtype, wide):
+    """Rows that start anywhere in a 16-byte word, the tensor's first included."""
+    check_scan([1, 40, 2, 21], d, 4, G, TYPES[dtype], wide=wide)
+    check_scan([230], d, 5, G, TYPES[dtype], gate=False, wide=wide)
+
+
+@pytest.mark.parametrize("d,G,T", [(2048, 1, 1200), (2048, 1, 520), (623, 1, 700), (1246, 2, 900)])
+def test_scan_windows_joined_in_runs(d, G, T):
+    """Window counts that are joined in one, four and sixteen runs, and narrow blocks."""
+    check_scan([T // 2, 0, T - T // 2], d, 3, G, torch.bfloat16)
+    check_scan([T], d, 3, G, torch.float32, gate=False)
+
+
 def test_scan_without_softplus_and_bias():
     """Steps taken as they are, negative ones among them, with growing states."""
     a = scan_args(40, 1, 24, 8, 1, torch.float32, True, True, True, False)
