@@ -34,11 +34,11 @@
 // Windows of a fixed length balance exactly, and a window whose end falls
 // between two sequences skips step 1.
 //
-// Measured, 4000 tokens of 6144 channels and 16 states in bf16: 75 us for step 1,
-// 10 for step 2, 112 for step 3, 185 in all (they overlap at their ends): 393 M
-// (token, channel, state) elements at 9 per clock and SM in step 3.  Issue
-// slots are 58 % busy, the fp32 pipe 54 %, the exponentials' pipe 58 and 43 %
-// (it takes 32 per clock and SM, fp32 128), memory 20 %: 207 instructions per
+// Measured, 4000 tokens of 6144 channels and 16 states in bf16: 74 us for step 1,
+// 10 for step 2, 108 for step 3, 181 in all (they overlap at their ends): 393 M
+// (token, channel, state) elements at 11.6 per clock and SM in step 3.  Issue
+// slots are 58 % busy, the fp32 pipe 55 %, the exponentials' pipe 59 and 45 %
+// (it takes 32 per clock and SM, fp32 128), memory 21 %: 199 instructions per
 // token of two channels, 96 of them the recurrence.  The bytes alone would
 // take 29 us, step 3's fp32 operations 42.
 #pragma once
