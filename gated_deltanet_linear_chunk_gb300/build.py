@@ -51,8 +51,8 @@ def _binding_command(out: str):
             "-I", os.path.join(home, "include"), "-I", sysconfig.get_paths()["include"],
             "-I", os.path.join(cuda, "include"), "-I", INCLUDE,
             os.path.join(CSRC, "block_binding.cpp"), "-o", out,
-            "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
-            "-lc10_cuda"]
+            "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda",
+            "-lc10", "-lc10_cuda"]
 
 
 def _build_binding() -> None:

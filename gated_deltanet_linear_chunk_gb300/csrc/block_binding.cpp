@@ -9,7 +9,7 @@
 // bind() with its error class.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -123,8 +123,9 @@ int64_t taps(const at::Tensor &w) {
     return w.size(1);
 }
 
+// A new tensor beside `first`, without the dispatcher's detour.
 at::Tensor make(at::IntArrayRef shape, at::ScalarType type, const at::Tensor &first) {
-    return at::empty(shape, first.options().dtype(type));
+    return at::detail::empty_cuda(shape, type, first.device(), std::nullopt);
 }
 
 // The device and stream of a call.
