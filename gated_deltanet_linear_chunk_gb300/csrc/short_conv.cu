@@ -385,8 +385,11 @@ gdn_status run_step(const gdn_conv_problem &p, const void *x, const float *weigh
     auto blocks = [&](int run) {
         return (int64_t)a.n_chan * ((p.num_seqs + (int64_t)run * ty - 1) / ((int64_t)run * ty));
     };
+    // Sequences per thread: as many, up to 8, as leave four blocks per SM, or
+    // hardly fewer.  (300 sequences of 6144: 2 8.2 us, 3 6.6, 4 7.0, 8 8.7;
+    // 256 of 10240: 2 11.3, 4 10.3, 6 11.0; 512 of 8192: 4 16.2, 6 14.5, 8 15.5.)
     a.run = 8;
-    while (a.run > 1 && blocks(a.run) < 4 * kGridSms) a.run /= 2;
+    while (a.run > 1 && blocks(a.run) * 50 < 4 * kGridSms * 49) --a.run;
     if (blocks(a.run) > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     gdn_short_conv_step_kernel<T, V, K>
         <<<(unsigned)blocks(a.run), kThreads, (size_t)a.tx * V * K * sizeof(float), stream>>>(a);
