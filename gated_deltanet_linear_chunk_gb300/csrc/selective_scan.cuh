@@ -513,6 +513,16 @@ __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(co
 
 constexpr int kCombineThreads = 256;
 
+// 2^(x / 2), the factor that a window or run multiplies a state by twice.  Whole
+// windows of growing states (A or the steps may have any sign) pass what one
+// fp32 factor holds while the state does not, above all a state that is still
+// zero.  Within 2^-126 .. 2^127 neither factor is zero or infinite: a zero state
+// stays zero and an infinite one infinite, and the two take any fp32 state past
+// either end of the range.
+__device__ __forceinline__ float half_factor(float x) {
+    return ex2(fminf(fmaxf(0.5f * x, -126.f), 127.f));
+}
+
 // States entering the windows: in window order, c <- exp(A sum s) c + h, from
 // the window's own state alone where its last sequence starts inside it.  The
 // steps compose, (h, k) then (h', k') being (k' h + h', k k'), so a block cuts
@@ -550,7 +560,8 @@ __global__ void __launch_bounds__(kCombineThreads) gdn_scan_combine_kernel(const
                 if (w + k >= w1) break;
                 if (inside[w + k]) fresh = true;
                 steps += s[k];
-                c = inside[w + k] ? h[k] : fmaf(ex2(rate * s[k]), c, h[k]);
+                const float f = half_factor(rate * s[k]);
+                c = inside[w + k] ? h[k] : fmaf(f, f * c, h[k]);
                 if (write && ok) a.carry[(w + k) * ds + i] = c;
             }
         }
@@ -560,10 +571,10 @@ __global__ void __launch_bounds__(kCombineThreads) gdn_scan_combine_kernel(const
     bool fresh = false;  // a sequence starts in this run: nothing enters past it
     if (SEG > 1) {
         end[seg][e] = walk(0.f, false, steps, fresh);
-        kept[seg][e] = fresh ? -1.f : ex2(rate * steps);
+        kept[seg][e] = fresh ? -1.f : half_factor(rate * steps);
         __syncthreads();
         for (int k = 0; k < seg; ++k)
-            c = kept[k][e] < 0.f ? end[k][e] : fmaf(kept[k][e], c, end[k][e]);
+            c = kept[k][e] < 0.f ? end[k][e] : fmaf(kept[k][e], kept[k][e] * c, end[k][e]);
     }
     walk(c, true, steps, fresh);
 }
