@@ -197,7 +197,7 @@ template <> struct Vec<float, 2> {
     }
 };
 // Whether element p lies in the upper half of its 4-byte word.
-template <typename T> __device__ __forceinline__ int odd(const T *p) {
+template <typename T> __host__ __device__ __forceinline__ int odd(const T *p) {
     return (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & 1;
 }
 // V elements of a word as pairs (an element alone: with a zero), and back.
@@ -266,6 +266,31 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 // Waits until at most N committed groups of this thread's copies are on their way.
 template <int N> __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// What a copy of the 16-bit element at p reads: its 4-byte word up to the
+// element.  (high: odd(p).)  The element that begins its tensor (`first`) in the
+// upper half of a word has nothing before it that is the tensor's: no bytes are
+// read, and load_first brings it.
+template <typename T> struct ElementWord {
+    const T *from;
+    int bytes;
+};
+template <typename T>
+__host__ __device__ __forceinline__ ElementWord<T> element_word(const T *p, int high, bool first) {
+    return {p - high, high ? first ? 0 : 4 : 2};
+}
+// The 16-bit element at p to its half of a 4-byte word.
+template <typename T>
+__device__ __forceinline__ void copy_async_element(void *smem, const T *p, int high, bool first) {
+    const ElementWord<T> w = element_word(p, high, first);
+    copy_async_part(smem, w.from, w.bytes);
+}
+// A tensor's first element to the place that copy_async_element gave it, once
+// this thread's copies are there.
+template <typename T> __device__ __forceinline__ void load_first(void *smem, const T *p) {
+    if (!odd(p)) return;
+    copies_wait<0>();
+    *static_cast<uint32_t *>(smem) = (uint32_t)*reinterpret_cast<const uint16_t *>(p) << 16;
 }
 
 // A kernel has 48 KB of shared memory by default: for more the limit is raised

@@ -107,11 +107,12 @@ template <typename E, int V, int I> struct RowSlots {
     __device__ __forceinline__ static char *piece(char *base, int threads, int i, int k) {
         return base + ((i * kPieces + k) * threads + threadIdx.x) * kPiece;
     }
-    // high: whether a single 16-bit element lies in its 4-byte word's upper half.
+    // high: whether a single 16-bit element lies in its 4-byte word's upper half;
+    // first: whether it is its tensor's first.
     __device__ __forceinline__ static void copy(char *base, int threads, int i, const E *from,
-                                                int high) {
+                                                int high, bool first) {
         if constexpr (V * sizeof(E) == 2) {
-            copy_async_part(piece(base, threads, i, 0), from - high, high ? 4 : 2);
+            copy_async_element(piece(base, threads, i, 0), from, high, first);
         } else {
 #pragma unroll
             for (int k = 0; k < kPieces; ++k)
@@ -184,8 +185,9 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
     char *const staged = ring + a.ahead * a.row_bytes;  // weights
     Words<T, V> yw[I], gw[I];
     Words<R, V> rw[I];
-    // Row r's loads; in the ring's place `stage`, if it exists.
-    auto fetch = [&](int64_t r, char *stage) {
+    // Row r's loads; in the ring's place `stage`, if it exists.  first: this
+    // lane's first words there are the tensors' first.
+    auto fetch = [&](int64_t r, char *stage, bool first) {
         if (!RING) {
             r = min(r, a.rows - 1);
 #pragma unroll
@@ -200,13 +202,14 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
 #pragma unroll
             for (int i = 0; i < I; ++i) {
                 if (!ok(i)) break;
-                SlotT::copy(stage, threads, i, a.y + r * a.ys + c(i), high(a.y + r * a.ys, i));
+                const bool head = first && i == 0;
+                SlotT::copy(stage, threads, i, a.y + r * a.ys + c(i), high(a.y + r * a.ys, i), head);
                 if (a.gate)
                     SlotT::copy(in_gate(stage), threads, i, a.gate + r * a.gs + c(i),
-                                high(a.gate + r * a.gs, i));
+                                high(a.gate + r * a.gs, i), head);
                 if (a.residual)
                     SlotR::copy(in_residual(stage), threads, i, a.residual + r * a.rs + c(i),
-                                high(a.residual + r * a.rs, i));
+                                high(a.residual + r * a.rs, i), head);
             }
         }
         copies_commit();
@@ -216,15 +219,16 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             if (!ok(i)) break;
-            if (a.weight) SlotW::copy(staged, threads, i, a.weight + c(i), 0);
+            if (a.weight) SlotW::copy(staged, threads, i, a.weight + c(i), 0, false);
             if (a.next_weight)
-                SlotW::copy(staged + SlotW::kBytes * threads, threads, i, a.next_weight + c(i), 0);
+                SlotW::copy(staged + SlotW::kBytes * threads, threads, i, a.next_weight + c(i), 0,
+                            false);
         }
     if (RING)
         for (int k = 0; k < a.ahead; ++k)
-            fetch(row + k * step, ring + k * a.row_bytes);
+            fetch(row + k * step, ring + k * a.row_bytes, k == 0 && row == 0 && lane == 0);
     else
-        fetch(row, nullptr);
+        fetch(row, nullptr, false);
     if (HELD)
 #pragma unroll
         for (int i = 0; i < I; ++i) {
@@ -232,6 +236,12 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
             if (a.weight) load_f<V>(a.weight + at, w[i]);
             if (a.next_weight) load_f<V>(a.next_weight + at, nw[i]);
         }
+    if (RING && V * sizeof(T) == 2 && row == 0 && lane == 0) {
+        load_first(SlotT::piece(ring, threads, 0, 0), a.y);
+        if (a.gate) load_first(SlotT::piece(in_gate(ring), threads, 0, 0), a.gate);
+        if (sizeof(R) == 2 && a.residual)
+            load_first(SlotR::piece(in_residual(ring), threads, 0, 0), a.residual);
+    }
     auto weight = [&](const float *all, int second, int i, float *to) {
         if (a.staged)
             SlotW::read(staged + second * SlotW::kBytes * threads, threads, i, 0, to);
@@ -288,7 +298,7 @@ gdn_norm_kernel(const NormArgs<T, R> a) {
                 rw[i].to(r[i]);
             }
         }
-        fetch(row + (RING ? a.ahead : 1) * step, stage);
+        fetch(row + (RING ? a.ahead : 1) * step, stage, false);
         float inv = a.scale;
         if (a.weight)
             inv *= rsqrtf(fmaf(row_sum<BLOCK>(sum, lanes, sums[turn][0]), a.inv_dim, a.eps));

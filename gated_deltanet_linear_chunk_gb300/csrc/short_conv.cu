@@ -144,11 +144,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks<K>) gdn_short_conv_kernel(co
     Slot *ring = reinterpret_cast<Slot *>(sw + a.tx * V * K) + threadIdx.x;
     const T *ahead = a.x + t0 * a.xs + c;  // where copies go on
     int ahead_t = t0, ahead_slot = 0;
-    auto issue = [&] {
+    auto issue = [&](bool first) {
         Slot *to = ring + ahead_slot * kThreads;
         auto copy = [&](int u) {
             if constexpr (sizeof(Word) == 2)
-                copy_async_part(to + u * kThreads, ahead - odd(ahead), odd(ahead) ? 4 : 2);
+                copy_async_element(to + u * kThreads, ahead, odd(ahead), first && u == 0);
             else
                 copy_async<sizeof(Word)>(to + u * kThreads, ahead);
             ahead += a.xs;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<K>) gdn_short_conv_kernel(co
         }
     };
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) issue();
+    for (int g = 0; g < kGroups; ++g) issue(g == 0 && t0 == 0 && c == 0);
 
     // Then, while they come: the sequence, the inputs before the run, the weights.
     Span s{};
@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<K>) gdn_short_conv_kernel(co
         Word::from(y).store(to);
         to += a.os;
     };
+    if (sizeof(Word) == 2 && t0 == 0 && c == 0) load_first(ring, a.x);
     int slot = 0;
     for (int t = t0; t < t1; t += kStep) {
         copies_wait<kGroups - 1>();
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<K>) gdn_short_conv_kernel(co
             }
         }
         slot = slot + kStep == kSlots ? 0 : slot + kStep;
-        issue();
+        issue(false);
     }
 }
 

@@ -13,7 +13,10 @@
  *     contiguous.  Rows of an output must not overlap.
  *   - pointers need only the alignment of their elements.  Whole 16-byte
  *     words are loaded and stored where the rows allow it (pointer, stride and
- *     channel count); other alignments take narrower accesses.
+ *     channel count); other alignments take narrower accesses.  A strided
+ *     input's words between its first row and its last may be read (and are
+ *     not used) where they lie between rows; nothing before its first element
+ *     or after its last one is.
  * dtype is GDN_BF16 or GDN_F32.  Sums, states and statistics are fp32;
  * results are rounded once, to nearest even.
  *
