@@ -152,10 +152,30 @@ template <typename T, int NS> struct ScanThread {
             }
         }
     }
+    // The state after sequence n's last token in window w.  A final state written
+    // over the initial one must wait for the windows that read it: it takes the
+    // place of the state that entered this window, copied by a last launch.
+    __device__ __forceinline__ void finish(const ScanArgs<T> &a, int n, bool from_carry,
+                                           int w) const {
+        if (a.fin && from_carry && a.defer) store(a, a.carry, w - 1);
+        else if (a.fin) store(a, a.fin, n);
+    }
+    // Whether a step times x that was not finite has passed: a padding state (of
+    // S < NS states the last) is then NaN, a state infinite or NaN, and stays so.
+    __device__ __forceinline__ bool spoiled(int S) const {
+        bool r = false;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const float first = unpack2f(h[c][0]).x, last = unpack2f(h[c][NP - 1]).y;
+            r |= c < valid && !((S < NS ? last : 0.f * first) == 0.f);
+        }
+        return r;
+    }
     // One token: x and dt of the channels, B and C of the group; returns C . h.
-    template <bool OUT>
+    // EXACT: the padding states are kept at zero whatever x and dt are.
+    template <bool OUT, bool EXACT = false>
     __device__ __forceinline__ uint64_t token(bool softplus_on, uint64_t x, uint64_t dt,
-                                              const float *sB, const float *sC) {
+                                              const float *sB, const float *sC, int S = NS) {
         // (A choice, not a branch: the tokens of a run are one basic block,
         // which the compiler can interleave.)
         const uint64_t v = fadd2(dt, bias), sp = softplus2(v), s = softplus_on ? sp : v;
@@ -181,6 +201,10 @@ template <typename T, int NS> struct ScanThread {
                     const int p = k / 2 + i;
                     const float2 e = unpack2f(fmul2(s2[c], A[c][p]));
                     h[c][p] = ffma2(pack2f(ex2(e.x), ex2(e.y)), h[c][p], fmul2(u2[c], b[i]));
+                    if (EXACT) {
+                        const float2 f = unpack2f(h[c][p]);
+                        h[c][p] = pack2f(2 * p < S ? f.x : 0.f, 2 * p + 1 < S ? f.y : 0.f);
+                    }
                     if (OUT) y2[c] = ffma2(cc[i], h[c][p], y2[c]);
                 }
         }
@@ -425,8 +449,55 @@ __device__ void copy_empty(const ScanArgs<T> &a, int first, int step, int d0, in
     }
 }
 
-template <typename T, int NS, bool OUT, bool SHIFT>
-__global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(const ScanArgs<T> a) {
+// This thread's channels of window w once more, from the first token `t` of a
+// sequence's part in it, straight from global memory: the padding states are
+// kept at zero and a missing skip is left out, so that tokens that are not
+// finite give the definition's infinities; all others what scan_run gave.
+// (A function of its own, called when a window is done: inside the loop over the
+// tiles it cost the tokens that are finite 2 to 10 %, here 0 to 2; keeping the
+// padding at zero token by token 4 to 10.)
+template <typename T, int NS>
+__device__ __noinline__ void scan_again(const ScanArgs<T> &a, int w, int t, int group,
+                                        int in_group0) {
+    ScanThread<T, NS> th;
+    const int t0 = w * a.len, t1 = min(t0 + a.len, a.T_);
+    auto both = [&](const T *p, int64_t stride) {
+        p += t * stride + th.d;
+        return pack2f(to_f32(p[0]), th.valid > 1 ? to_f32(p[1]) : 0.f);
+    };
+    th.setup(a, group, in_group0);
+    Span s = locate(a.cu, a.N, a.T_, t);
+#pragma unroll 1
+    while (true) {
+        const bool from_carry = s.start < t0;
+        th.load(a, from_carry ? a.carry : a.init, from_carry ? w - 1 : s.n);
+#pragma unroll 1
+        for (const int te = min(s.end, t1); t < te; ++t) {
+            alignas(16) float b[NS], c[NS];
+#pragma unroll 1  // (in local memory: the registers are the states')
+            for (int k = 0; k < NS; ++k) {
+                b[k] = k < a.S ? to_f32(a.B[t * a.bs + group * a.S + k]) : 0.f;
+                c[k] = k < a.S ? to_f32(a.C[t * a.cs + group * a.S + k]) : 0.f;
+            }
+            const uint64_t x = both(a.x, a.xs);
+            const uint64_t sums =
+                th.template token<true, true>(a.softplus, x, both(a.dt, a.dts), b, c, a.S);
+            const uint64_t v = a.skip ? ffma2(th.skip, x, sums) : sums;
+            const float2 f = unpack2f(a.z ? fmul2(v, silu2(both(a.z, a.zs))) : v);
+            T *out = a.out + t * a.os + th.d;
+            out[0] = from_f32<T>(f.x);
+            if (th.valid > 1) out[1] = from_f32<T>(f.y);
+        }
+        if (s.end <= t1) th.finish(a, s.n, from_carry, w);
+        if (t >= t1) break;
+        s = next_span(a.cu, a.N, a.T_, s);
+    }
+}
+
+// GUARD: there are padding states, or there is no skip, whose zeros times an
+// infinity are NaN: tokens with any are taken again without them.
+template <typename T, int NS, bool OUT, bool SHIFT, bool GUARD>
+__global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(const __grid_constant__ ScanArgs<T> a) {
     constexpr int CH = kChannels<NS>, kTile = kTileOf<T, CH>, kTiles = kTilesOf<T, CH>;
     extern __shared__ __align__(16) char smem[];
     const int group = blockIdx.x / a.tiles;
@@ -464,6 +535,14 @@ __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(co
     if (OUT) ptx::griddep_wait();  // the carries: all above is input to the whole call
     if (from_carry) th.load(a, OUT ? a.carry : nullptr, w - 1);
     else th.load(a, a.init, s.n);
+    // Before a sequence's state is left: whether its tokens here have to be taken
+    // again, at the end.  From there on the thread writes nothing.
+    int again = -1;
+    auto leave = [&] {
+        if (!GUARD || !th.spoiled(a.S)) return;
+        again = max(t0, s.start);
+        th.valid = 0;
+    };
     Span next = OUT && s.end < t1 ? next_span(a.cu, a.N, a.T_, s) : s;
 
     for (int tile = 0, tt = t0; tt < t1; ++tile, tt += kTile) {
@@ -487,11 +566,8 @@ __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(co
                 scan_run<T, NS, OUT, SHIFT, kUnroll>(a, th, tl, buf, tt, t, shifts, steps);
             for (; t < e; ++t) scan_run<T, NS, OUT, SHIFT, 1>(a, th, tl, buf, tt, t, shifts, steps);
             if (OUT && t == s.end) {
-                // A final state written over the initial one must wait for
-                // the windows that read it: it takes the place of the state
-                // that entered this window, copied by a last launch.
-                if (a.fin && from_carry && a.defer) th.store(a, a.carry, w - 1);
-                else if (a.fin) th.store(a, a.fin, s.n);
+                leave();
+                th.finish(a, s.n, from_carry, w);
                 if (t < t1) {
                     s = next;
                     th.load(a, a.init, s.n);
@@ -501,6 +577,8 @@ __global__ void __launch_bounds__(kMaxThreads, kResident<NS>) gdn_scan_kernel(co
             }
         }
     }
+    if (OUT && s.end > t1) leave();
+    if (GUARD && again >= 0) scan_again<T, NS>(a, w, again, group, in_group0);
     if (!OUT) {
         ptx::griddep_launch_dependents();
         th.store(a, a.carry, w);
@@ -763,7 +841,7 @@ gdn_scan_step_kernel(const ScanStepArgs<T> a) {
                     own[k] = h;
                 }
             }
-            y = fmaf(skip, now.x, y);
+            if (a.skip) y = fmaf(skip, now.x, y);
             if (a.z) y *= silu(now.z);
             a.out[at.n * a.os + at.d0 + t] = from_f32<T>(y);
         }
@@ -860,7 +938,7 @@ template <typename T> ScanArgs<T> scan_args(const gdn_ssm_problem &p, const Scan
     return a;
 }
 
-template <typename T, int NS, bool SHIFT>
+template <typename T, int NS, bool SHIFT, bool GUARD>
 gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cudaStream_t stream) {
     const unsigned blocks = (unsigned)(a.G * pl.tiles);
     const int64_t ds = (int64_t)a.D * a.S;
@@ -869,8 +947,8 @@ gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cuda
     static std::atomic<bool> done[kMaxDevices];
     if (!raise_shared_memory(
             done,
-            {reinterpret_cast<const void *>(gdn_scan_kernel<T, NS, false, SHIFT>),
-             reinterpret_cast<const void *>(gdn_scan_kernel<T, NS, true, SHIFT>)},
+            {reinterpret_cast<const void *>(gdn_scan_kernel<T, NS, false, SHIFT, false>),
+             reinterpret_cast<const void *>(gdn_scan_kernel<T, NS, true, SHIFT, GUARD>)},
             {ScanTiles<T, NS, false, SHIFT>::bytes(kMaxThreads),
              ScanTiles<T, NS, true, SHIFT>::bytes(kMaxThreads)}))
         return GDN_ERR_CUDA;
@@ -884,7 +962,7 @@ gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cuda
     cfg.attrs = &attr;
     cfg.numAttrs = pl.W > 1 ? 1 : 0;
     if (pl.W > 1) {
-        gdn_scan_kernel<T, NS, false, SHIFT>
+        gdn_scan_kernel<T, NS, false, SHIFT, false>
             <<<dim3(blocks, pl.W - 1), pl.threads, in_bytes, stream>>>(a);
         if (launch_status() != GDN_OK) return GDN_ERR_CUDA;
         // Eight windows are loaded at once: more than a few rounds of them
@@ -906,7 +984,7 @@ gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cuda
         cfg.gridDim = dim3(blocks, rows);
         cfg.blockDim = dim3(pl.threads);
         cfg.dynamicSmemBytes = out_bytes;
-        if (cudaLaunchKernelEx(&cfg, gdn_scan_kernel<T, NS, true, SHIFT>, a) != cudaSuccess)
+        if (cudaLaunchKernelEx(&cfg, gdn_scan_kernel<T, NS, true, SHIFT, GUARD>, a) != cudaSuccess)
             return GDN_ERR_CUDA;
     }
     if (a.defer && pl.W > 1)
@@ -919,8 +997,11 @@ gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool empties, cuda
 template <typename T, int NS>
 gdn_status run_scan(const ScanPlan &pl, const ScanArgs<T> &a, bool shifted, bool empties,
                     cudaStream_t stream) {
-    return shifted ? run_scan<T, NS, true>(pl, a, empties, stream)
-                   : run_scan<T, NS, false>(pl, a, empties, stream);
+    if (a.S < NS || !a.skip)
+        return shifted ? run_scan<T, NS, true, true>(pl, a, empties, stream)
+                       : run_scan<T, NS, false, true>(pl, a, empties, stream);
+    return shifted ? run_scan<T, NS, true, false>(pl, a, empties, stream)
+                   : run_scan<T, NS, false, false>(pl, a, empties, stream);
 }
 
 template <typename T>

@@ -135,7 +135,8 @@ GDN_API size_t gdn_selective_scan_workspace_size(const gdn_ssm_problem *problem)
  *   initial_state  fp32 [N, D, S] or NULL (zeros)
  *   final_state    fp32 [N, D, S] or NULL (not written); may equal
  *                  initial_state (in-place resume)
- * out must not alias an input.
+ * out must not alias an input.  Infinities and NaN among the inputs give what
+ * the formula gives in fp32, in their own sequence only.
  *
  * The packed tokens are cut into windows of equal length (at least 8 tokens),
  * as many as make one wave of blocks.  With more than one, three launches
