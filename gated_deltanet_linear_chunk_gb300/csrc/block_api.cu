@@ -25,9 +25,11 @@ bool any_null(std::initializer_list<const void *> ptrs) {
     return false;
 }
 
-// Token counts and channels that the kernels' 32-bit indices hold.
+// Sequence and token counts and channels that the kernels' 32-bit indices hold
+// (the search of a token's sequence adds two of them).
 bool sizes_ok(int32_t seqs, int64_t tokens, int32_t channels) {
-    return seqs >= 0 && tokens >= 0 && channels >= 1 && tokens <= (int64_t)INT32_MAX / 2 &&
+    constexpr int64_t most = INT32_MAX / 2;
+    return seqs >= 0 && seqs <= most && tokens >= 0 && tokens <= most && channels >= 1 &&
            channels <= 1 << 20;
 }
 

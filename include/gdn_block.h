@@ -46,8 +46,8 @@ typedef enum {
 
 /*
  * Short causal depthwise convolution.
- *   num_seqs      N >= 0;  total_tokens T (step: must equal N)
- *   channels      C >= 1;  width K, 2 to 8
+ *   num_seqs      N;  total_tokens T (step: must equal N), each 0 to 2^30 - 1
+ *   channels      C, 1 to 2^20;  width K, 2 to 8
  *   activation    GDN_ACT_NONE or GDN_ACT_SILU
  *   x_stride, out_stride   elements between rows, >= C
  */
@@ -90,8 +90,8 @@ GDN_API gdn_status gdn_short_conv_step(const gdn_conv_problem *problem, const vo
 
 /*
  * Selective state space scan.
- *   num_seqs      N >= 0;  total_tokens T (step: must equal N)
- *   channels      D >= 1;  state_dim S, 1 to 64
+ *   num_seqs      N;  total_tokens T (step: must equal N), each 0 to 2^30 - 1
+ *   channels      D, 1 to 2^20;  state_dim S, 1 to 64
  *   num_groups    G >= 1, dividing D: channels d D/G .. share B and C
  *   dt_softplus   nonzero: the step is softplus(dt + dt_bias)
  *   strides       elements between rows: x, dt, z, out >= D, B, C >= G S
