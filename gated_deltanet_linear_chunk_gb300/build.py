@@ -36,8 +36,11 @@ def library_path(debug: bool = False) -> str:
 
 
 def binding_path() -> str:
-    """The extension module that marshals the block operators' tensors."""
-    return os.path.join(BUILD, f"gdn_block_binding_{platform.machine()}.so")
+    """The extension module that marshals the block operators' tensors, for this
+    Python and PyTorch: it uses their C++ interfaces, which others do not share."""
+    import torch
+    return os.path.join(BUILD, f"gdn_block_binding_{platform.machine()}_"
+                               f"{sysconfig.get_config_var('SOABI')}_torch-{torch.__version__}.so")
 
 
 def _binding_command(out: str):
