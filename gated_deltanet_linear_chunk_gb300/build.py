@@ -58,8 +58,11 @@ def _binding_command(out: str):
             "-lc10", "-lc10_cuda"]
 
 
-def _build_binding() -> None:
+def _build_binding(force: bool) -> None:
     out = binding_path()
+    if not (force or _stale(out)):
+        return
+    os.makedirs(BUILD, exist_ok=True)
     tmp = out + ".tmp"
     r = subprocess.run(_binding_command(tmp), capture_output=True, text=True)
     if r.returncode != 0:
@@ -94,13 +97,22 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug=None
     """Compile every CUDA source and link the library: debug=None builds the
     release and the GDN_DEBUG variants and the binding (their sources compiled
     in one parallel pool), False the release variant and the binding, True the
-    GDN_DEBUG one.  Returns the path of the
+    GDN_DEBUG one.  The libraries need nvcc alone: they are linked also where
+    the binding cannot be compiled (g++, Python's and PyTorch's headers), which
+    is raised after.  Returns the path of the
     release library (or of the one variant asked for)."""
     variants = [False, True] if debug is None else [bool(debug)]
     todo = [v for v in variants if force or _stale(library_path(v))]
-    binding = debug is not True and (force or _stale(binding_path()))
-    if binding and not todo:
-        _build_binding()
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_build_binding, force) if debug is not True else None
+        _build_libraries(todo, verbose, extra_flags)
+    if binding:
+        binding.result()
+    return library_path(False if debug is None else bool(debug))
+
+
+def _build_libraries(todo, verbose: bool, extra_flags) -> None:
+    """Compiles and links the variants of the library in `todo`."""
     if todo:
         nvcc = _nvcc()
         srcs = _sources()
@@ -123,11 +135,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug=None
         for dbg in todo:
             os.makedirs(obj_dir(dbg), exist_ok=True)
         jobs = [(dbg, src) for dbg in todo for src in srcs]
-        with cf.ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
-            module = ex.submit(_build_binding) if binding else None
+        with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             objs = list(ex.map(compile_one, jobs))
-            if module:
-                module.result()
         for dbg in todo:
             out = library_path(dbg)
             mine = [o for (d, _), o in zip(jobs, objs) if d == dbg]
@@ -138,7 +147,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug=None
             if r.returncode != 0:
                 raise RuntimeError(f"link failed:\n{r.stderr}")
             os.replace(tmp, out)
-    return library_path(False if debug is None else bool(debug))
 
 
 if __name__ == "__main__":
