@@ -19,6 +19,13 @@ bool misaligned(size_t size, std::initializer_list<const void *> ptrs) {
     return false;
 }
 
+// Whether the (non-null) result lies over one of the others.
+bool over(const void *result, std::initializer_list<const void *> others) {
+    for (const void *p : others)
+        if (result && result == p) return true;
+    return false;
+}
+
 bool any_null(std::initializer_list<const void *> ptrs) {
     for (const void *p : ptrs)
         if (!p) return true;
@@ -82,7 +89,8 @@ GDN_API gdn_status gdn_short_conv(const gdn_conv_problem *problem, const void *x
     if (misaligned(size_of(p.dtype), {x, initial_state, out, final_state}) ||
         misaligned(4, {weight, bias, cu_seqlens}))
         return GDN_ERR_MISALIGNED;
-    if (out && out == x) return GDN_ERR_INVALID_ARG;
+    if (over(out, {x, initial_state, final_state}) || over(final_state, {x}))
+        return GDN_ERR_INVALID_ARG;
     return launch_short_conv(p, x, weight, bias, cu_seqlens, initial_state, out, final_state,
                              reinterpret_cast<cudaStream_t>(stream));
 }
@@ -125,7 +133,8 @@ GDN_API gdn_status gdn_selective_scan(const gdn_ssm_problem *problem, const void
     if (misaligned(size_of(p.dtype), {x, dt, B, C, z, out}) ||
         misaligned(4, {A, skip, dt_bias, cu_seqlens, initial_state, final_state}))
         return GDN_ERR_MISALIGNED;
-    if (out && (out == x || out == dt || out == z || out == B || out == C))
+    if (over(out, {x, dt, z, B, C, initial_state, final_state}) ||
+        over(final_state, {x, dt, z, A, B, C}))
         return GDN_ERR_INVALID_ARG;
     const size_t need = scan_workspace_size(p);
     if (need > 0 && (!p.workspace || p.workspace_bytes < need || !aligned16(p.workspace)))

@@ -72,7 +72,7 @@ typedef struct {
  *   final_state    [N, K - 1, C] or NULL (not written): the last K - 1 inputs
  *                  of each sequence, the initial state's among them where it
  *                  is shorter.  May equal initial_state (in-place resume).
- * out must not alias x.
+ * Nothing else may overlap.
  */
 GDN_API gdn_status gdn_short_conv(const gdn_conv_problem *problem, const void *x,
                                   const float *weight, const float *bias,
@@ -135,8 +135,9 @@ GDN_API size_t gdn_selective_scan_workspace_size(const gdn_ssm_problem *problem)
  *   initial_state  fp32 [N, D, S] or NULL (zeros)
  *   final_state    fp32 [N, D, S] or NULL (not written); may equal
  *                  initial_state (in-place resume)
- * out must not alias an input.  Infinities and NaN among the inputs give what
- * the formula gives in fp32, in their own sequence only.
+ * Neither out nor final_state may overlap anything else.  Infinities and NaN
+ * among the inputs give what the formula gives in fp32, in their own sequence
+ * only.
  *
  * The packed tokens are cut into windows of equal length (at least 8 tokens),
  * as many as make one wave of blocks.  With more than one, three launches
