@@ -191,13 +191,16 @@ GDN_API gdn_status gdn_norm_gate_residual(const gdn_norm_problem *problem, const
         misaligned(size_of(p.residual_dtype), {residual, out}) ||
         misaligned(4, {weight, next_weight}))
         return GDN_ERR_MISALIGNED;
-    // In place only element by element: the same stride and element size.
+    // In place only element by element: the same element size and, of several
+    // rows, the same stride.
     const bool same_type = p.dtype == p.residual_dtype;
+    auto same_rows = [&](int64_t stride, int64_t other) { return p.rows == 1 || stride == other; };
     if (out == gate || out == next || (next && next == residual)) return GDN_ERR_INVALID_ARG;
-    if (out == y && !(same_type && p.out_stride == p.y_stride)) return GDN_ERR_INVALID_ARG;
-    if (out == residual && p.out_stride != p.residual_stride) return GDN_ERR_INVALID_ARG;
-    if (next && next == y && p.next_stride != p.y_stride) return GDN_ERR_INVALID_ARG;
-    if (next && next == gate && p.next_stride != p.gate_stride) return GDN_ERR_INVALID_ARG;
+    if (out == y && !(same_type && same_rows(p.out_stride, p.y_stride))) return GDN_ERR_INVALID_ARG;
+    if (out == residual && !same_rows(p.out_stride, p.residual_stride)) return GDN_ERR_INVALID_ARG;
+    if (next && next == y && !same_rows(p.next_stride, p.y_stride)) return GDN_ERR_INVALID_ARG;
+    if (next && next == gate && !same_rows(p.next_stride, p.gate_stride))
+        return GDN_ERR_INVALID_ARG;
     return launch_norm_gate_residual(p, y, weight, gate, residual, next_weight, out, next,
                                      reinterpret_cast<cudaStream_t>(stream));
 }

@@ -206,7 +206,8 @@ typedef struct {
  *   next_weight     fp32 [D], or NULL: next is not computed
  *   out, next       [R, D]; next is NULL exactly when next_weight is
  * out may equal y or residual, and next may equal y or gate, where pointer,
- * stride and element type are the same; nothing else may overlap.
+ * element type and, of several rows, stride are the same; nothing else may
+ * overlap.
  */
 GDN_API gdn_status gdn_norm_gate_residual(const gdn_norm_problem *problem, const void *y,
                                           const float *weight, const void *gate,
