@@ -32,8 +32,8 @@ __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 
 // log(1 + e^v) = max(v, 0) + log1p(e) with e = e^-|v| in (0, 1].  log1p(e) / e
 // is a polynomial of degree 8, fitted to the least largest relative error on
-// [0, 1] (3e-8; 1.4e-7 in fp32 arithmetic, 5e-8 on average): relative accuracy
-// is kept for the small steps of very negative v, where log1p(e) is e.  (NaN:
+// [0, 1] (6.4e-8 with the coefficients rounded to fp32; 1.8e-7 in fp32 arithmetic,
+// 4e-8 on average): relative accuracy is kept for the small steps of very negative v, where log1p(e) is e.  (NaN:
 // e is NaN, and so is the result.)
 __device__ __forceinline__ constexpr float softplus_coefficient(int power) {
     constexpr float c[9] = {0.9999999403953552f,  -0.4999949336051941f,  0.3331909775733948f,

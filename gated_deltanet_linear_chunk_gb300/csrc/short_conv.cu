@@ -38,7 +38,9 @@ constexpr int kStep = 4;   // tokens per group of copies
 // 8-byte ones, so that six blocks' rings stay on an SM.
 template <int Bytes> constexpr int kAhead = Bytes == 16 ? 2 : 4;
 template <int Bytes> constexpr int kRing = (kAhead<Bytes> + 1) * kStep;
-// Blocks per SM that the registers of a width's weights and inputs allow.
+// Blocks per SM that the registers are kept low for.  Above width 4 weights and
+// inputs of all taps take too many for six: two, three and four took the same
+// time at width 8 (4000 x 10240 bf16, 38 us now), short calls the least with two.
 template <int K> constexpr int kBlocks = K <= 4 ? 6 : 2;
 
 template <typename T> struct ConvArgs {
@@ -334,8 +336,7 @@ gdn_status run_conv(const gdn_conv_problem &p, const void *x, const float *weigh
     auto blocks = [&](int run) {
         return (int64_t)a.n_chan * ((p.total_tokens + (int64_t)run * ty - 1) / ((int64_t)run * ty));
     };
-    // One wave of blocks with runs of up to 64 tokens, or so many full waves;
-    // at least 8 tokens while four blocks per SM are left.
+    // One wave of blocks with runs of up to 64 tokens, or so many full waves.
     const int64_t slots = kBlocks<K> * kGridSms;
     const int64_t each = (p.total_tokens * a.n_chan + slots * ty - 1) / (slots * ty);
     const int64_t waves = (each + 63) / 64;
@@ -346,7 +347,7 @@ gdn_status run_conv(const gdn_conv_problem &p, const void *x, const float *weigh
         fin ? ((int64_t)p.num_seqs * words + kThreads - 1) / kThreads : 0;
     if (n_main + n_state > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     a.n_main = (int)n_main;
-    // (36 KB at most, at width 8.)
+    // (40 KB at most, in fp32 at width 8: 16 of weights and 24 of ring.)
     constexpr int kSlot = sizeof(T) * V < 4 ? 4 : sizeof(T) * V;
     static_assert((kThreads * V * K * 4 + kRing<kSlot> * kThreads * kSlot) <= 48 * 1024);
     const size_t smem = (size_t)a.tx * V * K * sizeof(float) + kRing<kSlot> * kThreads * kSlot;

@@ -129,9 +129,10 @@ GDN_API size_t gdn_selective_scan_workspace_size(const gdn_ssm_problem *problem)
  *   h_t = exp(s_t A[d, :]) h_{t-1} + s_t x[t, d] B[t, g, :]
  *   out[t, d] = (sum C[t, g, :] h_t + skip[d] x[t, d]) z[t, d] sigmoid(z[t, d])
  *   x, dt, z, out  [T, D]; z may be NULL (no gate)
- *   A              fp32 [D, S], finite (negative for a decaying state)
+ *   A              fp32 [D, S], finite, of any sign (negative for a decaying
+ *                  state)
  *   B, C           [T, G, S]
- *   skip, dt_bias  fp32 [D] or NULL (zeros)
+ *   skip, dt_bias  fp32 [D] or NULL (no such term)
  *   initial_state  fp32 [N, D, S] or NULL (zeros)
  *   final_state    fp32 [N, D, S] or NULL (not written); may equal
  *                  initial_state (in-place resume)
@@ -144,8 +145,10 @@ GDN_API size_t gdn_selective_scan_workspace_size(const gdn_ssm_problem *problem)
  * run: the state that each window adds on its own (from a zero state, or from
  * the sequence's start inside it), the states entering the windows, and the
  * outputs of all windows; the later ones may start while the one before ends
- * (programmatic launches on `stream`).  Few tokens run as one window, with
- * the last launch alone and no workspace.  The order of the fp32 sums depends
+ * (programmatic launches on `stream`).  Where final_state equals
+ * initial_state, a fourth launch writes the final states that other windows
+ * had to read as initial ones until then.  Few tokens run as one window, with
+ * the launch of the outputs alone and no workspace.  The order of the fp32 sums depends
  * on the sizes alone, so a call gives the same bits every time.
  */
 GDN_API gdn_status gdn_selective_scan(const gdn_ssm_problem *problem, const void *x,
