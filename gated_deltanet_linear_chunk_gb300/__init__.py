@@ -36,11 +36,14 @@ __all__ = [
     "gdn_short_conv", "gdn_short_conv_step",
     "gdn_selective_scan", "gdn_selective_scan_step", "gdn_selective_scan_workspace_size",
     "gdn_norm_gate_residual",
+    "gdn_qk_norm_rope", "gdn_paged_append", "gdn_paged_attention",
+    "gdn_paged_attention_workspace_size",
 ]
 
 GDN_BF16 = 0
 GDN_F32 = 1
 GDN_F16 = 2  # state storage of gdn_decode_step_half_state only
+GDN_E4M3 = 3  # storage of a paged cache only
 
 # gdn_status codes (include/gdn.h).
 GDN_OK = 0
@@ -150,6 +153,7 @@ def _load(path: str) -> ctypes.CDLL:
     lib.gdn_prefill_path.restype = ctypes.c_int32
     lib.gdn_prefill_path.argtypes = [PP, ctypes.c_int32, ctypes.c_int32]
     block.declare(lib)
+    attention.declare(lib)
     return lib
 
 
@@ -699,3 +703,6 @@ from . import block  # noqa: E402  (uses the helpers above)
 from .block import (  # noqa: E402
     gdn_norm_gate_residual, gdn_selective_scan, gdn_selective_scan_step,
     gdn_selective_scan_workspace_size, gdn_short_conv, gdn_short_conv_step)
+from . import attention  # noqa: E402
+from .attention import (  # noqa: E402
+    gdn_paged_append, gdn_paged_attention, gdn_paged_attention_workspace_size, gdn_qk_norm_rope)

@@ -44,8 +44,8 @@ def binding_path() -> str:
 
 
 def _binding_command(out: str):
-    """Compiles csrc/block_binding.cpp against this Python and PyTorch; their
-    libraries are those that `import torch` has already loaded."""
+    """Compiles csrc/block_binding.cpp and attention_binding.cpp against this
+    Python and PyTorch; their libraries are those that `import torch` has already loaded."""
     import torch
     home = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
@@ -53,7 +53,8 @@ def _binding_command(out: str):
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             "-I", os.path.join(home, "include"), "-I", sysconfig.get_paths()["include"],
             "-I", os.path.join(cuda, "include"), "-I", INCLUDE,
-            os.path.join(CSRC, "block_binding.cpp"), "-o", out,
+            os.path.join(CSRC, "block_binding.cpp"), os.path.join(CSRC, "attention_binding.cpp"),
+            "-o", out,
             "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda",
             "-lc10", "-lc10_cuda"]
 
@@ -83,7 +84,7 @@ def _sources():
 
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
+            + glob.glob(os.path.join(CSRC, "*.hpp")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
 def _stale(out: str) -> bool:

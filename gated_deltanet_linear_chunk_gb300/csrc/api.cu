@@ -299,6 +299,6 @@ GDN_API const char *gdn_status_string(gdn_status status) {
     return "GDN_ERR_UNKNOWN";
 }
 
-GDN_API int gdn_version(void) { return 200; }
+GDN_API int gdn_version(void) { return 300; }
 
 }  // extern "C"

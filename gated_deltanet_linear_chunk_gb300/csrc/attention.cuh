@@ -1,0 +1,27 @@
+// attention.cuh -- shared pieces of the operators of include/gdn_attention.h
+// (not part of the ABI).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "block.cuh"
+#include "gdn_attention.h"
+
+namespace gdn {
+
+constexpr int kMaxRotary = 512;     // elements of a head that are rotated, at most
+constexpr int kMaxNewTokens = 8;    // of a sequence, in one attention call
+constexpr int kMaxCached = (1 << 30) - 1;  // tokens of a sequence
+
+// ------------------------------------------------------------------ launchers
+// v, cache and cu belong to the append (cache null: gdn_qk_norm_rope).
+gdn_status launch_qk_rope(const gdn_rope_problem &p, const gdn_paged_cache *cache, const void *q,
+                          const void *k, const void *v, const float *q_weight,
+                          const float *k_weight, const int32_t *positions, const float *inv_freq,
+                          const int32_t *cu, void *q_out, void *k_out, cudaStream_t stream);
+size_t paged_attention_workspace(const gdn_attention_problem &p, const gdn_paged_cache &c);
+gdn_status launch_paged_attention(const gdn_attention_problem &p, const gdn_paged_cache &c,
+                                  const void *q, const void *gate, void *out, float *lse,
+                                  cudaStream_t stream);
+
+}  // namespace gdn

@@ -77,8 +77,10 @@ typedef enum {
 typedef enum {
     GDN_BF16 = 0,  /* q, k, v and out are bf16 (tensor-core path)   */
     GDN_F32 = 1,   /* q, k, v and out are fp32 (FFMA check path)    */
-    GDN_F16 = 2    /* only as the state storage of
+    GDN_F16 = 2,   /* only as the state storage of
                       gdn_decode_step_half_state                    */
+    GDN_E4M3 = 3   /* only as the storage of a paged cache
+                      (gdn_attention.h)                             */
 } gdn_dtype;
 
 /*
