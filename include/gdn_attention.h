@@ -90,7 +90,7 @@ GDN_API gdn_status gdn_qk_norm_rope(const gdn_rope_problem *problem, const void 
  *   dtype        GDN_BF16, GDN_F32, or GDN_E4M3: 8-bit floating point (4 bits of
  *                exponent, 3 of mantissa, no infinities) times a scale
  *   num_pages    P, 0 to 2^31 - 1;  page_size 1 to 2^20
- *   k_scale, v_scale   fp32 [kv heads] of GDN_E4M3; NULL otherwise
+ *   k_scale, v_scale   fp32 [kv heads] of GDN_E4M3, positive; NULL otherwise
  *   num_seqs     N;  max_pages: columns of page_table; max_pages page_size at
  *                most 2^30 - 1
  *   page_table   int32 [N, max_pages], rows table_stride elements apart
