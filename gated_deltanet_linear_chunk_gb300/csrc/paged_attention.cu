@@ -5,11 +5,11 @@
 namespace gdn {
 namespace {
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256, kJoinBlocks = 16 * kGridSms;
 
-// The pieces of one unit, for one row: block x is the block that left the
-// first, y the row.  Threads are four elements of a row each, several pieces at
-// a time.
+// The pieces of one unit: block x is the block that left the first, y its rows,
+// every gridDim.y-th.  Threads are four elements of a row each, several pieces
+// at a time.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
 gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows) {
@@ -19,7 +19,7 @@ gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows) {
     __shared__ float tops[kJoinThreads / 32], totals[kJoinThreads / 32];
     __shared__ float4 parts[kJoinThreads];
     ptx::griddep_wait();
-    const int block = blockIdx.x, r = blockIdx.y;
+    const int block = blockIdx.x;
     const int4 join = a.joins[block];
     Unit u;
     u.n = join.x;
@@ -27,59 +27,60 @@ gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows) {
     u.head = join.y / a.row_blocks;
     u.first_row = join.y % a.row_blocks * rows;
     u.rows = min(rows, a.R - u.first_row);
-    if (r >= u.rows) return;
     const int pieces = join.z + 1;
     // The first piece ends its block's range, the others begin theirs.
     auto slot = [&](int i) { return i == 0 ? 2 * block + 1 : 2 * (block + i); };
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    float top = kNone;
-    for (int i = threadIdx.x; i < pieces; i += kJoinThreads)
-        top = fmaxf(top, a.stats[slot(i) * rows + r].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, tops[w]);
-    float total = 0.f;
-    for (int i = threadIdx.x; i < pieces; i += kJoinThreads) {
-        const float2 s = a.stats[slot(i) * rows + r];
-        const float f = ex2(s.x - against(top));
-        weight[i] = f;
-        total += s.y * f;
-    }
-    total = warp_sum(total);
-    if (lane == 0) totals[warp] = total;
-    __syncthreads();
-    total = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) total += totals[w];
-
     const int team = threadIdx.x / WORDS, word = threadIdx.x % WORDS;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = team; i < pieces; i += TEAMS) {
-        const float4 x =
-            reinterpret_cast<const float4 *>(a.sums)[((int64_t)slot(i) * rows + r) * WORDS + word];
-        const float f = weight[i];
-        y.x = fmaf(f, x.x, y.x);
-        y.y = fmaf(f, x.y, y.y);
-        y.z = fmaf(f, x.z, y.z);
-        y.w = fmaf(f, x.w, y.w);
-    }
-    parts[threadIdx.x] = y;
-    __syncthreads();
-    const RowPlace p = row_place(a, u, r);
-    const float inv = inverse(total);
-    for (int e = threadIdx.x; e < D; e += kJoinThreads) {
-        float sum = 0.f;
+    for (int r = blockIdx.y; r < u.rows; r += gridDim.y) {
+        float top = kNone;
+        for (int i = threadIdx.x; i < pieces; i += kJoinThreads)
+            top = fmaxf(top, a.stats[slot(i) * rows + r].x);
 #pragma unroll
-        for (int t = 0; t < TEAMS; ++t)
-            sum += reinterpret_cast<const float *>(&parts[t * WORDS])[e];
-        const T *gate = a.gate ? (const T *)a.gate + p.token * a.gs + p.head * a.gh + e : nullptr;
-        ((T *)a.out)[p.token * a.os + p.head * a.oh + e] = from_f32<T>(finish(sum, inv, gate));
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        if (lane == 0) tops[warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, tops[w]);
+        float total = 0.f;
+        for (int i = threadIdx.x; i < pieces; i += kJoinThreads) {
+            const float2 s = a.stats[slot(i) * rows + r];
+            const float f = ex2(s.x - against(top));
+            weight[i] = f;
+            total += s.y * f;
+        }
+        total = warp_sum(total);
+        if (lane == 0) totals[warp] = total;
+        __syncthreads();
+        total = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinThreads / 32; ++w) total += totals[w];
+
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int i = team; i < pieces; i += TEAMS) {
+            const float4 x = reinterpret_cast<const float4 *>(
+                a.sums)[((int64_t)slot(i) * rows + r) * WORDS + word];
+            const float f = weight[i];
+            y.x = fmaf(f, x.x, y.x);
+            y.y = fmaf(f, x.y, y.y);
+            y.z = fmaf(f, x.z, y.z);
+            y.w = fmaf(f, x.w, y.w);
+        }
+        parts[threadIdx.x] = y;
+        __syncthreads();
+        const RowPlace p = row_place(a, u, r);
+        const float inv = inverse(total);
+        for (int e = threadIdx.x; e < D; e += kJoinThreads) {
+            float sum = 0.f;
+#pragma unroll
+            for (int t = 0; t < TEAMS; ++t)
+                sum += reinterpret_cast<const float *>(&parts[t * WORDS])[e];
+            const T *gate = a.gate ? (const T *)a.gate + p.token * a.gs + p.head * a.gh + e : nullptr;
+            ((T *)a.out)[p.token * a.os + p.head * a.oh + e] = from_f32<T>(finish(sum, inv, gate));
+        }
+        if (threadIdx.x == 0) store_lse(a, p, top, total);
     }
-    if (threadIdx.x == 0) store_lse(a, p, top, total);
 }
 
 struct Plan {
@@ -117,7 +118,8 @@ gdn_status join(const AttentionArgs &a, const Plan &pl, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3(pl.blocks, pl.rows < a.R ? pl.rows : a.R);
+    const int rows = pl.rows < a.R ? pl.rows : a.R, fit = kJoinBlocks / pl.blocks;
+    cfg.gridDim = dim3(pl.blocks, rows < fit ? rows : fit);
     cfg.blockDim = dim3(kJoinThreads);
     return cudaLaunchKernelEx(&cfg, gdn_attention_join_kernel<T, D>, a, pl.rows) == cudaSuccess
                ? GDN_OK
@@ -153,6 +155,13 @@ gdn_status launch_paged_attention(const gdn_attention_problem &p, const gdn_page
     a.page_size = c.page_size;
     a.capacity = c.max_pages * c.page_size;
     a.scale_log2 = p.scale * kLog2e;
+    auto words = [&](const void *x, int64_t stride, int64_t head_stride) {
+        const uint64_t size = p.dtype == GDN_F32 ? 4 : 2;
+        return aligned16(x) && (((a.N * a.L > 1 ? stride : 0) | (p.q_heads > 1 ? head_stride : 0)) * size) % 16 == 0;
+    };
+    a.q_words = words(q, p.q_stride, p.q_head_stride);
+    a.gate_words = words(gate, p.gate_stride, p.gate_head_stride);
+    a.out_words = words(out, p.out_stride, p.out_head_stride);
     if (pl.split) {
         // The sums first: they are read in 16-byte words.
         char *w = static_cast<char *>(p.workspace);

@@ -31,6 +31,7 @@ struct AttentionArgs {
     int64_t kps, kts, khs, vps, vts, vhs, table_stride;
     int64_t num_pages;
     int N, L, Hkv, G, R, row_blocks, page_size, capacity;
+    bool q_words, gate_words, out_words;  // rows of q, gate and out in whole 16-byte words
     float scale_log2;  // scale log2 e: scores in powers of two
     // workspace
     int4 *joins;     // [blocks] the unit whose first piece the block left: n, unit, blocks after it

@@ -67,6 +67,23 @@ __device__ __forceinline__ uint32_t widen(uint32_t two) {
     return r;
 }
 
+// Eight elements, in one word where the rows allow it.
+__device__ __forceinline__ Vec<__nv_bfloat16, 8> load8(const __nv_bfloat16 *p, bool words) {
+    if (words) return Vec<__nv_bfloat16, 8>::load(p);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_f32(p[i]);
+    return Vec<__nv_bfloat16, 8>::from(x);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, bool words, const float (&x)[8]) {
+    if (words) {
+        Vec<__nv_bfloat16, 8>::from(x).store(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = from_f32<__nv_bfloat16>(x[i]);
+    }
+}
+
 // What a variant keeps in shared memory.  EIGHT: an 8-bit cache; MT tiles of 16
 // rows, each of one warp, share a ring; GR such groups.
 template <bool EIGHT, int D, int MT, int GR> struct Tiles {
@@ -100,7 +117,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     constexpr int HOLD = (TK + 31) / 32;               // rows whose place a lane knows
     extern __shared__ __align__(16) char smem[];
     __shared__ float2 ml[GR][S::kRows];
-    __shared__ float row_scale[S::kRows];
+    __shared__ float row_scale[S::kRows], inverses[S::kRows];
     char *queries = smem, *ring = smem + S::kQueries;
     float *sums = reinterpret_cast<float *>(ring);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -117,6 +134,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
         else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(MT * 32) : "memory");
     };
 
+    ptx::griddep_launch_dependents();
     const Range range = find_range<S::kChunk, S::kThreads>(a, a.Hkv * a.row_blocks);
     for_pieces<S::kChunk, S::kRows>(a, range, [&](const Unit &u, int t0, int t1, int slot) {
         const int tiles = (t1 - t0 + TK - 1) / TK;
@@ -184,39 +202,56 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
 
         // Queries, times the sign of the scale; for fp16 products each row over
         // the power of two of its largest, in the order of an 8-bit key's
-        // elements (see below).
+        // elements (see below).  A thread has eight elements at a time, and all
+        // it takes are loaded together.
         const float sign = a.scale_log2 < 0.f ? -1.f : a.scale_log2 == 0.f ? 0.f : 1.f;
-        for (int r = warp; r < S::kRows; r += S::kThreads / 32) {
-            float x[D / 32];
-            const bool live = r < u.rows;
-            const RowPlace p = row_place(a, u, live ? r : 0);
-            const T *q = static_cast<const T *>(a.q) + p.token * a.qs + p.head * a.qh;
-            float top = 0.f;
+        {
+            constexpr int Q8 = D / 8, EACH = S::kRows * Q8 / S::kThreads, BATCH = EACH < 4 ? EACH : 4;
+#pragma unroll 1
+            for (int i0 = 0; i0 < EACH; i0 += BATCH) {
+                Vec<T, 8> x[BATCH];
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                x[i] = live ? to_f32(q[i * 32 + lane]) * sign : 0.f;
-                top = fmaxf(top, fabsf(x[i]));
-            }
-            char *to = queries + r * S::kQueryPitch;
-            if constexpr (EIGHT) {
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                // 2^e <= top < 2^(e + 1), from the exponent's bits.
-                const int e = top > 0x1p-120f && top < 0x1p120f ? (__float_as_int(top) >> 23) - 127 : 0;
-                const float down = __int_as_float((127 - e) << 23);
-                if (lane == 0) row_scale[r] = __int_as_float((127 + e) << 23);
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    float y = x[i] * down;
-                    if (fabsf(y) < __builtin_huge_valf()) y = fminf(fmaxf(y, -65504.f), 65504.f);
-                    const int d = i * 32 + lane, in = d & 15;  // element 4 c + j of 16
-                    const int at = (d & ~15) + (in >> 2) * 2 + (in & 1) + (in & 2) * 4;
-                    reinterpret_cast<__half *>(to)[at] = __float2half_rn(y);
+                for (int i = 0; i < BATCH; ++i) {
+                    const int at = (i0 + i) * S::kThreads + threadIdx.x, r = at / Q8, e = at % Q8 * 8;
+                    x[i] = Vec<T, 8>::zero();
+                    if (r >= u.rows) continue;
+                    const RowPlace p = row_place(a, u, r);
+                    x[i] = load8(static_cast<const T *>(a.q) + p.token * a.qs + p.head * a.qh + e, a.q_words);
                 }
-            } else {
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i)
-                    reinterpret_cast<T *>(to)[i * 32 + lane] = from_f32<T>(x[i]);
+                for (int i = 0; i < BATCH; ++i) {
+                    const int at = (i0 + i) * S::kThreads + threadIdx.x, r = at / Q8, e = at % Q8 * 8;
+                    char *to = queries + r * S::kQueryPitch;
+                    float y[8];
+                    x[i].to(y);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] *= sign;
+                    if constexpr (EIGHT) {
+                        float top = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(y[k]));
+#pragma unroll
+                        for (int d = Q8 / 2; d > 0; d >>= 1)
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        // 2^n <= top < 2^(n + 1), from the exponent's bits.
+                        const int n = top > 0x1p-120f && top < 0x1p120f ? (__float_as_int(top) >> 23) - 127 : 0;
+                        const float down = __int_as_float((127 - n) << 23);
+                        if (e == 0) row_scale[r] = __int_as_float((127 + n) << 23);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            y[k] *= down;
+                            if (fabsf(y[k]) < __builtin_huge_valf()) y[k] = fminf(fmaxf(y[k], -65504.f), 65504.f);
+                        }
+                        // Elements 4 c + j of 16: pairs of j < 2 first.
+                        uint32_t *half = reinterpret_cast<uint32_t *>(to + (e & ~15) * 2) + (e & 8) / 4;
+                        half[0] = pack_weights<true>(y[0], y[1]);
+                        half[4] = pack_weights<true>(y[2], y[3]);
+                        half[1] = pack_weights<true>(y[4], y[5]);
+                        half[5] = pack_weights<true>(y[6], y[7]);
+                    } else {
+                        Vec<T, 8>::from(y).store(reinterpret_cast<T *>(to) + e);
+                    }
+                }
             }
         }
         __syncthreads();
@@ -485,27 +520,72 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             }
         }
         __syncthreads();
-        const float v_scale = EIGHT ? a.v_scale[u.head] : 1.f;
-        for (int i = threadIdx.x; i < u.rows * D; i += S::kThreads) {
-            const int r = i / D, e = i % D;
-            float top = kMinusInfinity, sum = 0.f, y = 0.f;
+        // Each row's factors for the groups' sums, the values' scale among them.
+        if (threadIdx.x < u.rows) {
+            const int r = threadIdx.x;
+            const float v_scale = EIGHT ? a.v_scale[u.head] : 1.f;
+            float top = kMinusInfinity, sum = 0.f;
 #pragma unroll
             for (int w = 0; w < GR; ++w) top = fmaxf(top, ml[w][r].x);
 #pragma unroll
             for (int w = 0; w < GR; ++w) {
                 const float f = ex2(ml[w][r].x - against(top));
                 sum += ml[w][r].y * f;
-                y += sums[(w * S::kRows + r) * S::kSumPitch + e] * f;
+                ml[w][r].x = f * v_scale;
             }
-            y *= v_scale;
             if (slot < 0) {
-                const RowPlace p = row_place(a, u, r);
-                const T *gate = a.gate ? (const T *)a.gate + p.token * a.gs + p.head * a.gh + e : nullptr;
-                ((T *)a.out)[p.token * a.os + p.head * a.oh + e] = from_f32<T>(finish(y, inverse(sum), gate));
-                if (e == 0) store_lse(a, p, top, sum);
+                store_lse(a, row_place(a, u, r), top, sum);
+                inverses[r] = inverse(sum);
             } else {
-                a.sums[((int64_t)slot * S::kRows + r) * D + e] = y;
-                if (e == 0) a.stats[slot * S::kRows + r] = make_float2(top, sum);
+                a.stats[slot * S::kRows + r] = make_float2(top, sum);
+            }
+        }
+        __syncthreads();
+        const int words = u.rows * (D / 8);
+        constexpr int BATCH = 4;
+#pragma unroll 1
+        for (int i0 = threadIdx.x; i0 < words; i0 += BATCH * S::kThreads) {
+            Vec<T, 8> gate[BATCH];
+            if (slot < 0 && a.gate) {
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int i = i0 + k * S::kThreads;
+                    if (i >= words) continue;
+                    const RowPlace p = row_place(a, u, i / (D / 8));
+                    gate[k] = load8((const T *)a.gate + p.token * a.gs + p.head * a.gh + i % (D / 8) * 8,
+                                    a.gate_words);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int i = i0 + k * S::kThreads, r = i / (D / 8), e = i % (D / 8) * 8;
+                if (i >= words) continue;
+                float y[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) y[q] = 0.f;
+#pragma unroll
+                for (int w = 0; w < GR; ++w) {
+                    const float f = ml[w][r].x;
+                    const float4 *x = reinterpret_cast<const float4 *>(sums + (w * S::kRows + r) * S::kSumPitch + e);
+                    const float4 x0 = x[0], x1 = x[1];
+                    y[0] = fmaf(f, x0.x, y[0]), y[1] = fmaf(f, x0.y, y[1]);
+                    y[2] = fmaf(f, x0.z, y[2]), y[3] = fmaf(f, x0.w, y[3]);
+                    y[4] = fmaf(f, x1.x, y[4]), y[5] = fmaf(f, x1.y, y[5]);
+                    y[6] = fmaf(f, x1.z, y[6]), y[7] = fmaf(f, x1.w, y[7]);
+                }
+                if (slot < 0) {
+                    const float inv = inverses[r];
+                    float by[8];
+                    if (a.gate) gate[k].to(by);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) y[q] *= a.gate ? inv * sigmoid(by[q]) : inv;
+                    const RowPlace p = row_place(a, u, r);
+                    store8((T *)a.out + p.token * a.os + p.head * a.oh + e, a.out_words, y);
+                } else {
+                    float4 *to = reinterpret_cast<float4 *>(a.sums + ((int64_t)slot * S::kRows + r) * D + e);
+                    to[0] = make_float4(y[0], y[1], y[2], y[3]);
+                    to[1] = make_float4(y[4], y[5], y[6], y[7]);
+                }
             }
         }
     });
