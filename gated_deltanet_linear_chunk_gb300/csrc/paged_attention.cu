@@ -5,32 +5,105 @@
 namespace gdn {
 namespace {
 
-constexpr int kJoinThreads = 256, kJoinBlocks = 16 * kGridSms;
+constexpr int kJoinThreads = 256, kJoinBlocks = 8 * kGridSms, kJoinAlone = 12;
 
-// The pieces of one unit: block x is the block that left the first, y its rows,
-// every gridDim.y-th.  Threads are four elements of a row each, several pieces
-// at a time.
+// The join of a unit: four elements of the sums of piece i, times f.
+template <int D>
+__device__ __forceinline__ void add_piece(const AttentionArgs &a, float4 &y, int slot, int rows, int r,
+                                          int word, float f) {
+    const float4 x =
+        reinterpret_cast<const float4 *>(a.sums)[((int64_t)slot * rows + r) * (D / 4) + word];
+    y.x = fmaf(f, x.x, y.x);
+    y.y = fmaf(f, x.y, y.y);
+    y.z = fmaf(f, x.z, y.z);
+    y.w = fmaf(f, x.w, y.w);
+}
+template <typename T>
+__device__ __forceinline__ void store_joined(const AttentionArgs &a, const RowPlace &p, int e, float inv,
+                                             const float4 &y) {
+    const float x[4] = {y.x, y.y, y.z, y.w};
+    const T *gate = a.gate ? (const T *)a.gate + p.token * a.gs + p.head * a.gh + e : nullptr;
+    T *out = (T *)a.out + p.token * a.os + p.head * a.oh + e;
+    float by[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) by[i] = gate ? to_f32(gate[i]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = from_f32<T>(gate ? x[i] * inv * sigmoid(by[i]) : x[i] * inv);
+}
+
+// Joins the pieces of one unit.  Block x is the unit, or where there are more
+// units than groups the group that left its first piece; y are its rows, every
+// gridDim.y-th.  Few pieces are a warp's work, a row each; many are a block's:
+// threads take four elements of a row, several pieces at a time.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
-gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows) {
-    constexpr int WORDS = D / 4, TEAMS = kJoinThreads / WORDS;
+gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows, int groups, bool by_unit) {
+    constexpr int WORDS = D / 4, TEAMS = kJoinThreads / WORDS, WARPS = kJoinThreads / 32;
     constexpr float kNone = -__builtin_huge_valf();
-    __shared__ float weight[kAttentionBlocks + 1];
-    __shared__ float tops[kJoinThreads / 32], totals[kJoinThreads / 32];
+    __shared__ float weight[kAttentionGroups + 1];
+    __shared__ float tops[WARPS], totals[WARPS];
     __shared__ float4 parts[kJoinThreads];
-    ptx::griddep_wait();
-    const int block = blockIdx.x;
-    const int4 join = a.joins[block];
-    Unit u;
-    u.n = join.x;
-    if (u.n < 0) return;
-    u.head = join.y / a.row_blocks;
-    u.first_row = join.y % a.row_blocks * rows;
-    u.rows = min(rows, a.R - u.first_row);
-    const int pieces = join.z + 1;
-    // The first piece ends its block's range, the others begin theirs.
-    auto slot = [&](int i) { return i == 0 ? 2 * block + 1 : 2 * (block + i); };
+    __shared__ int4 unit_join;
+    __shared__ int at;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int group = blockIdx.x;
+    if (by_unit) {
+        const int per_seq = a.Hkv * a.row_blocks;
+        const int n = blockIdx.x / per_seq, unit = blockIdx.x % per_seq;
+        if (threadIdx.x == 0) at = -1;
+        ptx::griddep_wait();
+        __syncthreads();
+        for (int i = threadIdx.x; i < groups; i += kJoinThreads) {
+            const int4 j = a.joins[i];
+            if (j.x == n && j.y == unit) at = i, unit_join = j;
+        }
+        __syncthreads();
+        group = at;
+        if (group < 0) return;
+    } else {
+        ptx::griddep_wait();
+    }
+    const int4 join = by_unit ? unit_join : a.joins[group];
+    if (join.x < 0) return;
+    const Unit u = [&] {
+        Unit v;
+        v.n = join.x;
+        v.head = join.y / a.row_blocks;
+        v.first_row = join.y % a.row_blocks * rows;
+        v.rows = min(rows, a.R - v.first_row);
+        v.len = 0;
+        return v;
+    }();
+    const int pieces = join.z + 1;
+    // The first piece ends its group's range, the others begin theirs.
+    auto slot = [&](int i) { return i == 0 ? 2 * group + 1 : 2 * (group + i); };
+
+    if (pieces <= kJoinAlone) {
+        for (int r = blockIdx.y * WARPS + warp; r < u.rows; r += gridDim.y * WARPS) {
+            const float2 s = lane < pieces ? a.stats[slot(lane) * rows + r] : make_float2(kNone, 0.f);
+            float top = s.x;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float f = ex2(s.x - against(top));
+            const float total = warp_sum(s.y * f);
+            const bool some = s.x != kNone || s.y != 0.f;
+            const unsigned have = __ballot_sync(0xffffffffu, some);
+            const RowPlace p = row_place(a, u, r);
+#pragma unroll
+            for (int w = lane; w < WORDS; w += 32) {
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int i = 0; i < pieces; ++i) {
+                    const float fi = __shfl_sync(0xffffffffu, f, i);
+                    if (have >> i & 1) add_piece<D>(a, y, slot(i), rows, r, w, fi);
+                }
+                store_joined<T>(a, p, w * 4, inverse(total), y);
+            }
+            if (lane == 0) store_lse(a, p, top, total);
+        }
+        return;
+    }
+
     const int team = threadIdx.x / WORDS, word = threadIdx.x % WORDS;
     for (int r = blockIdx.y; r < u.rows; r += gridDim.y) {
         float top = kNone;
@@ -41,12 +114,12 @@ gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows) {
         if (lane == 0) tops[warp] = top;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, tops[w]);
+        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, tops[w]);
         float total = 0.f;
         for (int i = threadIdx.x; i < pieces; i += kJoinThreads) {
             const float2 s = a.stats[slot(i) * rows + r];
             const float f = ex2(s.x - against(top));
-            weight[i] = f;
+            weight[i] = s.x == kNone && s.y == 0.f ? -1.f : f;  // -1: a piece without sums
             total += s.y * f;
         }
         total = warp_sum(total);
@@ -54,37 +127,31 @@ gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows) {
         __syncthreads();
         total = 0.f;
 #pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) total += totals[w];
-
+        for (int w = 0; w < WARPS; ++w) total += totals[w];
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
         for (int i = team; i < pieces; i += TEAMS) {
-            const float4 x = reinterpret_cast<const float4 *>(
-                a.sums)[((int64_t)slot(i) * rows + r) * WORDS + word];
             const float f = weight[i];
-            y.x = fmaf(f, x.x, y.x);
-            y.y = fmaf(f, x.y, y.y);
-            y.z = fmaf(f, x.z, y.z);
-            y.w = fmaf(f, x.w, y.w);
+            if (f != -1.f) add_piece<D>(a, y, slot(i), rows, r, word, f);
         }
         parts[threadIdx.x] = y;
         __syncthreads();
         const RowPlace p = row_place(a, u, r);
-        const float inv = inverse(total);
-        for (int e = threadIdx.x; e < D; e += kJoinThreads) {
-            float sum = 0.f;
+        if (threadIdx.x < WORDS) {
 #pragma unroll
-            for (int t = 0; t < TEAMS; ++t)
-                sum += reinterpret_cast<const float *>(&parts[t * WORDS])[e];
-            const T *gate = a.gate ? (const T *)a.gate + p.token * a.gs + p.head * a.gh + e : nullptr;
-            ((T *)a.out)[p.token * a.os + p.head * a.oh + e] = from_f32<T>(finish(sum, inv, gate));
+            for (int t = 1; t < TEAMS; ++t) {
+                const float4 x = parts[t * WORDS + threadIdx.x];
+                y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
+            }
+            store_joined<T>(a, p, threadIdx.x * 4, inverse(total), y);
         }
         if (threadIdx.x == 0) store_lse(a, p, top, total);
     }
 }
 
 struct Plan {
-    int rows, blocks, chunk;
+    int rows, blocks, groups;
+    int64_t units;
     bool split;
     size_t joins, stats, sums;  // bytes
 };
@@ -96,16 +163,15 @@ Plan plan(const gdn_attention_problem &p, const gdn_paged_cache &c) {
                              : c.dtype == GDN_E4M3 ? shape_e4m3(R, p.head_dim)
                                                    : shape_bf16(R, p.head_dim);
     pl.rows = s.rows;
-    pl.chunk = s.chunk;
-    const int64_t units = (int64_t)c.num_seqs * p.kv_heads * ((R + s.rows - 1) / s.rows);
-    const int64_t chunks =
-        ((int64_t)c.max_pages * c.page_size + s.chunk - 1) / s.chunk;  // of a unit, at most
-    const int64_t all = units * (chunks > 1 ? chunks : 1);
-    pl.blocks = (int)(all < s.blocks ? all : s.blocks);
-    pl.split = chunks > 1;
-    pl.joins = pl.split ? (size_t)pl.blocks * sizeof(int4) : 0;
-    pl.stats = pl.split ? (size_t)pl.blocks * 2 * s.rows * sizeof(float2) : 0;
-    pl.sums = pl.split ? (size_t)pl.blocks * 2 * s.rows * p.head_dim * sizeof(float) : 0;
+    pl.units = (int64_t)c.num_seqs * p.kv_heads * ((R + s.rows - 1) / s.rows);
+    const int64_t tiles = 1 + ((int64_t)c.max_pages * c.page_size + s.tokens - 1) / s.tokens;
+    const int64_t need = (pl.units * tiles + s.groups - 1) / s.groups;  // blocks, at most
+    pl.blocks = (int)(need < s.blocks ? need : s.blocks);
+    pl.groups = pl.blocks * s.groups;
+    pl.split = c.max_pages > 0;  // a sequence without room is its tile without tokens
+    pl.joins = pl.split ? ((size_t)pl.groups * sizeof(int4)) : 0;
+    pl.stats = pl.split ? (size_t)pl.groups * 2 * s.rows * sizeof(float2) : 0;
+    pl.sums = pl.split ? (size_t)pl.groups * 2 * s.rows * p.head_dim * sizeof(float) : 0;
     return pl;
 }
 
@@ -118,10 +184,13 @@ gdn_status join(const AttentionArgs &a, const Plan &pl, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const int rows = pl.rows < a.R ? pl.rows : a.R, fit = kJoinBlocks / pl.blocks;
-    cfg.gridDim = dim3(pl.blocks, rows < fit ? rows : fit);
+    const bool by_unit = pl.units <= pl.groups;
+    const int x = by_unit ? (int)pl.units : pl.groups;
+    const int rows = pl.rows < a.R ? pl.rows : a.R, fit = kJoinBlocks > x ? kJoinBlocks / x : 1;
+    cfg.gridDim = dim3(x, rows < fit ? rows : fit);
     cfg.blockDim = dim3(kJoinThreads);
-    return cudaLaunchKernelEx(&cfg, gdn_attention_join_kernel<T, D>, a, pl.rows) == cudaSuccess
+    return cudaLaunchKernelEx(&cfg, gdn_attention_join_kernel<T, D>, a, pl.rows, pl.groups,
+                              by_unit) == cudaSuccess
                ? GDN_OK
                : GDN_ERR_CUDA;
 }

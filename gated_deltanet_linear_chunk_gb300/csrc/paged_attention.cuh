@@ -5,12 +5,13 @@
 // times query heads of the group) that attend to it; the softmax runs in one
 // pass over the unit's tokens with a running maximum and sum.  The cache is
 // read once, which bounds the operator, and every SM has to read its share of
-// it, whatever the lengths are: the chunks (of a fixed number of tokens) of all
-// units, one unit after the other, are divided evenly among the blocks, which
-// find their place from the lengths on the device.  A block's range begins and
-// ends inside units: what it has of those goes to the workspace, one piece for
-// the range's begin and one for its end, and a second launch joins the pieces
-// in their order.
+// it, whatever the lengths are: the tiles (of a fixed number of tokens) of all
+// units, one unit after the other, are divided evenly among groups of warps,
+// which find their place from the lengths on the device.  A unit counts one
+// tile more than it has: what its queries and results cost; that tile has no
+// tokens.  A group's range begins and ends inside units: what it has of those
+// goes to the workspace, one piece for the range's begin and one for its end,
+// and a second launch joins the pieces in their order.
 #pragma once
 
 #include "attention.cuh"
@@ -34,9 +35,9 @@ struct AttentionArgs {
     bool q_words, gate_words, out_words;  // rows of q, gate and out in whole 16-byte words
     float scale_log2;  // scale log2 e: scores in powers of two
     // workspace
-    int4 *joins;     // [blocks] the unit whose first piece the block left: n, unit, blocks after it
-    float2 *stats;   // [blocks, 2, row block] maximum and sum
-    float *sums;     // [blocks, 2, row block, D]
+    int4 *joins;     // [groups] the unit whose first piece the group left: n, unit, groups after it
+    float2 *stats;   // [groups, 2, row block] maximum and sum; -infinity and 0: no sums
+    float *sums;     // [groups, 2, row block, D]
 };
 
 // Rows of a unit's row block: tokens t = r / G, heads h G + r % G.
@@ -47,37 +48,40 @@ struct Unit {
 __device__ __forceinline__ int held_tokens(const AttentionArgs &a, int n) {
     return min(max(a.lens[n], 0), a.capacity);
 }
-template <int CHUNK> __device__ __forceinline__ int chunks_of(int len) {
-    return max(1, (len + CHUNK - 1) / CHUNK);  // an empty sequence has its rows to write
+// One without tokens comes first.
+template <int TOKENS> __device__ __forceinline__ int tiles_of(int len) {
+    return 1 + (len + TOKENS - 1) / TOKENS;
 }
 
-// A block's range of chunks.  (No more blocks than chunks have one: pieces of a
-// unit are those of blocks that follow one another.)
+// A group's range of tiles, and that of its block's groups together.  (No more
+// groups than tiles have one: pieces of a unit are those of groups that follow
+// one another.)
 struct Range {
-    int64_t begin, end, total;
-    int block, blocks;
+    int64_t begin, end, total, block_end;
+    int group, groups;
     int n;          // the sequence it begins in
-    int64_t base;   // that sequence's first chunk
+    int64_t base;   // that sequence's first tile
 };
 
-// The first chunk of block b, and the block of a chunk.
-__device__ __forceinline__ int64_t first_chunk(int64_t total, int blocks, int b) {
-    return total * b / blocks;
+// The first tile of a group, and the group of a tile.
+__host__ __device__ __forceinline__ int64_t first_tile(int64_t total, int groups, int group) {
+    return group < groups ? total * group / groups : total;
 }
-__device__ __forceinline__ int block_of(int64_t total, int blocks, int64_t chunk) {
-    return (int)(((chunk + 1) * blocks - 1) / total);
+__host__ __device__ __forceinline__ int group_of(int64_t total, int groups, int64_t tile) {
+    return (int)(((tile + 1) * groups - 1) / total);
 }
 
 // By all threads of a block: sums over the sequences, a run of them per thread.
-template <int CHUNK, int THREADS>
-__device__ Range find_range(const AttentionArgs &a, int per_seq) {
-    __shared__ int64_t warp_sums[THREADS / 32], found_base;
-    __shared__ int found;
+// `mine`: the thread's group in the block, of GROUPS.
+template <int TOKENS, int THREADS, int GROUPS>
+__device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
+    __shared__ int64_t warp_sums[THREADS / 32], found_base[GROUPS];
+    __shared__ int found[GROUPS];
     const int run = (a.N + THREADS - 1) / THREADS;
     const int n0 = min((int)threadIdx.x * run, a.N), n1 = min(n0 + run, a.N);
-    int64_t mine = 0;
-    for (int n = n0; n < n1; ++n) mine += chunks_of<CHUNK>(held_tokens(a, n));
-    int64_t upto = mine;
+    int64_t count = 0;
+    for (int n = n0; n < n1; ++n) count += tiles_of<TOKENS>(held_tokens(a, n));
+    int64_t upto = count;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -85,6 +89,7 @@ __device__ Range find_range(const AttentionArgs &a, int per_seq) {
         if (lane >= o) upto += below;
     }
     if (lane == 31) warp_sums[warp] = upto;
+    if (threadIdx.x < GROUPS) found[threadIdx.x] = 0, found_base[threadIdx.x] = 0;
     __syncthreads();
     int64_t total = 0;
 #pragma unroll
@@ -94,27 +99,30 @@ __device__ Range find_range(const AttentionArgs &a, int per_seq) {
     }
     Range r;
     r.total = total * per_seq;
-    r.block = blockIdx.x;
-    r.blocks = (int)min((int64_t)gridDim.x, r.total);
-    r.begin = r.block < r.blocks ? first_chunk(r.total, r.blocks, r.block) : r.total;
-    r.end = r.block < r.blocks ? first_chunk(r.total, r.blocks, r.block + 1) : r.total;
-    if (threadIdx.x == 0) found = 0;
-    __syncthreads();
-    int64_t base = (upto - mine) * per_seq;
-    if (r.begin >= base && r.begin < upto * per_seq) {
+    r.groups = (int)min((int64_t)gridDim.x * GROUPS, r.total);
+    const int64_t base = (upto - count) * per_seq;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+        const int64_t begin = first_tile(r.total, r.groups, blockIdx.x * GROUPS + g);
+        if (begin < base || begin >= upto * per_seq) continue;
+        int64_t at = base;
         for (int n = n0; n < n1; ++n) {
-            const int64_t next = base + (int64_t)chunks_of<CHUNK>(held_tokens(a, n)) * per_seq;
-            if (r.begin < next) {
-                found = n;
-                found_base = base;
+            const int64_t next = at + (int64_t)tiles_of<TOKENS>(held_tokens(a, n)) * per_seq;
+            if (begin < next) {
+                found[g] = n;
+                found_base[g] = at;
                 break;
             }
-            base = next;
+            at = next;
         }
     }
     __syncthreads();
-    r.n = found;
-    r.base = found_base;
+    r.group = blockIdx.x * GROUPS + mine;
+    r.begin = first_tile(r.total, r.groups, r.group);
+    r.end = first_tile(r.total, r.groups, r.group + 1);
+    r.block_end = first_tile(r.total, r.groups, (blockIdx.x + 1) * GROUPS);
+    r.n = found[mine];
+    r.base = found_base[mine];
     return r;
 }
 
@@ -132,40 +140,59 @@ __device__ __forceinline__ int seen_by(const AttentionArgs &a, const Unit &u, in
     return u.len - a.L + 1 + (u.first_row + r) / a.G;
 }
 
-// Runs `piece(unit, first token, last token, slot)` over a block's range; slot
-// -1: the whole unit, else the workspace's.
-template <int CHUNK, int ROWS, typename F>
-__device__ __forceinline__ void for_pieces(const AttentionArgs &a, const Range &g, F &&piece) {
+// What a group has of a unit: tiles [first, last) of `tiles`.
+struct Piece {
+    int unit, tiles, first, last;
+    __device__ __forceinline__ bool whole() const { return first == 0 && last == tiles; }
+    // The workspace's slot: the begin of a unit ends its group's range.
+    __device__ __forceinline__ int slot(int group) const { return 2 * group + (first == 0 ? 1 : 0); }
+    template <int TOKENS> __device__ __forceinline__ int first_token(int len) const {
+        return min(max(first - 1, 0) * TOKENS, len);
+    }
+    template <int TOKENS> __device__ __forceinline__ int last_token(int len) const {
+        return min((last - 1) * TOKENS, len);
+    }
+};
+template <int ROWS>
+__device__ __forceinline__ Unit unit_of(const AttentionArgs &a, int n, int unit, int len) {
+    Unit u;
+    u.n = n;
+    u.head = unit / a.row_blocks;
+    u.first_row = unit % a.row_blocks * ROWS;
+    u.rows = min(ROWS, a.R - u.first_row);
+    u.len = len;
+    return u;
+}
+// The join of a unit whose first tile is `at`, from a group's piece on.
+__device__ __forceinline__ int4 join_from(const Range &g, int group, int n, const Piece &p, int64_t at) {
+    if (p.first != 0 || p.last == p.tiles) return make_int4(-1, 0, 0, 0);
+    return make_int4(n, p.unit, group_of(g.total, g.groups, at + p.tiles - 1) - group, 0);
+}
+
+// Runs `work(unit, piece)` over a group's range; its last join.
+template <int TOKENS, int ROWS, typename F>
+__device__ __forceinline__ int4 for_pieces(const AttentionArgs &a, const Range &g, F &&work) {
     const int per_seq = a.Hkv * a.row_blocks;
     int4 join = make_int4(-1, 0, 0, 0);
-    if (g.begin >= g.end) {
-        if (a.joins && threadIdx.x == 0) a.joins[g.block] = join;
-        return;
-    }
-    int n = g.n, len = held_tokens(a, n), chunks = chunks_of<CHUNK>(len);
-    int unit = (int)((g.begin - g.base) / chunks), c = (int)((g.begin - g.base) % chunks);
+    if (g.begin >= g.end) return join;
+    int n = g.n, len = held_tokens(a, n);
+    Piece p;
+    p.tiles = tiles_of<TOKENS>(len);
+    p.unit = (int)((g.begin - g.base) / p.tiles);
+    p.first = (int)((g.begin - g.base) % p.tiles);
     for (int64_t pos = g.begin; pos < g.end;) {
-        const int c1 = (int)min((int64_t)chunks, c + (g.end - pos));
-        Unit u;
-        u.n = n;
-        u.head = unit / a.row_blocks;
-        u.first_row = unit % a.row_blocks * ROWS;
-        u.rows = min(ROWS, a.R - u.first_row);
-        u.len = len;
-        const bool first = c == 0, last = c1 == chunks;
-        if (first && !last)  // the pieces after it: up to the block of the unit's last chunk
-            join = make_int4(n, unit, block_of(g.total, g.blocks, pos + chunks - 1) - g.block, 0);
-        piece(u, min(c * CHUNK, len), min(c1 * CHUNK, len),
-              first && last ? -1 : 2 * g.block + (first ? 1 : 0));
-        pos += c1 - c;
-        c = 0;
-        if (++unit == per_seq && pos < g.end) {
-            unit = 0;
+        p.last = (int)min((int64_t)p.tiles, p.first + (g.end - pos));
+        join = join_from(g, g.group, n, p, pos - p.first);
+        work(unit_of<ROWS>(a, n, p.unit, len), p);
+        pos += p.last - p.first;
+        p.first = 0;
+        if (++p.unit == per_seq && pos < g.end) {
+            p.unit = 0;
             len = held_tokens(a, ++n);
-            chunks = chunks_of<CHUNK>(len);
+            p.tiles = tiles_of<TOKENS>(len);
         }
     }
-    if (a.joins && threadIdx.x == 0) a.joins[g.block] = join;
+    return join;
 }
 
 // A row's element i, divided by the sum and gated.
@@ -216,12 +243,12 @@ template <int E> __device__ __forceinline__ void load_cached(const __nv_fp8_e4m3
     }
 }
 
-// What a kernel takes at a time, for units of R rows: rows, the chunk, and its
-// blocks on a GB300.
+// What a kernel takes at a time, for units of R rows: rows, the tokens of a
+// tile, its groups per block and its blocks on a GB300.
 struct AttentionShape {
-    int rows, chunk, blocks;
+    int rows, tokens, groups, blocks;
 };
-constexpr int kAttentionBlocks = 2 * kGridSms;  // at most
+constexpr int kAttentionGroups = 8 * kGridSms;  // at most
 AttentionShape shape_f32(int R, int D);
 AttentionShape shape_bf16(int R, int D);
 AttentionShape shape_e4m3(int R, int D);

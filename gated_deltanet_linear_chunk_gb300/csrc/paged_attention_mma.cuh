@@ -1,21 +1,20 @@
 // paged_attention_mma.cuh -- the attention of paged_attention.cuh for bf16
 // queries over a bf16 or an 8-bit cache.
 //
-// The rows of a unit (query heads that share a key head, times new tokens)
-// are the rows of small matrix products with the unit's tokens, so every
-// element of the cache takes part in as many products as there are rows: far
-// fewer than the 256 or so per byte at which a GB300's tensor cores would bound the
-// operator, and more than fp32 units do beside a stream at full bandwidth.  So
-// the products are warp-wide ones (m16n8k16) straight from the tiles that the
-// copies land in, which have no setup, and the design is about keeping copies
-// in flight: every group of warps has a ring of half stages (a tile's keys, then
-// its values) that asynchronous copies fill ahead, and no barrier but those of
-// the warps that share the ring.
-//   keys     S = Q K^T: a warp has 16 rows, and the scores of a tile's tokens
+// Every element of the cache takes part in as many products as there are rows
+// (query heads that share a key head, times new tokens): far fewer than the 280
+// per byte at which a GB300's tensor cores would bound the operator, and more
+// than fp32 units do beside a stream at full bandwidth.  So the products are
+// warp-wide ones (m16n8k16) straight from the tiles that the copies land in,
+// which have no setup, and the design is about keeping copies in flight: a
+// group of warps has a ring of half stages (a tile's keys, then its values) that
+// asynchronous copies fill ahead, over the units' ends, and no barrier but that
+// of the warps that share the ring.  Most groups are one warp.
+//   keys     S^T = K Q^T: 16 tokens by 8 rows at a time, so that eight rows (the
+//            usual group of query heads) leave no part of a product empty
 //   softmax  a running maximum and sum per row; sums are scaled down only when a
 //            maximum grows by more than 2^8, weights are up to that
-//   values   O += P V: 16 rows of D sums in registers
-// Groups take the tiles of a block's piece in turn and are joined at its end.
+//   values   O^T += V^T P^T: 16 elements by 8 rows
 #pragma once
 
 #include "paged_attention.cuh"
@@ -35,6 +34,12 @@ __device__ __forceinline__ void load_matrices_transposed(uint32_t (&r)[4], uint3
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(at)
                  : "memory");
+}
+// A lane's elements (row lane / 4, two columns) of an 8 x 8 matrix, transposed.
+__device__ __forceinline__ uint32_t transpose_matrix(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
 }
 // c += a b, 16 x 8 x 16, of bf16 or fp16.
 template <bool HALF>
@@ -84,50 +89,51 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, bool words, const float
     }
 }
 
-// What a variant keeps in shared memory.  EIGHT: an 8-bit cache; MT tiles of 16
-// rows, each of one warp, share a ring; GR such groups.
-template <bool EIGHT, int D, int MT, int GR> struct Tiles {
+// What a variant keeps in shared memory.  EIGHT: an 8-bit cache; NB blocks of 8
+// rows per warp, MT warps that share a ring, GR such groups.
+template <bool EIGHT, int D, int NB, int MT, int GR> struct Tiles {
     static constexpr int kRowBytes = D * (EIGHT ? 1 : 2);
     static constexpr int kPitch = kRowBytes + 16;  // rows of a matrix on different banks
     static constexpr int kTokens = 8192 / kRowBytes < 64 ? 8192 / kRowBytes : 64;
     static constexpr int kTile = kTokens * kPitch;
-    static constexpr int kThreads = MT * GR * 32, kRows = MT * 16;
-    static constexpr int kQueryPitch = D * 2 + 16;
-    static constexpr int kQueries = kRows * kQueryPitch;
-    static constexpr int kRoom = 115712 - 512;  // of two blocks per SM, each
-    static constexpr int kFit = (kRoom - kQueries) / (GR * kTile);
+    static constexpr int kThreads = MT * GR * 32, kWarpRows = NB * 8, kRows = MT * kWarpRows;
+    // Eight rows' sums, on their way out: in a stage that is free, or where
+    // warps share a ring in a place of each warp's own.
+    static constexpr int kSumPitch = D + 4;
+    static constexpr int kSums = 8 * kSumPitch * 4;
+    static constexpr int kOwn = MT > 1 ? MT * GR * kSums : 0;
+    static constexpr int kRoom = 115712 - 1024;  // of two blocks per SM, each
+    static constexpr int kFit = (kRoom - kOwn) / (GR * kTile);
     static constexpr int kStages = kFit >= 9 ? 9 : kFit % 2 ? kFit : kFit - 1;  // odd
-    static constexpr int kSumPitch = D + (EIGHT ? 16 : 8);
     static constexpr int kRing = GR * kStages * kTile;
-    static constexpr int kBytes = kQueries + kRing;
-    static constexpr int kChunk = 4 * kTokens;
-    static_assert(kStages >= 3, "");
-    static_assert(GR * kRows * kSumPitch * 4 <= kRing, "");
-    static_assert(kChunk % (GR * kTokens) == 0, "");
+    static constexpr int kBytes = kRing + kOwn;
+    static_assert(kStages >= 3 && kSums <= kTile, "");
+    static_assert(GR == 1 || GR * kRows * kSumPitch * 4 <= kBytes, "");
 };
 
-template <bool EIGHT, int D, int MT, int GR>
+template <bool EIGHT, int D, int NB, int MT, int GR>
 __global__ void __launch_bounds__(MT *GR * 32, 2)
 gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
-    using S = Tiles<EIGHT, D, MT, GR>;
+    using S = Tiles<EIGHT, D, NB, MT, GR>;
     using T = __nv_bfloat16;
-    constexpr int TK = S::kTokens, NT = TK / 8, ST = S::kStages, AHEAD = (ST - 1) / 2;
-    constexpr int WORDS = S::kRowBytes / 16;           // of a token's row
-    constexpr int PER = MT * 32 / WORDS;               // rows that a group copies at once
-    constexpr int HOLD = (TK + 31) / 32;               // rows whose place a lane knows
+    constexpr int TK = S::kTokens, TT = TK / 16, ST = S::kStages, AHEAD = (ST - 1) / 2;
+    constexpr int ES = EIGHT ? 1 : 2, DT = D / 16;
+    constexpr int WORDS = S::kRowBytes / 16;  // of a token's row
+    constexpr int PER = MT * 32 / WORDS;      // rows that a group copies at once
+    constexpr int HOLD = (TK + 31) / 32;      // rows whose place a lane knows
     extern __shared__ __align__(16) char smem[];
     __shared__ float2 ml[GR][S::kRows];
-    __shared__ float row_scale[S::kRows], inverses[S::kRows];
-    char *queries = smem, *ring = smem + S::kQueries;
-    float *sums = reinterpret_cast<float *>(ring);
+    __shared__ float inverses[S::kRows];
+    __shared__ int4 joined;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int group = warp / MT, mt = warp % MT;
     const int g8 = lane / 4, c4 = lane % 4;
-    const uint32_t mine = ptx::smem_u32(ring + group * ST * S::kTile);
-    // A lane's address in a key tile (tokens by elements) and in a value tile.
-    const uint32_t k_lane = EIGHT ? ((lane & 7) + (lane >> 3 & 1) * 8) * S::kPitch + (lane >> 4) * 16
-                                  : ((lane & 7) + (lane >> 4) * 8) * S::kPitch + (lane >> 3 & 1) * 16;
-    const uint32_t v_lane = ((lane & 7) + (lane >> 3 & 1) * 8) * S::kPitch + (lane >> 4) * 16;
+    char *ring = smem + group * ST * S::kTile;
+    const uint32_t ring_at = ptx::smem_u32(ring);
+    // A lane's address in a key tile and in a value tile (transposed).
+    const uint32_t k_lane = ((lane & 7) + (lane >> 3 & 1) * 8) * S::kPitch + (lane >> 4) * 16;
+    const uint32_t v_lane =
+        EIGHT ? k_lane : ((lane & 7) + (lane >> 4) * 8) * S::kPitch + (lane >> 3 & 1) * 16;
 
     auto group_sync = [&] {
         if constexpr (MT == 1) __syncwarp();
@@ -135,254 +141,351 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     };
 
     ptx::griddep_launch_dependents();
-    const Range range = find_range<S::kChunk, S::kThreads>(a, a.Hkv * a.row_blocks);
-    for_pieces<S::kChunk, S::kRows>(a, range, [&](const Unit &u, int t0, int t1, int slot) {
-        const int tiles = (t1 - t0 + TK - 1) / TK;
-        const int own = tiles > group ? (tiles - group + GR - 1) / GR : 0;  // this group's
-        auto first_token = [&](int i) { return t0 + (i * GR + group) * TK; };
-        const int32_t *table = a.table + u.n * a.table_stride;
+    const int per_seq = a.Hkv * a.row_blocks;
+    const Range range = find_range<TK, S::kThreads, GR>(a, per_seq, group);
+
+    // ---- the copies, ahead of the products.  The cursor is at the tile whose
+    // entries of the page table are on their way.
+    struct {
+        int64_t left;  // tiles of the range from this one on
+        int n, unit, tile, tiles, len;
+    } c;
+    c.left = range.end - range.begin;
+    c.n = range.n;
+    c.len = c.left > 0 ? held_tokens(a, c.n) : 0;
+    c.tiles = tiles_of<TK>(c.len);
+    c.unit = (int)((range.begin - range.base) / c.tiles);
+    c.tile = (int)((range.begin - range.base) % c.tiles);
+    // Where a whole block lies inside one unit its groups' sums are joined
+    // here, and it has one piece: {whether, n, unit, its first and last tile}.
+    if (threadIdx.x == 0) {
+        const int64_t last = c.tile + range.block_end - range.begin;
+        joined = make_int4(GR > 1 && c.left > 0 && last <= c.tiles, c.n, c.unit,
+                           (c.tile == 0 ? 1 : 0) | (last == c.tiles ? 2 : 0));
+    }
+    Piece piece;
+    piece.unit = c.unit, piece.first = c.tile, piece.tiles = c.tiles;
+    int n = c.n, len = c.len;
+
+    int entry[HOLD];
+    auto look_up = [&] {
+        while (c.left > 0 && (c.tile == 0 || c.tile == c.tiles)) {  // no tokens
+            if (c.tile == c.tiles) {
+                c.tile = 0;
+                if (++c.unit == per_seq) {
+                    c.unit = 0;
+                    c.len = held_tokens(a, ++c.n);
+                    c.tiles = tiles_of<TK>(c.len);
+                }
+            }
+            ++c.tile, --c.left;
+        }
+#pragma unroll
+        for (int h = 0; h < HOLD; ++h) {
+            const int j = (c.tile - 1) * TK + h * 32 + lane;
+            entry[h] = -1;
+            if (c.left > 0 && h * 32 + lane < TK && j < c.len)
+                entry[h] = a.table[c.n * a.table_stride + j / a.page_size];
+        }
+    };
+    int64_t k_at[HOLD], v_at[HOLD];  // bytes from the cache's start; -1: none
+    uint32_t bad_tiles = 0;          // bit i: of the i-th tile ahead, a page out of range
+    auto place = [&](int ahead) {
+        const int head = c.unit / a.row_blocks;
         bool bad = false;
-
-        // The entries of tile i's rows, loaded a tile before they are needed.
-        int entry[HOLD];
-        auto look_up = [&](int i) {
 #pragma unroll
-            for (int h = 0; h < HOLD; ++h) {
-                const int j = first_token(i) + h * 32 + lane;
-                entry[h] = i < own && h * 32 + lane < TK && j < t1 ? table[j / a.page_size] : -1;
+        for (int h = 0; h < HOLD; ++h) {
+            const int j = (c.tile - 1) * TK + h * 32 + lane, p = entry[h];
+            k_at[h] = v_at[h] = -1;
+            if (!(c.left > 0 && h * 32 + lane < TK && j < c.len)) continue;
+            if (p < 0 || p >= a.num_pages) {
+                bad = true;
+                continue;
             }
-        };
-        int64_t k_at[HOLD], v_at[HOLD];  // bytes from the cache's start; -1: none
-        auto place = [&](int i) {
-#pragma unroll
-            for (int h = 0; h < HOLD; ++h) {
-                const int j = first_token(i) + h * 32 + lane, p = entry[h];
-                k_at[h] = v_at[h] = -1;
-                if (!(i < own && h * 32 + lane < TK && j < t1)) continue;
-                if (p < 0 || p >= a.num_pages) {
-                    bad = true;
-                    continue;
-                }
-                const int at = j % a.page_size;
-                k_at[h] = (p * a.kps + at * a.kts + u.head * a.khs) * (EIGHT ? 1 : 2);
-                v_at[h] = (p * a.vps + at * a.vts + u.head * a.vhs) * (EIGHT ? 1 : 2);
-            }
-        };
-        // Copies a half stage: rows that do not exist become zeros.
-        auto copy = [&](int stage, const void *from, const int64_t (&at)[HOLD]) {
-            const int sub = mt * 32 + lane, word = sub % WORDS;
-            char *to = ring + (group * ST + stage) * S::kTile + word * 16;
-#pragma unroll
-            for (int r0 = 0; r0 < TK; r0 += PER) {
-                const int r = r0 + sub / WORDS;
-                int64_t off = at[0];
-                off = __shfl_sync(0xffffffffu, at[0], r & 31);
-                if (HOLD > 1) {
-                    const int64_t upper = __shfl_sync(0xffffffffu, at[HOLD - 1], r & 31);
-                    off = r & 32 ? upper : off;
-                }
-                if (TK % PER == 0 || r < TK)
-                    copy_async_head(to + r * S::kPitch,
-                                    static_cast<const char *>(from) + (off < 0 ? 0 : off + word * 16),
-                                    off < 0 ? 0 : 16);
-            }
-            copies_commit();
-        };
-
-        __syncthreads();  // the last piece's sums
-        int stage = 0;
-        look_up(0);
-#pragma unroll 1
-        for (int i = 0; i < AHEAD; ++i) {
-            place(i);
-            look_up(i + 1);
-            copy(2 * i, a.k, k_at);
-            copy(2 * i + 1, a.v, v_at);
+            const int at = j % a.page_size;
+            k_at[h] = (p * a.kps + at * a.kts + head * a.khs) * ES;
+            v_at[h] = (p * a.vps + at * a.vts + head * a.vhs) * ES;
         }
-
-        // Queries, times the sign of the scale; for fp16 products each row over
-        // the power of two of its largest, in the order of an 8-bit key's
-        // elements (see below).  A thread has eight elements at a time, and all
-        // it takes are loaded together.
-        const float sign = a.scale_log2 < 0.f ? -1.f : a.scale_log2 == 0.f ? 0.f : 1.f;
-        {
-            constexpr int Q8 = D / 8, EACH = S::kRows * Q8 / S::kThreads, BATCH = EACH < 4 ? EACH : 4;
+        if (__any_sync(0xffffffffu, bad)) bad_tiles |= 1u << ahead;
+        if (c.left > 0) {
+            ++c.tile, --c.left;
+            look_up();
+        }
+    };
+    // Copies a half stage: rows that do not exist become zeros.
+    auto copy = [&](int stage, const void *from, const int64_t (&at)[HOLD]) {
+        const int sub = mt * 32 + lane, word = sub % WORDS;
+        char *to = ring + stage * S::kTile + word * 16;
+#pragma unroll
+        for (int r0 = 0; r0 < TK; r0 += PER) {
+            const int r = r0 + sub / WORDS;
+            int64_t off = __shfl_sync(0xffffffffu, at[0], r & 31);
+            if (HOLD > 1) {
+                const int64_t upper = __shfl_sync(0xffffffffu, at[HOLD - 1], r & 31);
+                off = r & 32 ? upper : off;
+            }
+            if (TK % PER == 0 || r < TK)
+                copy_async_head(to + r * S::kPitch,
+                                static_cast<const char *>(from) + (off < 0 ? 0 : off + word * 16),
+                                off < 0 ? 0 : 16);
+        }
+        copies_commit();
+    };
+    int stage = 0;  // the next to be used; the one before it is free
+    auto free_stage = [&] { return stage == 0 ? ST - 1 : stage - 1; };
+    look_up();
 #pragma unroll 1
-            for (int i0 = 0; i0 < EACH; i0 += BATCH) {
-                Vec<T, 8> x[BATCH];
+    for (int i = 0; i < AHEAD; ++i) {
+        place(i);
+        copy(2 * i, a.k, k_at);
+        copy(2 * i + 1, a.v, v_at);
+    }
+    __syncthreads();
+    const bool together = joined.x != 0;
+
+    // Sums of the piece's unit: element 16 d + g8 (and + 8; of 8-bit tiles 2 g8
+    // and + 1) of rows 8 b + 2 c4 (and + 1).
+    float o[DT][NB][4], m[NB][2], l[NB][2];
 #pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const int at = (i0 + i) * S::kThreads + threadIdx.x, r = at / Q8, e = at % Q8 * 8;
-                    x[i] = Vec<T, 8>::zero();
-                    if (r >= u.rows) continue;
-                    const RowPlace p = row_place(a, u, r);
-                    x[i] = load8(static_cast<const T *>(a.q) + p.token * a.qs + p.head * a.qh + e, a.q_words);
-                }
+    for (int b = 0; b < NB; ++b) {
 #pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const int at = (i0 + i) * S::kThreads + threadIdx.x, r = at / Q8, e = at % Q8 * 8;
-                    char *to = queries + r * S::kQueryPitch;
-                    float y[8];
-                    x[i].to(y);
+        for (int e = 0; e < 2; ++e) m[b][e] = kMinusInfinity, l[b][e] = 0.f;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] *= sign;
-                    if constexpr (EIGHT) {
-                        float top = 0.f;
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(y[k]));
+            for (int e = 0; e < 4; ++e) o[d][b][e] = 0.f;
+    }
+    // l of all tokens, from the lanes'.
+    auto total_sums = [&](bool bad) {
 #pragma unroll
-                        for (int d = Q8 / 2; d > 0; d >>= 1)
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        // 2^n <= top < 2^(n + 1), from the exponent's bits.
-                        const int n = top > 0x1p-120f && top < 0x1p120f ? (__float_as_int(top) >> 23) - 127 : 0;
-                        const float down = __int_as_float((127 - n) << 23);
-                        if (e == 0) row_scale[r] = __int_as_float((127 + n) << 23);
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            y[k] *= down;
-                            if (fabsf(y[k]) < __builtin_huge_valf()) y[k] = fminf(fmaxf(y[k], -65504.f), 65504.f);
-                        }
-                        // Elements 4 c + j of 16: pairs of j < 2 first.
-                        uint32_t *half = reinterpret_cast<uint32_t *>(to + (e & ~15) * 2) + (e & 8) / 4;
-                        half[0] = pack_weights<true>(y[0], y[1]);
-                        half[4] = pack_weights<true>(y[2], y[3]);
-                        half[1] = pack_weights<true>(y[4], y[5]);
-                        half[5] = pack_weights<true>(y[6], y[7]);
-                    } else {
-                        Vec<T, 8>::from(y).store(reinterpret_cast<T *>(to) + e);
-                    }
-                }
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
+                if (bad) l[b][e] = __int_as_float(0x7fffffff);
+            }
+    };
+    // Block b's sums times by[] as rows of D elements.
+    auto lay_out = [&](float *to, int b, float by0, float by1) {
+        to += c4 * 2 * S::kSumPitch;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            if constexpr (EIGHT) {
+                float2 *x = reinterpret_cast<float2 *>(to + d * 16 + g8 * 2);
+                x[0] = make_float2(o[d][b][0] * by0, o[d][b][2] * by0);
+                x[S::kSumPitch / 2] = make_float2(o[d][b][1] * by1, o[d][b][3] * by1);
+            } else {
+                float *x = to + d * 16 + g8;
+                x[0] = o[d][b][0] * by0;
+                x[8] = o[d][b][2] * by0;
+                x[S::kSumPitch] = o[d][b][1] * by1;
+                x[S::kSumPitch + 8] = o[d][b][3] * by1;
             }
         }
-        __syncthreads();
-        uint32_t qf[D / 16][4];
+    };
+
+    // ---- the products, unit by unit
+    int4 join = make_int4(-1, 0, 0, 0);
+    const float sign = a.scale_log2 < 0.f ? -1.f : a.scale_log2 == 0.f ? 0.f : 1.f;
+    const float magnitude = sign == 0.f ? 1.f : fabsf(a.scale_log2);
+    for (int64_t pos = range.begin; pos < range.end;) {
+        piece.last = (int)min((int64_t)piece.tiles, piece.first + (range.end - pos));
+        const Unit u = unit_of<S::kRows>(a, n, piece.unit, len);
+        const int t0 = piece.template first_token<TK>(len), t1 = piece.template last_token<TK>(len);
+
+        // Queries, times the sign of the scale: rows 8 b + g8, elements 16 k + 2 c4
+        // and + 8 (two each).  For an 8-bit cache elements 16 k + 4 c4 (four), in
+        // fp16, each row over the power of two of its largest.
+        uint32_t q[DT][NB][2];
+        float scale[NB][2];
+        int seen[NB][2];
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-            load_matrices(qf[k], ptx::smem_u32(queries) + (mt * 16 + (lane & 15)) * S::kQueryPitch +
-                                     k * 32 + (lane >> 4) * 16);
-        // Rows g8 and g8 + 8 of the tile.
-        const int row0 = mt * 16 + g8;
-        float scale[2];
-        int seen[2];
+        for (int b = 0; b < NB; ++b) {
+            const int r = mt * S::kWarpRows + b * 8 + g8;
+            const bool live = r < u.rows;
+            const RowPlace p = row_place(a, u, live ? r : 0);
+            const T *from = static_cast<const T *>(a.q) + p.token * a.qs + p.head * a.qh;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = row0 + e * 8;
-            scale[e] = (sign == 0.f ? 1.f : fabsf(a.scale_log2)) * (EIGHT ? row_scale[r] * a.k_scale[u.head] : 1.f);
-            seen[e] = min(t1, seen_by(a, u, r));
+            for (int k = 0; k < DT; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const T *x = from + k * 16 + (EIGHT ? c4 * 4 + h * 2 : c4 * 2 + h * 8);
+                    if (!live) q[k][b][h] = 0;
+                    else if (a.q_words) q[k][b][h] = *reinterpret_cast<const uint32_t *>(x);
+                    else q[k][b][h] = (uint32_t) reinterpret_cast<const uint16_t *>(x)[0] |
+                                      (uint32_t) reinterpret_cast<const uint16_t *>(x)[1] << 16;
+                }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float up = 1.f;
+            if constexpr (EIGHT) {
+                float top = 0.f;
+#pragma unroll
+                for (int k = 0; k < DT; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(q[k][b][h] << 16)),
+                                               fabsf(__uint_as_float(q[k][b][h] & 0xffff0000u))));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // 2^x <= top < 2^(x + 1), from the exponent's bits.
+                const int x = top > 0x1p-120f && top < 0x1p120f ? (__float_as_int(top) >> 23) - 127 : 0;
+                up = __int_as_float((127 + x) << 23);
+                const float down = __int_as_float((127 - x) << 23) * sign;
+                auto fit = [&](float v) {  // infinities stay, nothing becomes one
+                    const float y = v * down;
+                    return fabsf(v) < __builtin_huge_valf() ? fminf(fmaxf(y, -65504.f), 65504.f) : y;
+                };
+#pragma unroll
+                for (int k = 0; k < DT; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        q[k][b][h] = pack_weights<true>(fit(__uint_as_float(q[k][b][h] << 16)),
+                                                        fit(__uint_as_float(q[k][b][h] & 0xffff0000u)));
+            } else if (sign != 1.f) {
+#pragma unroll
+                for (int k = 0; k < DT; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        q[k][b][h] = pack_weights<false>(__uint_as_float(q[k][b][h] << 16) * sign,
+                                                         __uint_as_float(q[k][b][h] & 0xffff0000u) * sign);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                scale[b][e] = magnitude;
+                if (EIGHT) scale[b][e] *= a.k_scale[u.head] * __shfl_sync(0xffffffffu, up, (c4 * 2 + e) * 4);
+                seen[b][e] = min(t1, seen_by(a, u, mt * S::kWarpRows + b * 8 + c4 * 2 + e));
+            }
         }
         // From here on not every row sees a token.
-        const int all_see = min(t1, u.len - a.L + 1);
-
-        float o[D / 8][4], m[2] = {kMinusInfinity, kMinusInfinity}, l[2] = {0.f, 0.f};
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+        const int all_see = min(t1, len - a.L + 1);
+        bool bad = false;
 
 #pragma unroll 1
-        for (int i = 0; i < own; ++i) {
-            const int j0 = first_token(i);
+        for (int j0 = t0; j0 < t1; j0 += TK) {
             // ---- keys
             copies_wait<ST - 2>();
             group_sync();
-            {
-                const int to = stage + ST - 1;
-                place(i + AHEAD);
-                look_up(i + AHEAD + 1);
-                copy(to >= ST ? to - ST : to, a.k, k_at);
-            }
-            float s[NT][4];
+            place(AHEAD);
+            bad |= bad_tiles & 1;
+            bad_tiles >>= 1;
+            copy(free_stage(), a.k, k_at);
+            // Short chains of products: where they are few, even and odd steps
+            // have sums of their own.
+            constexpr int CHAINS = TT * NB < 4 ? 2 : 1;
+            float s[TT][NB][4], odd[CHAINS == 2 ? TT : 1][CHAINS == 2 ? NB : 1][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int t = 0; t < TT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-            const uint32_t keys = mine + stage * S::kTile + k_lane;
-            if constexpr (EIGHT) {
-                // A matrix is 8 tokens by 16 elements, of which a lane gets four
-                // that follow one another: two pairs, for both halves of k.
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int k = 0; k < D / 16; k += 2)
-#pragma unroll
-                    for (int n = 0; n < NT; n += 2) {
-                        uint32_t b[4];
-                        load_matrices(b, keys + n * 8 * S::kPitch + k * 16);
-                        multiply<true>(s[n], qf[k], widen(b[0]), widen(b[0] >> 16));
-                        multiply<true>(s[n + 1], qf[k], widen(b[1]), widen(b[1] >> 16));
-                        multiply<true>(s[n], qf[k + 1], widen(b[2]), widen(b[2] >> 16));
-                        multiply<true>(s[n + 1], qf[k + 1], widen(b[3]), widen(b[3] >> 16));
+                    for (int e = 0; e < 4; ++e) {
+                        s[t][b][e] = 0.f;
+                        if constexpr (CHAINS == 2) odd[t][b][e] = 0.f;
                     }
-            } else {
+            const uint32_t keys = ring_at + stage * S::kTile + k_lane;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
+            for (int k = 0; k < DT; k += EIGHT ? 2 : 1)
 #pragma unroll
-                    for (int n = 0; n < NT; n += 2) {
-                        uint32_t b[4];
-                        load_matrices(b, keys + n * 8 * S::kPitch + k * 32);
-                        multiply<false>(s[n], qf[k], b[0], b[1]);
-                        multiply<false>(s[n + 1], qf[k], b[2], b[3]);
+                for (int t = 0; t < TT; ++t) {
+                    uint32_t x[4];
+                    load_matrices(x, keys + t * 16 * S::kPitch + k * 16 * ES);
+                    if constexpr (EIGHT) {
+                        // A matrix is 8 tokens by 16 elements, of which a lane gets
+                        // four that follow one another: two pairs, for both halves
+                        // of k.
+                        const uint32_t y0[4] = {widen(x[0]), widen(x[1]), widen(x[0] >> 16), widen(x[1] >> 16)};
+                        const uint32_t y1[4] = {widen(x[2]), widen(x[3]), widen(x[2] >> 16), widen(x[3] >> 16)};
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            multiply<true>(s[t][b], y0, q[k][b][0], q[k][b][1]);
+                            if constexpr (CHAINS == 2) multiply<true>(odd[t][b], y1, q[k + 1][b][0], q[k + 1][b][1]);
+                            else multiply<true>(s[t][b], y1, q[k + 1][b][0], q[k + 1][b][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            if (CHAINS == 2 && k % 2)
+                                multiply<false>(odd[CHAINS == 2 ? t : 0][CHAINS == 2 ? b : 0], x, q[k][b][0], q[k][b][1]);
+                            else
+                                multiply<false>(s[t][b], x, q[k][b][0], q[k][b][1]);
+                        }
                     }
+                }
+            if constexpr (CHAINS == 2) {
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[t][b][e] += odd[t][b][e];
             }
             if (++stage == ST) stage = 0;
 
-            // ---- softmax
+            // ---- softmax: token 16 t + g8 (e < 2, else + 8), row 8 b + 2 c4 + e % 2
             const bool edge = j0 + TK > all_see;
             if (edge) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int t = 0; t < TT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (j0 + n * 8 + c4 * 2 + (e & 1) >= seen[e >> 1]) s[n][e] = kMinusInfinity;
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (j0 + t * 16 + g8 + (e >> 1) * 8 >= seen[b][e & 1]) s[t][b][e] = kMinusInfinity;
             }
-            float top[2] = {kMinusInfinity, kMinusInfinity};
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
+            float top[NB][2];
             bool grown = false;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
-                top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
-                top[e] *= scale[e];
-                grown |= top[e] > m[e] + 8.f;
-            }
-            if (__any_sync(0xffffffffu, grown)) {
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float next = fmaxf(m[e], top[e]), fade = ex2(m[e] - against(next));
-                    m[e] = next;
-                    l[e] *= fade;
+                    float x = fmaxf(s[0][b][e], s[0][b][e + 2]);
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        o[n][2 * e] *= fade;
-                        o[n][2 * e + 1] *= fade;
-                    }
+                    for (int t = 1; t < TT; ++t) x = fmaxf(x, fmaxf(s[t][b][e], s[t][b][e + 2]));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                    top[b][e] = x * scale[b][e];
+                    grown |= top[b][e] > m[b][e] + 8.f;
                 }
-            }
-            uint32_t p[NT / 2][4];
-            {
-                const float low[2] = {against(m[0]), against(m[1])};
+            if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float next = fmaxf(m[b][e], top[b][e]), fade = ex2(m[b][e] - against(next));
+                        m[b][e] = next;
+                        l[b][e] *= fade;
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) {
+                            o[d][b][e] *= fade;
+                            o[d][b][e + 2] *= fade;
+                        }
+                    }
+            }
+            uint32_t p[TT][NB][2];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float low[2] = {against(m[b][0]), against(m[b][1])};
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[n][e] = ex2(fmaf(s[n][e], scale[e >> 1], -low[e >> 1]));
-                        l[e >> 1] += s[n][e];
+                        s[t][b][e] = ex2(fmaf(s[t][b][e], scale[b][e & 1], -low[e & 1]));
+                        l[b][e & 1] += s[t][b][e];
                     }
-                    p[n / 2][n % 2 * 2] = pack_weights<EIGHT>(s[n][0], s[n][1]);
-                    p[n / 2][n % 2 * 2 + 1] = pack_weights<EIGHT>(s[n][2], s[n][3]);
+                    p[t][b][0] = transpose_matrix(pack_weights<EIGHT>(s[t][b][0], s[t][b][1]));
+                    p[t][b][1] = transpose_matrix(pack_weights<EIGHT>(s[t][b][2], s[t][b][3]));
                 }
             }
 
             // ---- values
             copies_wait<ST - 2>();
             group_sync();
-            {
-                const int to = stage + ST - 1;
-                copy(to >= ST ? to - ST : to, a.v, v_at);
-            }
-            const char *tile = ring + (group * ST + stage) * S::kTile;
-            const uint32_t values = mine + stage * S::kTile + v_lane;
+            copy(free_stage(), a.v, v_at);
+            const char *tile = ring + stage * S::kTile;
+            const uint32_t values = ring_at + stage * S::kTile + v_lane;
             // The newest tokens' values may be infinite or NaN where some rows
             // do not see them: a weight of zero would not keep them out.
             bool apart = false;
@@ -415,38 +518,39 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             };
             auto add_values = [&](auto masked) {
 #pragma unroll
-                for (int k = 0; k < NT / 2; ++k) {
-                    const int j = k * 16 + c4 * 2;
+                for (int t = 0; t < TT; ++t) {
+                    const int j = t * 16 + c4 * 2;
 #pragma unroll
-                    for (int n = 0; n < D / 8; n += EIGHT ? 4 : 2) {
-                        uint32_t b[4];
-                        load_matrices_transposed(b, values + k * 16 * S::kPitch + n * (EIGHT ? 8 : 16));
+                    for (int d = 0; d < DT; d += EIGHT ? 2 : 1) {
+                        uint32_t x[4];
+                        load_matrices_transposed(x, values + t * 16 * S::kPitch + d * 16 * ES);
                         if constexpr (EIGHT) {
-                            // A matrix is 8 tokens by 16 elements, of which a lane
-                            // gets two neighbours of two tokens: one for each of
-                            // two products, whose columns are even and odd elements.
-                            uint32_t lo[4], hi[4];
+                            // A matrix is 8 tokens by 16 elements, of which a lane gets
+                            // two neighbours of two tokens: rows g8 and g8 + 8 of the
+                            // product are even and odd elements.
+                            uint32_t y[2][4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const uint32_t x = widen(b[i]), y = widen(b[i] >> 16);
-                                lo[i] = __byte_perm(x, y, 0x5410);
-                                hi[i] = __byte_perm(x, y, 0x7632);
-                                if (masked) {
-                                    lo[i] = kept(lo[i], j + (i & 1) * 8);
-                                    hi[i] = kept(hi[i], j + (i & 1) * 8);
-                                }
+                                const uint32_t even = widen(x[i]), next = widen(x[i] >> 16);
+                                y[i / 2][i % 2 * 2] = __byte_perm(even, next, 0x5410);
+                                y[i / 2][i % 2 * 2 + 1] = __byte_perm(even, next, 0x7632);
                             }
-                            multiply<true>(o[n], p[k], lo[0], lo[1]);
-                            multiply<true>(o[n + 1], p[k], hi[0], hi[1]);
-                            multiply<true>(o[n + 2], p[k], lo[2], lo[3]);
-                            multiply<true>(o[n + 3], p[k], hi[2], hi[3]);
+                            if (masked) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) y[i / 4][i % 4] = kept(y[i / 4][i % 4], j + (i % 4 / 2) * 8);
+                            }
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) {
+                                multiply<true>(o[d][b], y[0], p[t][b][0], p[t][b][1]);
+                                multiply<true>(o[d + 1][b], y[1], p[t][b][0], p[t][b][1]);
+                            }
                         } else {
                             if (masked) {
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) b[i] = kept(b[i], j + (i & 1) * 8);
+                                for (int i = 0; i < 4; ++i) x[i] = kept(x[i], j + (i / 2) * 8);
                             }
-                            multiply<false>(o[n], p[k], b[0], b[1]);
-                            multiply<false>(o[n + 1], p[k], b[2], b[3]);
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) multiply<false>(o[d][b], x, p[t][b][0], p[t][b][1]);
                         }
                     }
                 }
@@ -456,68 +560,139 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             } else {
                 add_values(std::true_type());
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int t = 0; t < TT; ++t)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            const int j = n * 8 + c * 2 + b;
-                            const float w0 = __shfl_sync(0xffffffffu, s[n][b], (lane & ~3) + c);
-                            const float w1 = __shfl_sync(0xffffffffu, s[n][2 + b], (lane & ~3) + c);
+                        for (int i = 0; i < 8; ++i) {
+                            const int j = t * 16 + h * 8 + i;
+                            float w[NB][2];
+#pragma unroll
+                            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    w[b][e] = __shfl_sync(0xffffffffu, s[t][b][h * 2 + e], i * 4 + c4);
                             if (j < keep || j0 + j >= t1) continue;
-                            const bool see0 = j0 + j < seen[0], see1 = j0 + j < seen[1];
                             const char *row = tile + j * S::kPitch;
-                            auto add = [&](float &x0, float &x1, float v) {
-                                if (isfinite(v)) return;
-                                if (see0) x0 = fmaf(w0, v, x0);
-                                if (see1) x1 = fmaf(w1, v, x1);
-                            };
-                            if constexpr (EIGHT) {
 #pragma unroll
-                                for (int q = 0; q < D / 8; q += 2) {
-                                    const uint32_t x = *reinterpret_cast<const uint32_t *>(row + q * 8 + c4 * 4);
-                                    const float2 v = from_e4m3x2(x & 0xffff), y = from_e4m3x2(x >> 16);
-                                    add(o[q][0], o[q][2], v.x);
-                                    add(o[q + 1][0], o[q + 1][2], v.y);
-                                    add(o[q][1], o[q][3], y.x);
-                                    add(o[q + 1][1], o[q + 1][3], y.y);
-                                }
-                            } else {
+                            for (int d = 0; d < DT; ++d)
 #pragma unroll
-                                for (int q = 0; q < D / 8; ++q) {
-                                    const uint32_t x = *reinterpret_cast<const uint32_t *>(row + q * 16 + c4 * 4);
-                                    add(o[q][0], o[q][2], __uint_as_float(x << 16));
-                                    add(o[q][1], o[q][3], __uint_as_float(x & 0xffff0000u));
+                                for (int k = 0; k < 2; ++k) {
+                                    const int at = d * 16 + (EIGHT ? g8 * 2 + k : g8 + k * 8);
+                                    float v;
+                                    if constexpr (EIGHT) v = from_e4m3x2((uint8_t)row[at]).x;
+                                    else v = to_f32(reinterpret_cast<const T *>(row)[at]);
+                                    if (isfinite(v)) continue;
+#pragma unroll
+                                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                                        for (int e = 0; e < 2; ++e)
+                                            if (j0 + j < seen[b][e])
+                                                o[d][b][k * 2 + e] = fmaf(w[b][e], v, o[d][b][k * 2 + e]);
                                 }
-                            }
                         }
             }
             if (++stage == ST) stage = 0;
         }
-        copies_wait<0>();
-        bad = __any_sync(0xffffffffu, bad);
+        total_sums(bad);
 
-        // ---- the groups' sums, joined
+        if (!together) {
+            // ---- the unit's rows, or the piece of them, eight at a time
+            const bool whole = piece.whole();
+            const int slot = piece.slot(range.group);
+            const float v_scale = EIGHT ? a.v_scale[u.head] : 1.f;
+            float *sums = reinterpret_cast<float *>(
+                MT > 1 ? smem + S::kRing + warp * S::kSums : ring + free_stage() * S::kTile);
+            join = join_from(range, range.group, n, piece, pos - piece.first);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int r0 = mt * S::kWarpRows + b * 8;
+                constexpr int Q8 = D / 8, EACH = 8 * Q8 / 32;
+                Vec<T, 8> gate[EACH];
+                if (whole && a.gate) {
+#pragma unroll
+                    for (int i = 0; i < EACH; ++i) {
+                        const int at = i * 32 + lane, r = r0 + at / Q8;
+                        if (r >= u.rows) continue;
+                        const RowPlace p = row_place(a, u, r);
+                        gate[i] = load8((const T *)a.gate + p.token * a.gs + p.head * a.gh + at % Q8 * 8,
+                                        a.gate_words);
+                    }
+                }
+                lay_out(sums, b, whole ? inverse(l[b][0]) * v_scale : v_scale,
+                        whole ? inverse(l[b][1]) * v_scale : v_scale);
+                if (g8 == 0) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = r0 + c4 * 2 + e;
+                        if (r >= u.rows) continue;
+                        if (whole) store_lse(a, row_place(a, u, r), m[b][e], l[b][e]);
+                        else a.stats[slot * S::kRows + r] = make_float2(m[b][e], l[b][e]);
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < EACH; ++i) {
+                    const int at = i * 32 + lane, r = r0 + at / Q8, e = at % Q8 * 8;
+                    if (r >= u.rows) continue;
+                    const float4 *x = reinterpret_cast<const float4 *>(sums + at / Q8 * S::kSumPitch + e);
+                    const float4 x0 = x[0], x1 = x[1];
+                    if (whole) {
+                        float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+                        if (a.gate) {
+                            float by[8];
+                            gate[i].to(by);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) y[k] *= sigmoid(by[k]);
+                        }
+                        const RowPlace p = row_place(a, u, r);
+                        store8((T *)a.out + p.token * a.os + p.head * a.oh + e, a.out_words, y);
+                    } else {
+                        float4 *to = reinterpret_cast<float4 *>(a.sums + ((int64_t)slot * S::kRows + r) * D + e);
+                        to[0] = x0;
+                        to[1] = x1;
+                    }
+                }
+                __syncwarp();
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) m[b][e] = kMinusInfinity, l[b][e] = 0.f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[d][b][e] = 0.f;
+            }
+        }
+        pos += piece.last - piece.first;
+        piece.first = 0;
+        if (++piece.unit == per_seq && pos < range.end) {
+            piece.unit = 0;
+            len = held_tokens(a, ++n);
+            piece.tiles = tiles_of<TK>(len);
+        }
+    }
+    copies_wait<0>();
+    if (!together) {
+        if (a.joins && mt == 0 && lane == 0) a.joins[range.group] = join;
+        return;
+    }
+
+    // ---- the groups' sums, joined
+    if constexpr (GR > 1) {
+        const Unit u = unit_of<S::kRows>(a, joined.y, joined.z, 0);
+        const bool whole = joined.w == 3;
+        const int group0 = blockIdx.x * GR, slot = 2 * group0 + (joined.w & 1);
+        float *sums = reinterpret_cast<float *>(smem);
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-            const int r = row0 + e * 8;
-            if (r >= u.rows) continue;
-            if (c4 == 0) ml[group][r] = make_float2(m[e], bad ? __int_as_float(0x7fffffff) : l[e]);
-            float *to = sums + (group * S::kRows + r) * S::kSumPitch;
+        for (int b = 0; b < NB; ++b) {
+            const int r0 = mt * S::kWarpRows + b * 8;
+            lay_out(sums + (group * S::kRows + r0) * S::kSumPitch, b, 1.f, 1.f);
+            if (g8 == 0)
 #pragma unroll
-            for (int n = 0; n < D / 8; n += 2) {
-                if constexpr (EIGHT) {
-                    *reinterpret_cast<float4 *>(to + n * 8 + c4 * 4) =
-                        make_float4(o[n][2 * e], o[n + 1][2 * e], o[n][2 * e + 1], o[n + 1][2 * e + 1]);
-                } else {
-                    *reinterpret_cast<float2 *>(to + n * 8 + c4 * 2) = make_float2(o[n][2 * e], o[n][2 * e + 1]);
-                    *reinterpret_cast<float2 *>(to + n * 8 + 8 + c4 * 2) =
-                        make_float2(o[n + 1][2 * e], o[n + 1][2 * e + 1]);
-                }
-            }
+                for (int e = 0; e < 2; ++e) ml[group][r0 + c4 * 2 + e] = make_float2(m[b][e], l[b][e]);
         }
         __syncthreads();
         // Each row's factors for the groups' sums, the values' scale among them.
@@ -532,88 +707,85 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
                 const float f = ex2(ml[w][r].x - against(top));
                 sum += ml[w][r].y * f;
                 ml[w][r].x = f * v_scale;
+                if (w > 0 && !whole) a.stats[2 * (group0 + w) * S::kRows + r] = make_float2(kMinusInfinity, 0.f);
             }
-            if (slot < 0) {
-                store_lse(a, row_place(a, u, r), top, sum);
-                inverses[r] = inverse(sum);
-            } else {
-                a.stats[slot * S::kRows + r] = make_float2(top, sum);
+            if (whole) store_lse(a, row_place(a, u, r), top, sum);
+            else a.stats[slot * S::kRows + r] = make_float2(top, sum);
+            inverses[r] = whole ? inverse(sum) : 1.f;
+        }
+        if (a.joins && threadIdx.x < GR) {
+            // The unit begins with the block's first tile: its other tiles are
+            // counted from there.
+            int4 mine = make_int4(-1, 0, 0, 0);
+            if (threadIdx.x == 0 && joined.w == 1) {
+                Piece p;
+                p.unit = joined.z, p.first = 0, p.last = 0, p.tiles = tiles_of<TK>(held_tokens(a, joined.y));
+                mine = join_from(range, group0, joined.y, p, range.begin);
             }
+            a.joins[group0 + threadIdx.x] = mine;
         }
         __syncthreads();
-        const int words = u.rows * (D / 8);
-        constexpr int BATCH = 4;
-#pragma unroll 1
-        for (int i0 = threadIdx.x; i0 < words; i0 += BATCH * S::kThreads) {
-            Vec<T, 8> gate[BATCH];
-            if (slot < 0 && a.gate) {
+        constexpr int Q8 = D / 8;
+        const int words = u.rows * Q8;
+#pragma unroll 2
+        for (int i = threadIdx.x; i < words; i += S::kThreads) {
+            const int r = i / Q8, e = i % Q8 * 8;
+            const RowPlace p = row_place(a, u, r);
+            Vec<T, 8> gate = Vec<T, 8>::zero();
+            if (whole && a.gate)
+                gate = load8((const T *)a.gate + p.token * a.gs + p.head * a.gh + e, a.gate_words);
+            float y[8];
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const int i = i0 + k * S::kThreads;
-                    if (i >= words) continue;
-                    const RowPlace p = row_place(a, u, i / (D / 8));
-                    gate[k] = load8((const T *)a.gate + p.token * a.gs + p.head * a.gh + i % (D / 8) * 8,
-                                    a.gate_words);
-                }
+            for (int k = 0; k < 8; ++k) y[k] = 0.f;
+#pragma unroll
+            for (int w = 0; w < GR; ++w) {
+                const float f = ml[w][r].x;
+                const float4 *x = reinterpret_cast<const float4 *>(sums + (w * S::kRows + r) * S::kSumPitch + e);
+                const float4 x0 = x[0], x1 = x[1];
+                y[0] = fmaf(f, x0.x, y[0]), y[1] = fmaf(f, x0.y, y[1]);
+                y[2] = fmaf(f, x0.z, y[2]), y[3] = fmaf(f, x0.w, y[3]);
+                y[4] = fmaf(f, x1.x, y[4]), y[5] = fmaf(f, x1.y, y[5]);
+                y[6] = fmaf(f, x1.z, y[6]), y[7] = fmaf(f, x1.w, y[7]);
             }
+            if (whole) {
+                float by[8];
+                gate.to(by);
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                const int i = i0 + k * S::kThreads, r = i / (D / 8), e = i % (D / 8) * 8;
-                if (i >= words) continue;
-                float y[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) y[q] = 0.f;
-#pragma unroll
-                for (int w = 0; w < GR; ++w) {
-                    const float f = ml[w][r].x;
-                    const float4 *x = reinterpret_cast<const float4 *>(sums + (w * S::kRows + r) * S::kSumPitch + e);
-                    const float4 x0 = x[0], x1 = x[1];
-                    y[0] = fmaf(f, x0.x, y[0]), y[1] = fmaf(f, x0.y, y[1]);
-                    y[2] = fmaf(f, x0.z, y[2]), y[3] = fmaf(f, x0.w, y[3]);
-                    y[4] = fmaf(f, x1.x, y[4]), y[5] = fmaf(f, x1.y, y[5]);
-                    y[6] = fmaf(f, x1.z, y[6]), y[7] = fmaf(f, x1.w, y[7]);
-                }
-                if (slot < 0) {
-                    const float inv = inverses[r];
-                    float by[8];
-                    if (a.gate) gate[k].to(by);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) y[q] *= a.gate ? inv * sigmoid(by[q]) : inv;
-                    const RowPlace p = row_place(a, u, r);
-                    store8((T *)a.out + p.token * a.os + p.head * a.oh + e, a.out_words, y);
-                } else {
-                    float4 *to = reinterpret_cast<float4 *>(a.sums + ((int64_t)slot * S::kRows + r) * D + e);
-                    to[0] = make_float4(y[0], y[1], y[2], y[3]);
-                    to[1] = make_float4(y[4], y[5], y[6], y[7]);
-                }
+                for (int k = 0; k < 8; ++k) y[k] *= a.gate ? inverses[r] * sigmoid(by[k]) : inverses[r];
+                store8((T *)a.out + p.token * a.os + p.head * a.oh + e, a.out_words, y);
+            } else {
+                float4 *to = reinterpret_cast<float4 *>(a.sums + ((int64_t)slot * S::kRows + r) * D + e);
+                to[0] = make_float4(y[0], y[1], y[2], y[3]);
+                to[1] = make_float4(y[4], y[5], y[6], y[7]);
             }
         }
-    });
+    }
 }
 
-template <bool EIGHT, int D, int MT, int GR>
+template <bool EIGHT, int D, int NB, int MT, int GR>
 gdn_status mma_run(int blocks, const AttentionArgs &a, cudaStream_t stream) {
-    using S = Tiles<EIGHT, D, MT, GR>;
+    using S = Tiles<EIGHT, D, NB, MT, GR>;
     static std::atomic<bool> done[kMaxDevices];
-    const auto kernel = gdn_attention_mma_kernel<EIGHT, D, MT, GR>;
+    const auto kernel = gdn_attention_mma_kernel<EIGHT, D, NB, MT, GR>;
     if (!raise_shared_memory(done, {reinterpret_cast<const void *>(kernel)}, {(size_t)S::kBytes}))
         return GDN_ERR_CUDA;
     kernel<<<blocks, S::kThreads, S::kBytes, stream>>>(a);
     return launch_status();
 }
 
-// Rows of a unit in whole tiles of 16, up to four of them at a time.
+// Up to 64 rows of a unit at a time: 8 or 16 by a warp, up to four warps.
 inline AttentionShape mma_shape(bool eight, int R, int D) {
     const int bytes = D * (eight ? 1 : 2), tokens = 8192 / bytes < 64 ? 8192 / bytes : 64;
-    return {R > 48 ? 64 : (R + 15) / 16 * 16, 4 * tokens, 2 * kGridSms};
+    return {R <= 8 ? 8 : R > 48 ? 64 : (R + 15) / 16 * 16, tokens, R <= 16 ? 4 : R <= 32 ? 2 : 1, 2 * kGridSms};
 }
 
 template <bool EIGHT, int D>
 gdn_status mma_rows(int blocks, const AttentionArgs &a, cudaStream_t stream) {
-    if (a.R <= 16) return mma_run<EIGHT, D, 1, 4>(blocks, a, stream);
-    if (a.R <= 32) return mma_run<EIGHT, D, 2, 2>(blocks, a, stream);
-    if (a.R <= 48) return mma_run<EIGHT, D, 3, 1>(blocks, a, stream);
-    return mma_run<EIGHT, D, 4, 1>(blocks, a, stream);
+    if (a.R <= 8) return mma_run<EIGHT, D, 1, 1, 4>(blocks, a, stream);
+    if (a.R <= 16) return mma_run<EIGHT, D, 2, 1, 4>(blocks, a, stream);
+    if (a.R <= 32) return mma_run<EIGHT, D, 2, 2, 2>(blocks, a, stream);
+    if (a.R <= 48) return mma_run<EIGHT, D, 2, 3, 1>(blocks, a, stream);
+    return mma_run<EIGHT, D, 2, 4, 1>(blocks, a, stream);
 }
 
 template <bool EIGHT> gdn_status mma_attention(int D, int blocks, const AttentionArgs &a, cudaStream_t stream) {

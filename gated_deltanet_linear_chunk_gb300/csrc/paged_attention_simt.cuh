@@ -27,8 +27,11 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int tok = lane / 4, s = lane % 4;
     float *pw = ps + warp * RR * kSimtTokens;
-    const Range range = find_range<kSimtChunk, kSimtWarps * 32>(a, a.Hkv * a.row_blocks);
-    for_pieces<kSimtChunk, RR>(a, range, [&](const Unit &u, int t0, int t1, int slot) {
+    ptx::griddep_launch_dependents();
+    const Range range = find_range<kSimtChunk, kSimtWarps * 32, 1>(a, a.Hkv * a.row_blocks, 0);
+    const int4 join = for_pieces<kSimtChunk, RR>(a, range, [&](const Unit &u, const Piece &piece) {
+        const int t0 = piece.first_token<kSimtChunk>(u.len), t1 = piece.last_token<kSimtChunk>(u.len);
+        const int slot = piece.whole() ? -1 : piece.slot(range.group);
         __syncthreads();  // the last piece's rows
         for (int i = threadIdx.x; i < RR * D; i += kSimtWarps * 32) {
             const int r = i / D;
@@ -151,11 +154,12 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
             }
         }
     });
+    if (a.joins && threadIdx.x == 0) a.joins[range.group] = join;
 }
 
 // Rows at a time: those of a unit, up to 16.
 inline AttentionShape simt_shape(int R) {
-    return {R <= 4 ? 4 : R <= 8 ? 8 : 16, kSimtChunk, kAttentionBlocks};
+    return {R <= 4 ? 4 : R <= 8 ? 8 : 16, kSimtChunk, 1, 2 * kGridSms};
 }
 
 template <typename T, typename TC, int D, int RR>
