@@ -6,6 +6,8 @@ namespace gdn {
 namespace {
 
 constexpr int kJoinThreads = 256, kJoinBlocks = 8 * kGridSms, kJoinAlone = 12;
+// Pieces that a thread looks over, at most.
+constexpr int kJoinEach = (kAttentionGroups + kJoinThreads) / kJoinThreads;
 
 // The join of a unit: four elements of the sums of piece i, times f.
 template <int D>
@@ -41,6 +43,7 @@ gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows, int
     constexpr int WORDS = D / 4, TEAMS = kJoinThreads / WORDS, WARPS = kJoinThreads / 32;
     constexpr float kNone = -__builtin_huge_valf();
     __shared__ float weight[kAttentionGroups + 1];
+    __shared__ int slots[kAttentionGroups + 1], counts[kJoinEach * (kJoinThreads / 32)];
     __shared__ float tops[WARPS], totals[WARPS];
     __shared__ float4 parts[kJoinThreads];
     __shared__ int4 unit_join;
@@ -53,10 +56,15 @@ gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows, int
         if (threadIdx.x == 0) at = -1;
         ptx::griddep_wait();
         __syncthreads();
-        for (int i = threadIdx.x; i < groups; i += kJoinThreads) {
-            const int4 j = a.joins[i];
-            if (j.x == n && j.y == unit) at = i, unit_join = j;
+        int4 j[kJoinEach];
+#pragma unroll
+        for (int k = 0; k < kJoinEach; ++k) {
+            const int i = k * kJoinThreads + threadIdx.x;
+            j[k] = i < groups ? a.joins[i] : make_int4(-1, 0, 0, 0);
         }
+#pragma unroll
+        for (int k = 0; k < kJoinEach; ++k)
+            if (j[k].x == n && j[k].y == unit) at = k * kJoinThreads + threadIdx.x, unit_join = j[k];
         __syncthreads();
         group = at;
         if (group < 0) return;
@@ -106,21 +114,45 @@ gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows, int
 
     const int team = threadIdx.x / WORDS, word = threadIdx.x % WORDS;
     for (int r = blockIdx.y; r < u.rows; r += gridDim.y) {
+        float2 s[kJoinEach];
         float top = kNone;
-        for (int i = threadIdx.x; i < pieces; i += kJoinThreads)
-            top = fmaxf(top, a.stats[slot(i) * rows + r].x);
+#pragma unroll
+        for (int k = 0; k < kJoinEach; ++k) {
+            const int i = k * kJoinThreads + threadIdx.x;
+            s[k] = i < pieces ? a.stats[slot(i) * rows + r] : make_float2(kNone, 0.f);
+            top = fmaxf(top, s[k].x);
+        }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         if (lane == 0) tops[warp] = top;
+        // The pieces that have sums, in their order.
+#pragma unroll
+        for (int k = 0; k < kJoinEach; ++k) {
+            const unsigned have = __ballot_sync(0xffffffffu, s[k].x != kNone || s[k].y != 0.f);
+            if (lane == 0) counts[k * WARPS + warp] = __popc(have);
+        }
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < WARPS; ++w) top = fmaxf(top, tops[w]);
         float total = 0.f;
-        for (int i = threadIdx.x; i < pieces; i += kJoinThreads) {
-            const float2 s = a.stats[slot(i) * rows + r];
-            const float f = ex2(s.x - against(top));
-            weight[i] = s.x == kNone && s.y == 0.f ? -1.f : f;  // -1: a piece without sums
-            total += s.y * f;
+        int some = 0;
+#pragma unroll
+        for (int k = 0; k < kJoinEach; ++k) {
+            const float f = ex2(s[k].x - against(top));
+            total += s[k].y * f;
+            const bool has = s[k].x != kNone || s[k].y != 0.f;
+            const unsigned have = __ballot_sync(0xffffffffu, has);
+            int before = some;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
+                if (w < warp) before += counts[k * WARPS + w];
+                some += counts[k * WARPS + w];
+            }
+            if (has) {
+                const int to = before + __popc(have & ((1u << lane) - 1));
+                weight[to] = f;
+                slots[to] = slot(k * kJoinThreads + threadIdx.x);
+            }
         }
         total = warp_sum(total);
         if (lane == 0) totals[warp] = total;
@@ -130,10 +162,7 @@ gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows, int
         for (int w = 0; w < WARPS; ++w) total += totals[w];
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int i = team; i < pieces; i += TEAMS) {
-            const float f = weight[i];
-            if (f != -1.f) add_piece<D>(a, y, slot(i), rows, r, word, f);
-        }
+        for (int i = team; i < some; i += TEAMS) add_piece<D>(a, y, slots[i], rows, r, word, weight[i]);
         parts[threadIdx.x] = y;
         __syncthreads();
         const RowPlace p = row_place(a, u, r);
@@ -152,7 +181,6 @@ gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows, int
 struct Plan {
     int rows, blocks, groups;
     int64_t units;
-    bool split;
     size_t joins, stats, sums;  // bytes
 };
 
@@ -164,14 +192,14 @@ Plan plan(const gdn_attention_problem &p, const gdn_paged_cache &c) {
                                                    : shape_bf16(R, p.head_dim);
     pl.rows = s.rows;
     pl.units = (int64_t)c.num_seqs * p.kv_heads * ((R + s.rows - 1) / s.rows);
-    const int64_t tiles = 1 + ((int64_t)c.max_pages * c.page_size + s.tokens - 1) / s.tokens;
+    const int64_t tiles = s.setup + ((int64_t)c.max_pages * c.page_size + s.tokens - 1) / s.tokens;
     const int64_t need = (pl.units * tiles + s.groups - 1) / s.groups;  // blocks, at most
     pl.blocks = (int)(need < s.blocks ? need : s.blocks);
     pl.groups = pl.blocks * s.groups;
-    pl.split = c.max_pages > 0;  // a sequence without room is its tile without tokens
-    pl.joins = pl.split ? ((size_t)pl.groups * sizeof(int4)) : 0;
-    pl.stats = pl.split ? (size_t)pl.groups * 2 * s.rows * sizeof(float2) : 0;
-    pl.sums = pl.split ? (size_t)pl.groups * 2 * s.rows * p.head_dim * sizeof(float) : 0;
+    // Any unit can be cut, also one without tokens.
+    pl.joins = (size_t)pl.groups * sizeof(int4);
+    pl.stats = (size_t)pl.groups * 2 * s.rows * sizeof(float2);
+    pl.sums = (size_t)pl.groups * 2 * s.rows * p.head_dim * sizeof(float);
     return pl;
 }
 
@@ -214,14 +242,17 @@ gdn_status launch_paged_attention(const gdn_attention_problem &p, const gdn_page
     a.qs = p.q_stride, a.qh = p.q_head_stride;
     a.gs = p.gate_stride, a.gh = p.gate_head_stride;
     a.os = p.out_stride, a.oh = p.out_head_stride;
-    a.kps = c.k_page_stride, a.kts = c.k_token_stride, a.khs = c.k_head_stride;
-    a.vps = c.v_page_stride, a.vts = c.v_token_stride, a.vhs = c.v_head_stride;
+    const int64_t e = c.dtype == GDN_F32 ? 4 : c.dtype == GDN_E4M3 ? 1 : 2;
+    a.kps = c.k_page_stride * e, a.kts = c.k_token_stride * e, a.khs = c.k_head_stride * e;
+    a.vps = c.v_page_stride * e, a.vts = c.v_token_stride * e, a.vhs = c.v_head_stride * e;
     a.table_stride = c.table_stride, a.num_pages = c.num_pages;
     a.N = c.num_seqs, a.L = p.new_tokens, a.Hkv = p.kv_heads;
     a.G = p.q_heads / p.kv_heads;
     a.R = a.L * a.G;
     a.row_blocks = (a.R + pl.rows - 1) / pl.rows;
+    a.inv_group = 1.f / (float)a.G;
     a.page_size = c.page_size;
+    a.by_page = Division::by(c.page_size);
     a.capacity = c.max_pages * c.page_size;
     a.scale_log2 = p.scale * kLog2e;
     auto words = [&](const void *x, int64_t stride, int64_t head_stride) {
@@ -231,17 +262,15 @@ gdn_status launch_paged_attention(const gdn_attention_problem &p, const gdn_page
     a.q_words = words(q, p.q_stride, p.q_head_stride);
     a.gate_words = words(gate, p.gate_stride, p.gate_head_stride);
     a.out_words = words(out, p.out_stride, p.out_head_stride);
-    if (pl.split) {
-        // The sums first: they are read in 16-byte words.
-        char *w = static_cast<char *>(p.workspace);
-        a.sums = reinterpret_cast<float *>(w);
-        a.joins = reinterpret_cast<int4 *>(w + pl.sums);
-        a.stats = reinterpret_cast<float2 *>(w + pl.sums + pl.joins);
-    }
+    // Multiples of 16 bytes first: they are read in such words.
+    char *w = static_cast<char *>(p.workspace);
+    a.sums = reinterpret_cast<float *>(w);
+    a.joins = reinterpret_cast<int4 *>(w + pl.sums);
+    a.stats = reinterpret_cast<float2 *>(w + pl.sums + pl.joins);
     const gdn_status st = p.dtype == GDN_F32      ? attention_f32(p.head_dim, pl.blocks, a, stream)
                           : c.dtype == GDN_E4M3 ? attention_e4m3(p.head_dim, pl.blocks, a, stream)
                                                 : attention_bf16(p.head_dim, pl.blocks, a, stream);
-    if (st != GDN_OK || !pl.split) return st;
+    if (st != GDN_OK) return st;
     const bool f32 = p.dtype == GDN_F32;
     switch (p.head_dim) {
         case 64: return f32 ? join<float, 64>(a, pl, stream) : join<__nv_bfloat16, 64>(a, pl, stream);

@@ -7,9 +7,9 @@
 // read once, which bounds the operator, and every SM has to read its share of
 // it, whatever the lengths are: the tiles (of a fixed number of tokens) of all
 // units, one unit after the other, are divided evenly among groups of warps,
-// which find their place from the lengths on the device.  A unit counts one
-// tile more than it has: what its queries and results cost; that tile has no
-// tokens.  A group's range begins and ends inside units: what it has of those
+// which find their place from the lengths on the device.  A unit counts a few
+// tiles more than it has, for what its queries and results cost: its first
+// tiles have no tokens.  A group's range begins and ends inside units: what it has of those
 // goes to the workspace, one piece for the range's begin and one for its end,
 // and a second launch joins the pieces in their order.
 #pragma once
@@ -21,6 +21,24 @@ namespace gdn {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
+// x / d for 0 <= x < 2^30 and d up to 2^20, as one product: with s = ceil(log2 d)
+// the factor 2^(30 + s) / d, rounded up, is off by less than one in d <= 2^s, so
+// the quotient of x by less than x / 2^30 of a step.
+struct Division {
+    uint32_t factor;
+    int shift;
+    static Division by(int d) {
+        int s = 0;
+        while ((1 << s) < d) ++s;
+        const uint64_t two = 1ull << (30 + s);
+        return {(uint32_t)((two + d - 1) / d), 30 + s};
+    }
+    __host__ __device__ __forceinline__ int of(int x) const {
+        return (int)((uint64_t)(uint32_t)x * factor >> shift);
+    }
+};
+
+// Strides of q, gate and out are in elements, of the cache in bytes.
 struct AttentionArgs {
     const void *q, *gate;
     void *out;
@@ -32,6 +50,8 @@ struct AttentionArgs {
     int64_t kps, kts, khs, vps, vts, vhs, table_stride;
     int64_t num_pages;
     int N, L, Hkv, G, R, row_blocks, page_size, capacity;
+    float inv_group;         // 1 / G
+    Division by_page;        // tokens by page_size
     bool q_words, gate_words, out_words;  // rows of q, gate and out in whole 16-byte words
     float scale_log2;  // scale log2 e: scores in powers of two
     // workspace
@@ -48,9 +68,9 @@ struct Unit {
 __device__ __forceinline__ int held_tokens(const AttentionArgs &a, int n) {
     return min(max(a.lens[n], 0), a.capacity);
 }
-// One without tokens comes first.
-template <int TOKENS> __device__ __forceinline__ int tiles_of(int len) {
-    return 1 + (len + TOKENS - 1) / TOKENS;
+// SETUP of them, at least one, are without tokens and come first.
+template <int TOKENS, int SETUP> __device__ __forceinline__ int tiles_of(int len) {
+    return SETUP + (len + TOKENS - 1) / TOKENS;
 }
 
 // A group's range of tiles, and that of its block's groups together.  (No more
@@ -73,14 +93,14 @@ __host__ __device__ __forceinline__ int group_of(int64_t total, int groups, int6
 
 // By all threads of a block: sums over the sequences, a run of them per thread.
 // `mine`: the thread's group in the block, of GROUPS.
-template <int TOKENS, int THREADS, int GROUPS>
+template <int TOKENS, int SETUP, int THREADS, int GROUPS>
 __device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
     __shared__ int64_t warp_sums[THREADS / 32], found_base[GROUPS];
     __shared__ int found[GROUPS];
     const int run = (a.N + THREADS - 1) / THREADS;
     const int n0 = min((int)threadIdx.x * run, a.N), n1 = min(n0 + run, a.N);
     int64_t count = 0;
-    for (int n = n0; n < n1; ++n) count += tiles_of<TOKENS>(held_tokens(a, n));
+    for (int n = n0; n < n1; ++n) count += tiles_of<TOKENS, SETUP>(held_tokens(a, n));
     int64_t upto = count;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
 #pragma unroll
@@ -107,7 +127,7 @@ __device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
         if (begin < base || begin >= upto * per_seq) continue;
         int64_t at = base;
         for (int n = n0; n < n1; ++n) {
-            const int64_t next = at + (int64_t)tiles_of<TOKENS>(held_tokens(a, n)) * per_seq;
+            const int64_t next = at + (int64_t)tiles_of<TOKENS, SETUP>(held_tokens(a, n)) * per_seq;
             if (begin < next) {
                 found[g] = n;
                 found_base[g] = at;
@@ -126,18 +146,24 @@ __device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
     return r;
 }
 
+// The new token of a row, row / G: the quotient is at most 8 (and a block's
+// rows beyond), so its rounding, some 2^-20, is far from the half step of at
+// least 2^-13 that the sum begins with.
+__device__ __forceinline__ int row_token(const AttentionArgs &a, int row) {
+    return (int)(((float)row + 0.5f) * a.inv_group);
+}
 // Where row r of a unit lies in q, gate, out (times its strides) and lse.
 struct RowPlace {
     int64_t token;
     int head;
 };
 __device__ __forceinline__ RowPlace row_place(const AttentionArgs &a, const Unit &u, int r) {
-    const int row = u.first_row + r;
-    return {(int64_t)u.n * a.L + row / a.G, u.head * a.G + row % a.G};
+    const int row = u.first_row + r, t = row_token(a, row);
+    return {(int64_t)u.n * a.L + t, u.head * a.G + row - t * a.G};
 }
 // How many of the unit's tokens row r sees.
 __device__ __forceinline__ int seen_by(const AttentionArgs &a, const Unit &u, int r) {
-    return u.len - a.L + 1 + (u.first_row + r) / a.G;
+    return u.len - a.L + 1 + row_token(a, u.first_row + r);
 }
 
 // What a group has of a unit: tiles [first, last) of `tiles`.
@@ -146,11 +172,11 @@ struct Piece {
     __device__ __forceinline__ bool whole() const { return first == 0 && last == tiles; }
     // The workspace's slot: the begin of a unit ends its group's range.
     __device__ __forceinline__ int slot(int group) const { return 2 * group + (first == 0 ? 1 : 0); }
-    template <int TOKENS> __device__ __forceinline__ int first_token(int len) const {
-        return min(max(first - 1, 0) * TOKENS, len);
+    template <int TOKENS, int SETUP> __device__ __forceinline__ int first_token(int len) const {
+        return min(max(first - SETUP, 0) * TOKENS, len);
     }
-    template <int TOKENS> __device__ __forceinline__ int last_token(int len) const {
-        return min((last - 1) * TOKENS, len);
+    template <int TOKENS, int SETUP> __device__ __forceinline__ int last_token(int len) const {
+        return min(max(last - SETUP, 0) * TOKENS, len);
     }
 };
 template <int ROWS>
@@ -170,14 +196,14 @@ __device__ __forceinline__ int4 join_from(const Range &g, int group, int n, cons
 }
 
 // Runs `work(unit, piece)` over a group's range; its last join.
-template <int TOKENS, int ROWS, typename F>
+template <int TOKENS, int SETUP, int ROWS, typename F>
 __device__ __forceinline__ int4 for_pieces(const AttentionArgs &a, const Range &g, F &&work) {
     const int per_seq = a.Hkv * a.row_blocks;
     int4 join = make_int4(-1, 0, 0, 0);
     if (g.begin >= g.end) return join;
     int n = g.n, len = held_tokens(a, n);
     Piece p;
-    p.tiles = tiles_of<TOKENS>(len);
+    p.tiles = tiles_of<TOKENS, SETUP>(len);
     p.unit = (int)((g.begin - g.base) / p.tiles);
     p.first = (int)((g.begin - g.base) % p.tiles);
     for (int64_t pos = g.begin; pos < g.end;) {
@@ -189,7 +215,7 @@ __device__ __forceinline__ int4 for_pieces(const AttentionArgs &a, const Range &
         if (++p.unit == per_seq && pos < g.end) {
             p.unit = 0;
             len = held_tokens(a, ++n);
-            p.tiles = tiles_of<TOKENS>(len);
+            p.tiles = tiles_of<TOKENS, SETUP>(len);
         }
     }
     return join;
@@ -244,9 +270,9 @@ template <int E> __device__ __forceinline__ void load_cached(const __nv_fp8_e4m3
 }
 
 // What a kernel takes at a time, for units of R rows: rows, the tokens of a
-// tile, its groups per block and its blocks on a GB300.
+// tile, a unit's tiles without any, groups per block and its blocks on a GB300.
 struct AttentionShape {
-    int rows, tokens, groups, blocks;
+    int rows, tokens, setup, groups, blocks;
 };
 constexpr int kAttentionGroups = 8 * kGridSms;  // at most
 AttentionShape shape_f32(int R, int D);

@@ -89,6 +89,9 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, bool words, const float
     }
 }
 
+// What a unit costs beside its tokens, in tiles.
+__host__ __device__ constexpr int setup_tiles(int nb, int mt) { return mt > 1 ? 6 : nb > 1 ? 3 : 2; }
+
 // What a variant keeps in shared memory.  EIGHT: an 8-bit cache; NB blocks of 8
 // rows per warp, MT warps that share a ring, GR such groups.
 template <bool EIGHT, int D, int NB, int MT, int GR> struct Tiles {
@@ -96,6 +99,7 @@ template <bool EIGHT, int D, int NB, int MT, int GR> struct Tiles {
     static constexpr int kPitch = kRowBytes + 16;  // rows of a matrix on different banks
     static constexpr int kTokens = 8192 / kRowBytes < 64 ? 8192 / kRowBytes : 64;
     static constexpr int kTile = kTokens * kPitch;
+    static constexpr int kSetup = setup_tiles(NB, MT);
     static constexpr int kThreads = MT * GR * 32, kWarpRows = NB * 8, kRows = MT * kWarpRows;
     // Eight rows' sums, on their way out: in a stage that is free, or where
     // warps share a ring in a place of each warp's own.
@@ -117,7 +121,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     using S = Tiles<EIGHT, D, NB, MT, GR>;
     using T = __nv_bfloat16;
     constexpr int TK = S::kTokens, TT = TK / 16, ST = S::kStages, AHEAD = (ST - 1) / 2;
-    constexpr int ES = EIGHT ? 1 : 2, DT = D / 16;
+    constexpr int ES = EIGHT ? 1 : 2, DT = D / 16, SETUP = S::kSetup;
     constexpr int WORDS = S::kRowBytes / 16;  // of a token's row
     constexpr int PER = MT * 32 / WORDS;      // rows that a group copies at once
     constexpr int HOLD = (TK + 31) / 32;      // rows whose place a lane knows
@@ -142,7 +146,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
 
     ptx::griddep_launch_dependents();
     const int per_seq = a.Hkv * a.row_blocks;
-    const Range range = find_range<TK, S::kThreads, GR>(a, per_seq, group);
+    const Range range = find_range<TK, SETUP, S::kThreads, GR>(a, per_seq, group);
 
     // ---- the copies, ahead of the products.  The cursor is at the tile whose
     // entries of the page table are on their way.
@@ -153,7 +157,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     c.left = range.end - range.begin;
     c.n = range.n;
     c.len = c.left > 0 ? held_tokens(a, c.n) : 0;
-    c.tiles = tiles_of<TK>(c.len);
+    c.tiles = tiles_of<TK, SETUP>(c.len);
     c.unit = (int)((range.begin - range.base) / c.tiles);
     c.tile = (int)((range.begin - range.base) % c.tiles);
     // Where a whole block lies inside one unit its groups' sums are joined
@@ -167,44 +171,51 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     piece.unit = c.unit, piece.first = c.tile, piece.tiles = c.tiles;
     int n = c.n, len = c.len;
 
+    // Sixteen tokens that follow one another share a page where the size allows
+    // it: then a lane knows the places of a whole segment, else of one token.
+    const bool segments = a.page_size % 16 == 0;
+    const int step = segments ? 16 : 1;
     int entry[HOLD];
+    auto token_of = [&](int h) { return (c.tile - SETUP) * TK + (h * 32 + lane) * step; };
     auto look_up = [&] {
-        while (c.left > 0 && (c.tile == 0 || c.tile == c.tiles)) {  // no tokens
+        while (c.left > 0 && (c.tile < SETUP || c.tile == c.tiles)) {  // no tokens
             if (c.tile == c.tiles) {
                 c.tile = 0;
                 if (++c.unit == per_seq) {
                     c.unit = 0;
                     c.len = held_tokens(a, ++c.n);
-                    c.tiles = tiles_of<TK>(c.len);
+                    c.tiles = tiles_of<TK, SETUP>(c.len);
                 }
             }
             ++c.tile, --c.left;
         }
 #pragma unroll
         for (int h = 0; h < HOLD; ++h) {
-            const int j = (c.tile - 1) * TK + h * 32 + lane;
+            const int j = token_of(h);
             entry[h] = -1;
-            if (c.left > 0 && h * 32 + lane < TK && j < c.len)
-                entry[h] = a.table[c.n * a.table_stride + j / a.page_size];
+            if (c.left > 0 && (h * 32 + lane) * step < TK && j < c.len)
+                entry[h] = a.table[c.n * a.table_stride + a.by_page.of(j)];
         }
     };
     int64_t k_at[HOLD], v_at[HOLD];  // bytes from the cache's start; -1: none
+    int held = 0;                    // of the tile's tokens
     uint32_t bad_tiles = 0;          // bit i: of the i-th tile ahead, a page out of range
     auto place = [&](int ahead) {
-        const int head = c.unit / a.row_blocks;
+        const int head = a.row_blocks == 1 ? c.unit : c.unit / a.row_blocks;
         bool bad = false;
+        held = c.left > 0 ? c.len - (c.tile - SETUP) * TK : 0;
 #pragma unroll
         for (int h = 0; h < HOLD; ++h) {
-            const int j = (c.tile - 1) * TK + h * 32 + lane, p = entry[h];
+            const int j = token_of(h), p = entry[h];
             k_at[h] = v_at[h] = -1;
-            if (!(c.left > 0 && h * 32 + lane < TK && j < c.len)) continue;
+            if (!((h * 32 + lane) * step < TK && (h * 32 + lane) * step < held)) continue;
             if (p < 0 || p >= a.num_pages) {
                 bad = true;
                 continue;
             }
-            const int at = j % a.page_size;
-            k_at[h] = (p * a.kps + at * a.kts + head * a.khs) * ES;
-            v_at[h] = (p * a.vps + at * a.vts + head * a.vhs) * ES;
+            const int at = j - a.by_page.of(j) * a.page_size;
+            k_at[h] = (uint32_t)p * a.kps + (uint32_t)at * a.kts + (uint32_t)head * a.khs;
+            v_at[h] = (uint32_t)p * a.vps + (uint32_t)at * a.vts + (uint32_t)head * a.vhs;
         }
         if (__any_sync(0xffffffffu, bad)) bad_tiles |= 1u << ahead;
         if (c.left > 0) {
@@ -213,21 +224,36 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
         }
     };
     // Copies a half stage: rows that do not exist become zeros.
-    auto copy = [&](int stage, const void *from, const int64_t (&at)[HOLD]) {
-        const int sub = mt * 32 + lane, word = sub % WORDS;
-        char *to = ring + stage * S::kTile + word * 16;
+    auto copy = [&](int stage, const void *from, int64_t token_stride, const int64_t (&at)[HOLD]) {
+        const int sub = mt * 32 + lane, word = sub % WORDS, r_lane = sub / WORDS;
+        char *to = ring + stage * S::kTile + r_lane * S::kPitch + word * 16;
+        const char *base = static_cast<const char *>(from) + word * 16;
+        if (segments) {
+            int64_t off = 0;
+            const char *x = base;
 #pragma unroll
-        for (int r0 = 0; r0 < TK; r0 += PER) {
-            const int r = r0 + sub / WORDS;
-            int64_t off = __shfl_sync(0xffffffffu, at[0], r & 31);
-            if (HOLD > 1) {
-                const int64_t upper = __shfl_sync(0xffffffffu, at[HOLD - 1], r & 31);
-                off = r & 32 ? upper : off;
+            for (int r0 = 0; r0 < TK; r0 += PER) {
+                const int r = r0 + r_lane;
+                if (16 % PER != 0 || r0 % 16 == 0) {
+                    off = __shfl_sync(0xffffffffu, at[0], r >> 4 & 31);
+                    x = base + (off < 0 ? 0 : off) + (r & 15) * token_stride;
+                }
+                if (TK % PER == 0 || r < TK)
+                    copy_async_head(to + r0 * S::kPitch, x, off >= 0 && r < held ? 16 : 0);
+                x += PER * token_stride;
             }
-            if (TK % PER == 0 || r < TK)
-                copy_async_head(to + r * S::kPitch,
-                                static_cast<const char *>(from) + (off < 0 ? 0 : off + word * 16),
-                                off < 0 ? 0 : 16);
+        } else {
+#pragma unroll
+            for (int r0 = 0; r0 < TK; r0 += PER) {
+                const int r = r0 + r_lane;
+                int64_t off = __shfl_sync(0xffffffffu, at[0], r & 31);
+                if (HOLD > 1) {
+                    const int64_t upper = __shfl_sync(0xffffffffu, at[HOLD - 1], r & 31);
+                    off = r & 32 ? upper : off;
+                }
+                if (TK % PER == 0 || r < TK)
+                    copy_async_head(to + r0 * S::kPitch, base + (off < 0 ? 0 : off), off < 0 ? 0 : 16);
+            }
         }
         copies_commit();
     };
@@ -237,8 +263,8 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
 #pragma unroll 1
     for (int i = 0; i < AHEAD; ++i) {
         place(i);
-        copy(2 * i, a.k, k_at);
-        copy(2 * i + 1, a.v, v_at);
+        copy(2 * i, a.k, a.kts, k_at);
+        copy(2 * i + 1, a.v, a.vts, v_at);
     }
     __syncthreads();
     const bool together = joined.x != 0;
@@ -292,7 +318,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     for (int64_t pos = range.begin; pos < range.end;) {
         piece.last = (int)min((int64_t)piece.tiles, piece.first + (range.end - pos));
         const Unit u = unit_of<S::kRows>(a, n, piece.unit, len);
-        const int t0 = piece.template first_token<TK>(len), t1 = piece.template last_token<TK>(len);
+        const int t0 = piece.template first_token<TK, SETUP>(len), t1 = piece.template last_token<TK, SETUP>(len);
 
         // Queries, times the sign of the scale: rows 8 b + g8, elements 16 k + 2 c4
         // and + 8 (two each).  For an 8-bit cache elements 16 k + 4 c4 (four), in
@@ -371,7 +397,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             place(AHEAD);
             bad |= bad_tiles & 1;
             bad_tiles >>= 1;
-            copy(free_stage(), a.k, k_at);
+            copy(free_stage(), a.k, a.kts, k_at);
             // Short chains of products: where they are few, even and odd steps
             // have sums of their own.
             constexpr int CHAINS = TT * NB < 4 ? 2 : 1;
@@ -483,7 +509,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             // ---- values
             copies_wait<ST - 2>();
             group_sync();
-            copy(free_stage(), a.v, v_at);
+            copy(free_stage(), a.v, a.vts, v_at);
             const char *tile = ring + stage * S::kTile;
             const uint32_t values = ring_at + stage * S::kTile + v_lane;
             // The newest tokens' values may be infinite or NaN where some rows
@@ -670,12 +696,12 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
         if (++piece.unit == per_seq && pos < range.end) {
             piece.unit = 0;
             len = held_tokens(a, ++n);
-            piece.tiles = tiles_of<TK>(len);
+            piece.tiles = tiles_of<TK, SETUP>(len);
         }
     }
     copies_wait<0>();
     if (!together) {
-        if (a.joins && mt == 0 && lane == 0) a.joins[range.group] = join;
+        if (mt == 0 && lane == 0) a.joins[range.group] = join;
         return;
     }
 
@@ -713,13 +739,13 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             else a.stats[slot * S::kRows + r] = make_float2(top, sum);
             inverses[r] = whole ? inverse(sum) : 1.f;
         }
-        if (a.joins && threadIdx.x < GR) {
+        if (threadIdx.x < GR) {
             // The unit begins with the block's first tile: its other tiles are
             // counted from there.
             int4 mine = make_int4(-1, 0, 0, 0);
             if (threadIdx.x == 0 && joined.w == 1) {
                 Piece p;
-                p.unit = joined.z, p.first = 0, p.last = 0, p.tiles = tiles_of<TK>(held_tokens(a, joined.y));
+                p.unit = joined.z, p.first = 0, p.last = 0, p.tiles = tiles_of<TK, SETUP>(held_tokens(a, joined.y));
                 mine = join_from(range, group0, joined.y, p, range.begin);
             }
             a.joins[group0 + threadIdx.x] = mine;
@@ -776,7 +802,8 @@ gdn_status mma_run(int blocks, const AttentionArgs &a, cudaStream_t stream) {
 // Up to 64 rows of a unit at a time: 8 or 16 by a warp, up to four warps.
 inline AttentionShape mma_shape(bool eight, int R, int D) {
     const int bytes = D * (eight ? 1 : 2), tokens = 8192 / bytes < 64 ? 8192 / bytes : 64;
-    return {R <= 8 ? 8 : R > 48 ? 64 : (R + 15) / 16 * 16, tokens, R <= 16 ? 4 : R <= 32 ? 2 : 1, 2 * kGridSms};
+    return {R <= 8 ? 8 : R > 48 ? 64 : (R + 15) / 16 * 16, tokens,
+            setup_tiles(R <= 8 ? 1 : 2, R <= 16 ? 1 : 2), R <= 16 ? 4 : R <= 32 ? 2 : 1, 2 * kGridSms};
 }
 
 template <bool EIGHT, int D>

@@ -28,9 +28,9 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
     const int tok = lane / 4, s = lane % 4;
     float *pw = ps + warp * RR * kSimtTokens;
     ptx::griddep_launch_dependents();
-    const Range range = find_range<kSimtChunk, kSimtWarps * 32, 1>(a, a.Hkv * a.row_blocks, 0);
-    const int4 join = for_pieces<kSimtChunk, RR>(a, range, [&](const Unit &u, const Piece &piece) {
-        const int t0 = piece.first_token<kSimtChunk>(u.len), t1 = piece.last_token<kSimtChunk>(u.len);
+    const Range range = find_range<kSimtChunk, 1, kSimtWarps * 32, 1>(a, a.Hkv * a.row_blocks, 0);
+    const int4 join = for_pieces<kSimtChunk, 1, RR>(a, range, [&](const Unit &u, const Piece &piece) {
+        const int t0 = piece.first_token<kSimtChunk, 1>(u.len), t1 = piece.last_token<kSimtChunk, 1>(u.len);
         const int slot = piece.whole() ? -1 : piece.slot(range.group);
         __syncthreads();  // the last piece's rows
         for (int i = threadIdx.x; i < RR * D; i += kSimtWarps * 32) {
@@ -62,7 +62,7 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
                 if (page < 0 || page >= a.num_pages) page = -1, bad = true;
             }
             const int place = j % a.page_size;
-            const TC *k = (const TC *)a.k + page * a.kps + place * a.kts + u.head * a.khs;
+            const TC *k = (const TC *)((const char *)a.k + page * a.kps + place * a.kts + u.head * a.khs);
             const int64_t v_at = page * a.vps + place * a.vts + u.head * a.vhs;
             float acc[RR];
 #pragma unroll
@@ -106,7 +106,7 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
                 const int64_t at = __shfl_sync(0xffffffffu, v_at, t * 4);
                 if (__shfl_sync(0xffffffffu, (int)(page < 0), t * 4)) continue;
                 float x[E];
-                load_cached((const TC *)a.v + at + lane * E, x);
+                load_cached((const TC *)((const char *)a.v + at) + lane * E, x);
 #pragma unroll
                 for (int r = 0; r < RR; ++r) {
                     if (j0 + t >= lims[r]) continue;
@@ -154,12 +154,12 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
             }
         }
     });
-    if (a.joins && threadIdx.x == 0) a.joins[range.group] = join;
+    if (threadIdx.x == 0) a.joins[range.group] = join;
 }
 
 // Rows at a time: those of a unit, up to 16.
 inline AttentionShape simt_shape(int R) {
-    return {R <= 4 ? 4 : R <= 8 ? 8 : 16, kSimtChunk, 1, 2 * kGridSms};
+    return {R <= 4 ? 4 : R <= 8 ? 8 : 16, kSimtChunk, 1, 1, 2 * kGridSms};
 }
 
 template <typename T, typename TC, int D, int RR>
