@@ -133,9 +133,12 @@ gdn_status check_cache(const gdn_paged_cache &c, int32_t dtype, int heads, int D
     return GDN_OK;
 }
 
-gdn_status check_attention(const gdn_attention_problem &p) {
+gdn_status check_attention(const gdn_attention_problem &p, const gdn_paged_cache &c) {
     if (p.new_tokens < 1 || p.q_heads < 1 || p.kv_heads < 1 || p.q_heads > kMostHeads ||
         p.head_dim < 1)
+        return GDN_ERR_INVALID_ARG;
+    // Rows of q: a grid has as many blocks at most.
+    if (c.num_seqs < 0 || (int64_t)c.num_seqs * p.new_tokens > INT32_MAX / p.q_heads)
         return GDN_ERR_INVALID_ARG;
     if (p.new_tokens > kMaxNewTokens || p.q_heads % p.kv_heads != 0 ||
         (p.head_dim != 64 && p.head_dim != 128 && p.head_dim != 256) ||
@@ -210,10 +213,9 @@ GDN_API gdn_status gdn_paged_append(const gdn_rope_problem *problem, const gdn_p
 
 GDN_API size_t gdn_paged_attention_workspace_size(const gdn_attention_problem *problem,
                                                   const gdn_paged_cache *cache) {
-    if (!problem || !cache || check_attention(*problem) != GDN_OK) return 0;
+    if (!problem || !cache || check_attention(*problem, *cache) != GDN_OK) return 0;
     const gdn_paged_cache &c = *cache;
-    if (c.num_seqs < 0 || c.num_seqs > kMostTokens / kMaxNewTokens || c.max_pages < 0 ||
-        c.page_size < 1 || (int64_t)c.max_pages * c.page_size > kMaxCached)
+    if (c.max_pages < 0 || c.page_size < 1 || c.page_size > 1 << 20 || (int64_t)c.max_pages * c.page_size > kMaxCached)
         return 0;
     return paged_attention_workspace(*problem, c);
 }
@@ -225,11 +227,10 @@ GDN_API gdn_status gdn_paged_attention(const gdn_attention_problem *problem,
     if (!problem || !cache) return GDN_ERR_INVALID_ARG;
     const gdn_attention_problem &p = *problem;
     const gdn_paged_cache &c = *cache;
-    gdn_status st = check_attention(p);
+    gdn_status st = check_attention(p, c);
     if (st != GDN_OK) return st;
     st = check_cache(c, p.dtype, p.kv_heads, p.head_dim, true);
     if (st != GDN_OK) return st;
-    if (c.num_seqs > kMostTokens / kMaxNewTokens) return GDN_ERR_INVALID_ARG;
     const int64_t T = (int64_t)c.num_seqs * p.new_tokens;
     const size_t size = size_of(p.dtype);
     st = check_rows(T, p.q_heads, p.head_dim, size, q, p.q_stride, p.q_head_stride, out,

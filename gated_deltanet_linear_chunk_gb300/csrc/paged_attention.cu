@@ -33,56 +33,31 @@ __device__ __forceinline__ void store_joined(const AttentionArgs &a, const RowPl
     for (int i = 0; i < 4; ++i) out[i] = from_f32<T>(gate ? x[i] * inv * sigmoid(by[i]) : x[i] * inv);
 }
 
-// Joins the pieces of one unit.  Block x is the unit, or where there are more
-// units than groups the group that left its first piece; y are its rows, every
-// gridDim.y-th.  Few pieces are a warp's work, a row each; many are a block's:
+// Joins the pieces of one unit: block x of the units, y of its rows (every
+// gridDim.y-th).  Few pieces are a warp's work, a row each; many are a block's:
 // threads take four elements of a row, several pieces at a time.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
-gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows, int groups, bool by_unit) {
+gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows) {
     constexpr int WORDS = D / 4, TEAMS = kJoinThreads / WORDS, WARPS = kJoinThreads / 32;
     constexpr float kNone = -__builtin_huge_valf();
     __shared__ float weight[kAttentionGroups + 1];
     __shared__ int slots[kAttentionGroups + 1], counts[kJoinEach * (kJoinThreads / 32)];
     __shared__ float tops[WARPS], totals[WARPS];
     __shared__ float4 parts[kJoinThreads];
-    __shared__ int4 unit_join;
-    __shared__ int at;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int group = blockIdx.x;
-    if (by_unit) {
-        const int per_seq = a.Hkv * a.row_blocks;
-        const int n = blockIdx.x / per_seq, unit = blockIdx.x % per_seq;
-        if (threadIdx.x == 0) at = -1;
-        ptx::griddep_wait();
-        __syncthreads();
-        int4 j[kJoinEach];
-#pragma unroll
-        for (int k = 0; k < kJoinEach; ++k) {
-            const int i = k * kJoinThreads + threadIdx.x;
-            j[k] = i < groups ? a.joins[i] : make_int4(-1, 0, 0, 0);
-        }
-#pragma unroll
-        for (int k = 0; k < kJoinEach; ++k)
-            if (j[k].x == n && j[k].y == unit) at = k * kJoinThreads + threadIdx.x, unit_join = j[k];
-        __syncthreads();
-        group = at;
-        if (group < 0) return;
-    } else {
-        ptx::griddep_wait();
-    }
-    const int4 join = by_unit ? unit_join : a.joins[group];
-    if (join.x < 0) return;
-    const Unit u = [&] {
-        Unit v;
-        v.n = join.x;
-        v.head = join.y / a.row_blocks;
-        v.first_row = join.y % a.row_blocks * rows;
-        v.rows = min(rows, a.R - v.first_row);
-        v.len = 0;
-        return v;
-    }();
-    const int pieces = join.z + 1;
+    const int per_seq = a.Hkv * a.row_blocks, unit = blockIdx.x % per_seq;
+    Unit u;
+    u.n = blockIdx.x / per_seq;
+    u.head = unit / a.row_blocks;
+    u.first_row = unit % a.row_blocks * rows;
+    u.rows = min(rows, a.R - u.first_row);
+    u.len = 0;
+    ptx::griddep_wait();
+    const int2 join = a.joins[blockIdx.x];
+    const int group = join.x;
+    if (group < 0) return;
+    const int pieces = join.y + 1;
     // The first piece ends its group's range, the others begin theirs.
     auto slot = [&](int i) { return i == 0 ? 2 * group + 1 : 2 * (group + i); };
 
@@ -197,7 +172,7 @@ Plan plan(const gdn_attention_problem &p, const gdn_paged_cache &c) {
     pl.blocks = (int)(need < s.blocks ? need : s.blocks);
     pl.groups = pl.blocks * s.groups;
     // Any unit can be cut, also one without tokens.
-    pl.joins = (size_t)pl.groups * sizeof(int4);
+    pl.joins = ((size_t)pl.units * sizeof(int2) + 15) / 16 * 16;
     pl.stats = (size_t)pl.groups * 2 * s.rows * sizeof(float2);
     pl.sums = (size_t)pl.groups * 2 * s.rows * p.head_dim * sizeof(float);
     return pl;
@@ -212,13 +187,11 @@ gdn_status join(const AttentionArgs &a, const Plan &pl, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const bool by_unit = pl.units <= pl.groups;
-    const int x = by_unit ? (int)pl.units : pl.groups;
-    const int rows = pl.rows < a.R ? pl.rows : a.R, fit = kJoinBlocks > x ? kJoinBlocks / x : 1;
-    cfg.gridDim = dim3(x, rows < fit ? rows : fit);
+    const int rows = pl.rows < a.R ? pl.rows : a.R;
+    const int fit = kJoinBlocks > pl.units ? (int)(kJoinBlocks / pl.units) : 1;
+    cfg.gridDim = dim3((unsigned)pl.units, rows < fit ? rows : fit);
     cfg.blockDim = dim3(kJoinThreads);
-    return cudaLaunchKernelEx(&cfg, gdn_attention_join_kernel<T, D>, a, pl.rows, pl.groups,
-                              by_unit) == cudaSuccess
+    return cudaLaunchKernelEx(&cfg, gdn_attention_join_kernel<T, D>, a, pl.rows) == cudaSuccess
                ? GDN_OK
                : GDN_ERR_CUDA;
 }
@@ -265,7 +238,7 @@ gdn_status launch_paged_attention(const gdn_attention_problem &p, const gdn_page
     // Multiples of 16 bytes first: they are read in such words.
     char *w = static_cast<char *>(p.workspace);
     a.sums = reinterpret_cast<float *>(w);
-    a.joins = reinterpret_cast<int4 *>(w + pl.sums);
+    a.joins = reinterpret_cast<int2 *>(w + pl.sums);
     a.stats = reinterpret_cast<float2 *>(w + pl.sums + pl.joins);
     const gdn_status st = p.dtype == GDN_F32      ? attention_f32(p.head_dim, pl.blocks, a, stream)
                           : c.dtype == GDN_E4M3 ? attention_e4m3(p.head_dim, pl.blocks, a, stream)

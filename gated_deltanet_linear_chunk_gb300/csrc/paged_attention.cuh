@@ -55,7 +55,7 @@ struct AttentionArgs {
     bool q_words, gate_words, out_words;  // rows of q, gate and out in whole 16-byte words
     float scale_log2;  // scale log2 e: scores in powers of two
     // workspace
-    int4 *joins;     // [groups] the unit whose first piece the group left: n, unit, groups after it
+    int2 *joins;     // [units] where the unit was cut: its first piece's group, groups after it
     float2 *stats;   // [groups, 2, row block] maximum and sum; -infinity and 0: no sums
     float *sums;     // [groups, 2, row block, D]
 };
@@ -79,7 +79,7 @@ template <int TOKENS, int SETUP> __device__ __forceinline__ int tiles_of(int len
 struct Range {
     int64_t begin, end, total, block_end;
     int group, groups;
-    int n;          // the sequence it begins in
+    int n, len;     // the sequence it begins in, and its tokens
     int64_t base;   // that sequence's first tile
 };
 
@@ -96,7 +96,7 @@ __host__ __device__ __forceinline__ int group_of(int64_t total, int groups, int6
 template <int TOKENS, int SETUP, int THREADS, int GROUPS>
 __device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
     __shared__ int64_t warp_sums[THREADS / 32], found_base[GROUPS];
-    __shared__ int found[GROUPS];
+    __shared__ int found[GROUPS], found_len[GROUPS];
     const int run = (a.N + THREADS - 1) / THREADS;
     const int n0 = min((int)threadIdx.x * run, a.N), n1 = min(n0 + run, a.N);
     int64_t count = 0;
@@ -109,7 +109,7 @@ __device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
         if (lane >= o) upto += below;
     }
     if (lane == 31) warp_sums[warp] = upto;
-    if (threadIdx.x < GROUPS) found[threadIdx.x] = 0, found_base[threadIdx.x] = 0;
+    if (threadIdx.x < GROUPS) found[threadIdx.x] = found_len[threadIdx.x] = 0, found_base[threadIdx.x] = 0;
     __syncthreads();
     int64_t total = 0;
 #pragma unroll
@@ -127,9 +127,11 @@ __device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
         if (begin < base || begin >= upto * per_seq) continue;
         int64_t at = base;
         for (int n = n0; n < n1; ++n) {
-            const int64_t next = at + (int64_t)tiles_of<TOKENS, SETUP>(held_tokens(a, n)) * per_seq;
+            const int len = held_tokens(a, n);
+            const int64_t next = at + (int64_t)tiles_of<TOKENS, SETUP>(len) * per_seq;
             if (begin < next) {
                 found[g] = n;
+                found_len[g] = len;
                 found_base[g] = at;
                 break;
             }
@@ -142,6 +144,7 @@ __device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
     r.end = first_tile(r.total, r.groups, r.group + 1);
     r.block_end = first_tile(r.total, r.groups, (blockIdx.x + 1) * GROUPS);
     r.n = found[mine];
+    r.len = found_len[mine];
     r.base = found_base[mine];
     return r;
 }
@@ -189,26 +192,27 @@ __device__ __forceinline__ Unit unit_of(const AttentionArgs &a, int n, int unit,
     u.len = len;
     return u;
 }
-// The join of a unit whose first tile is `at`, from a group's piece on.
-__device__ __forceinline__ int4 join_from(const Range &g, int group, int n, const Piece &p, int64_t at) {
-    if (p.first != 0 || p.last == p.tiles) return make_int4(-1, 0, 0, 0);
-    return make_int4(n, p.unit, group_of(g.total, g.groups, at + p.tiles - 1) - group, 0);
+// The join of a unit of `tiles` from `at` on, of which a group has the first
+// `last`; {-1, 0} where that is all.
+__device__ __forceinline__ int2 join_from(const Range &g, int group, int last, int tiles, int64_t at) {
+    return last == tiles ? make_int2(-1, 0)
+                         : make_int2(group, group_of(g.total, g.groups, at + tiles - 1) - group);
 }
 
-// Runs `work(unit, piece)` over a group's range; its last join.
+// Runs `work(unit, piece)` over a block's range, its only group's.
 template <int TOKENS, int SETUP, int ROWS, typename F>
-__device__ __forceinline__ int4 for_pieces(const AttentionArgs &a, const Range &g, F &&work) {
+__device__ __forceinline__ void for_pieces(const AttentionArgs &a, const Range &g, F &&work) {
     const int per_seq = a.Hkv * a.row_blocks;
-    int4 join = make_int4(-1, 0, 0, 0);
-    if (g.begin >= g.end) return join;
-    int n = g.n, len = held_tokens(a, n);
+    if (g.begin >= g.end) return;
+    int n = g.n, len = g.len;
     Piece p;
     p.tiles = tiles_of<TOKENS, SETUP>(len);
     p.unit = (int)((g.begin - g.base) / p.tiles);
     p.first = (int)((g.begin - g.base) % p.tiles);
     for (int64_t pos = g.begin; pos < g.end;) {
         p.last = (int)min((int64_t)p.tiles, p.first + (g.end - pos));
-        join = join_from(g, g.group, n, p, pos - p.first);
+        if (p.first == 0 && threadIdx.x == 0)
+            a.joins[(int64_t)n * per_seq + p.unit] = join_from(g, g.group, p.last, p.tiles, pos);
         work(unit_of<ROWS>(a, n, p.unit, len), p);
         pos += p.last - p.first;
         p.first = 0;
@@ -218,7 +222,6 @@ __device__ __forceinline__ int4 for_pieces(const AttentionArgs &a, const Range &
             p.tiles = tiles_of<TOKENS, SETUP>(len);
         }
     }
-    return join;
 }
 
 // A row's element i, divided by the sum and gated.

@@ -72,6 +72,18 @@ __device__ __forceinline__ uint32_t widen(uint32_t two) {
     return r;
 }
 
+// Asks for a unit's rows of x, a line of 128 bytes per lane.
+template <int D, typename T>
+__device__ __forceinline__ void prefetch_rows(const AttentionArgs &a, const Unit &u, const T *x,
+                                              int64_t stride, int64_t head_stride, int lane) {
+    constexpr int LINES = D * (int)sizeof(T) / 128;
+    for (int i = lane; i < u.rows * LINES; i += 32) {
+        const RowPlace p = row_place(a, u, i / LINES);
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(x + p.token * stride + p.head * head_stride +
+                                                      i % LINES * (D / LINES)));
+    }
+}
+
 // Eight elements, in one word where the rows allow it.
 __device__ __forceinline__ Vec<__nv_bfloat16, 8> load8(const __nv_bfloat16 *p, bool words) {
     if (words) return Vec<__nv_bfloat16, 8>::load(p);
@@ -106,17 +118,20 @@ template <bool EIGHT, int D, int NB, int MT, int GR> struct Tiles {
     static constexpr int kSumPitch = D + 4;
     static constexpr int kSums = 8 * kSumPitch * 4;
     static constexpr int kOwn = MT > 1 ? MT * GR * kSums : 0;
-    static constexpr int kRoom = 115712 - 1024;  // of two blocks per SM, each
-    static constexpr int kFit = (kRoom - kOwn) / (GR * kTile);
-    static constexpr int kStages = kFit >= 9 ? 9 : kFit % 2 ? kFit : kFit - 1;  // odd
+    // Two blocks per SM, with some 64 KB of copies in flight: enough for the
+    // memory's latency.  More only queue, and unfairly: the SMs of fuller GPCs
+    // then end later (three stages per warp, 128 KB: 262144 tokens 179 us, two
+    // stages 172; the last SM at 186 us of 162 on average).
+    static constexpr int kBlocks = 2;
+    static constexpr int kStages = MT > 2 ? 5 : MT > 1 ? 3 : 2;
     static constexpr int kRing = GR * kStages * kTile;
     static constexpr int kBytes = kRing + kOwn;
-    static_assert(kStages >= 3 && kSums <= kTile, "");
+    static_assert(kBytes <= 233472 / kBlocks - 2048 && kSums <= kTile, "");
     static_assert(GR == 1 || GR * kRows * kSumPitch * 4 <= kBytes, "");
 };
 
 template <bool EIGHT, int D, int NB, int MT, int GR>
-__global__ void __launch_bounds__(MT *GR * 32, 2)
+__global__ void __launch_bounds__(MT *GR * 32, Tiles<EIGHT, D, NB, MT, GR>::kBlocks)
 gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     using S = Tiles<EIGHT, D, NB, MT, GR>;
     using T = __nv_bfloat16;
@@ -147,6 +162,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     ptx::griddep_launch_dependents();
     const int per_seq = a.Hkv * a.row_blocks;
     const Range range = find_range<TK, SETUP, S::kThreads, GR>(a, per_seq, group);
+    const T *queries = static_cast<const T *>(a.q), *gates = static_cast<const T *>(a.gate);
 
     // ---- the copies, ahead of the products.  The cursor is at the tile whose
     // entries of the page table are on their way.
@@ -156,7 +172,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     } c;
     c.left = range.end - range.begin;
     c.n = range.n;
-    c.len = c.left > 0 ? held_tokens(a, c.n) : 0;
+    c.len = range.len;
     c.tiles = tiles_of<TK, SETUP>(c.len);
     c.unit = (int)((range.begin - range.base) / c.tiles);
     c.tile = (int)((range.begin - range.base) % c.tiles);
@@ -167,9 +183,12 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
         joined = make_int4(GR > 1 && c.left > 0 && last <= c.tiles, c.n, c.unit,
                            (c.tile == 0 ? 1 : 0) | (last == c.tiles ? 2 : 0));
     }
+    const int range_tiles = c.tiles;  // of the unit that the range begins in
     Piece piece;
     piece.unit = c.unit, piece.first = c.tile, piece.tiles = c.tiles;
     int n = c.n, len = c.len;
+    if (c.left > 0)
+        prefetch_rows<D>(a, unit_of<S::kRows>(a, n, c.unit, len), queries, a.qs, a.qh, lane);
 
     // Sixteen tokens that follow one another share a page where the size allows
     // it: then a lane knows the places of a whole segment, else of one token.
@@ -260,11 +279,16 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     int stage = 0;  // the next to be used; the one before it is free
     auto free_stage = [&] { return stage == 0 ? ST - 1 : stage - 1; };
     look_up();
+    if constexpr (ST == 2) {
+        place(0);
+        copy(0, a.k, a.kts, k_at);
+    } else {
 #pragma unroll 1
-    for (int i = 0; i < AHEAD; ++i) {
-        place(i);
-        copy(2 * i, a.k, a.kts, k_at);
-        copy(2 * i + 1, a.v, a.vts, v_at);
+        for (int i = 0; i < AHEAD; ++i) {
+            place(i);
+            copy(2 * i, a.k, a.kts, k_at);
+            copy(2 * i + 1, a.v, a.vts, v_at);
+        }
     }
     __syncthreads();
     const bool together = joined.x != 0;
@@ -312,12 +336,20 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     };
 
     // ---- the products, unit by unit
-    int4 join = make_int4(-1, 0, 0, 0);
     const float sign = a.scale_log2 < 0.f ? -1.f : a.scale_log2 == 0.f ? 0.f : 1.f;
     const float magnitude = sign == 0.f ? 1.f : fabsf(a.scale_log2);
     for (int64_t pos = range.begin; pos < range.end;) {
         piece.last = (int)min((int64_t)piece.tiles, piece.first + (range.end - pos));
         const Unit u = unit_of<S::kRows>(a, n, piece.unit, len);
+        // What is wanted later: the gates, and the next unit's queries.
+        if (!together) {
+            if (piece.whole() && a.gate) prefetch_rows<D>(a, u, gates, a.gs, a.gh, lane);
+            if (pos + piece.last - piece.first < range.end) {
+                const bool same = piece.unit + 1 < per_seq;
+                prefetch_rows<D>(a, unit_of<S::kRows>(a, same ? n : n + 1, same ? piece.unit + 1 : 0, 0),
+                                 queries, a.qs, a.qh, lane);
+            }
+        }
         const int t0 = piece.template first_token<TK, SETUP>(len), t1 = piece.template last_token<TK, SETUP>(len);
 
         // Queries, times the sign of the scale: rows 8 b + g8, elements 16 k + 2 c4
@@ -331,7 +363,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             const int r = mt * S::kWarpRows + b * 8 + g8;
             const bool live = r < u.rows;
             const RowPlace p = row_place(a, u, live ? r : 0);
-            const T *from = static_cast<const T *>(a.q) + p.token * a.qs + p.head * a.qh;
+            const T *from = queries + p.token * a.qs + p.head * a.qh;
 #pragma unroll
             for (int k = 0; k < DT; ++k)
 #pragma unroll
@@ -394,10 +426,11 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             // ---- keys
             copies_wait<ST - 2>();
             group_sync();
-            place(AHEAD);
+            if constexpr (ST > 2) place(AHEAD);
             bad |= bad_tiles & 1;
             bad_tiles >>= 1;
-            copy(free_stage(), a.k, a.kts, k_at);
+            if constexpr (ST > 2) copy(free_stage(), a.k, a.kts, k_at);
+            else copy(free_stage(), a.v, a.vts, v_at);
             // Short chains of products: where they are few, even and odd steps
             // have sums of their own.
             constexpr int CHAINS = TT * NB < 4 ? 2 : 1;
@@ -509,7 +542,12 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             // ---- values
             copies_wait<ST - 2>();
             group_sync();
-            copy(free_stage(), a.v, a.vts, v_at);
+            if constexpr (ST > 2) {
+                copy(free_stage(), a.v, a.vts, v_at);
+            } else {
+                place(0);
+                copy(free_stage(), a.k, a.kts, k_at);
+            }
             const char *tile = ring + stage * S::kTile;
             const uint32_t values = ring_at + stage * S::kTile + v_lane;
             // The newest tokens' values may be infinite or NaN where some rows
@@ -629,7 +667,8 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             const float v_scale = EIGHT ? a.v_scale[u.head] : 1.f;
             float *sums = reinterpret_cast<float *>(
                 MT > 1 ? smem + S::kRing + warp * S::kSums : ring + free_stage() * S::kTile);
-            join = join_from(range, range.group, n, piece, pos - piece.first);
+            if (piece.first == 0 && mt == 0 && lane == 0)
+                a.joins[(int64_t)n * per_seq + piece.unit] = join_from(range, range.group, piece.last, piece.tiles, pos);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 const int r0 = mt * S::kWarpRows + b * 8;
@@ -641,7 +680,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
                         const int at = i * 32 + lane, r = r0 + at / Q8;
                         if (r >= u.rows) continue;
                         const RowPlace p = row_place(a, u, r);
-                        gate[i] = load8((const T *)a.gate + p.token * a.gs + p.head * a.gh + at % Q8 * 8,
+                        gate[i] = load8(gates + p.token * a.gs + p.head * a.gh + at % Q8 * 8,
                                         a.gate_words);
                     }
                 }
@@ -700,10 +739,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
         }
     }
     copies_wait<0>();
-    if (!together) {
-        if (mt == 0 && lane == 0) a.joins[range.group] = join;
-        return;
-    }
+    if (!together) return;
 
     // ---- the groups' sums, joined
     if constexpr (GR > 1) {
@@ -739,17 +775,9 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             else a.stats[slot * S::kRows + r] = make_float2(top, sum);
             inverses[r] = whole ? inverse(sum) : 1.f;
         }
-        if (threadIdx.x < GR) {
-            // The unit begins with the block's first tile: its other tiles are
-            // counted from there.
-            int4 mine = make_int4(-1, 0, 0, 0);
-            if (threadIdx.x == 0 && joined.w == 1) {
-                Piece p;
-                p.unit = joined.z, p.first = 0, p.last = 0, p.tiles = tiles_of<TK, SETUP>(held_tokens(a, joined.y));
-                mine = join_from(range, group0, joined.y, p, range.begin);
-            }
-            a.joins[group0 + threadIdx.x] = mine;
-        }
+        if (threadIdx.x == 0 && joined.w & 1)
+            a.joins[(int64_t)joined.y * per_seq + joined.z] =
+                join_from(range, group0, whole ? range_tiles : 0, range_tiles, range.begin);
         __syncthreads();
         constexpr int Q8 = D / 8;
         const int words = u.rows * Q8;
@@ -759,7 +787,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             const RowPlace p = row_place(a, u, r);
             Vec<T, 8> gate = Vec<T, 8>::zero();
             if (whole && a.gate)
-                gate = load8((const T *)a.gate + p.token * a.gs + p.head * a.gh + e, a.gate_words);
+                gate = load8(gates + p.token * a.gs + p.head * a.gh + e, a.gate_words);
             float y[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) y[k] = 0.f;

@@ -29,7 +29,7 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
     float *pw = ps + warp * RR * kSimtTokens;
     ptx::griddep_launch_dependents();
     const Range range = find_range<kSimtChunk, 1, kSimtWarps * 32, 1>(a, a.Hkv * a.row_blocks, 0);
-    const int4 join = for_pieces<kSimtChunk, 1, RR>(a, range, [&](const Unit &u, const Piece &piece) {
+    for_pieces<kSimtChunk, 1, RR>(a, range, [&](const Unit &u, const Piece &piece) {
         const int t0 = piece.first_token<kSimtChunk, 1>(u.len), t1 = piece.last_token<kSimtChunk, 1>(u.len);
         const int slot = piece.whole() ? -1 : piece.slot(range.group);
         __syncthreads();  // the last piece's rows
@@ -154,7 +154,6 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
             }
         }
     });
-    if (threadIdx.x == 0) a.joins[range.group] = join;
 }
 
 // Rows at a time: those of a unit, up to 16.

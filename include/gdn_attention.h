@@ -149,7 +149,7 @@ GDN_API gdn_status gdn_paged_append(const gdn_rope_problem *problem, const gdn_p
  *                 n L + t of q, gate and out, and index seq_lens[n] - L + t of
  *                 the sequence
  *   q_heads       Hq, a multiple of kv_heads: query heads h Hq / Hkv .. share
- *                 key head h
+ *                 key head h; 1 to 4096, and N L Hq at most 2^31 - 1
  *   head_dim      D: 64, 128 or 256
  *   dtype         GDN_BF16 or GDN_F32; the cache has the same, or is GDN_E4M3
  *                 beside GDN_BF16
