@@ -80,6 +80,8 @@ struct Range {
     int64_t begin, end, total, block_end;
     int group, groups;
     int n, len;     // the sequence it begins in, and its tokens
+    int4 together;  // of the block, where it lies inside one unit: 1, n, the unit, and
+                    // whether its first (1) and last tile (2) are among the block's
     int64_t base;   // that sequence's first tile
 };
 
@@ -97,6 +99,7 @@ template <int TOKENS, int SETUP, int THREADS, int GROUPS>
 __device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
     __shared__ int64_t warp_sums[THREADS / 32], found_base[GROUPS];
     __shared__ int found[GROUPS], found_len[GROUPS];
+    __shared__ int4 together;
     const int run = (a.N + THREADS - 1) / THREADS;
     const int n0 = min((int)threadIdx.x * run, a.N), n1 = min(n0 + run, a.N);
     int64_t count = 0;
@@ -109,6 +112,7 @@ __device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
         if (lane >= o) upto += below;
     }
     if (lane == 31) warp_sums[warp] = upto;
+    if (threadIdx.x == 0) together = make_int4(0, 0, 0, 0);
     if (threadIdx.x < GROUPS) found[threadIdx.x] = found_len[threadIdx.x] = 0, found_base[threadIdx.x] = 0;
     __syncthreads();
     int64_t total = 0;
@@ -120,8 +124,9 @@ __device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
     Range r;
     r.total = total * per_seq;
     r.groups = (int)min((int64_t)gridDim.x * GROUPS, r.total);
+    r.block_end = first_tile(r.total, r.groups, (blockIdx.x + 1) * GROUPS);
     const int64_t base = (upto - count) * per_seq;
-#pragma unroll
+#pragma unroll 1
     for (int g = 0; g < GROUPS; ++g) {
         const int64_t begin = first_tile(r.total, r.groups, blockIdx.x * GROUPS + g);
         if (begin < base || begin >= upto * per_seq) continue;
@@ -133,6 +138,13 @@ __device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
                 found[g] = n;
                 found_len[g] = len;
                 found_base[g] = at;
+                if (GROUPS > 1 && g == 0) {
+                    const int tiles = tiles_of<TOKENS, SETUP>(len);
+                    const int unit = (int)((begin - at) / tiles), first = (int)((begin - at) % tiles);
+                    const int64_t last = first + r.block_end - begin;
+                    if (last <= tiles)
+                        together = make_int4(1, n, unit, (first == 0 ? 1 : 0) | (last == tiles ? 2 : 0));
+                }
                 break;
             }
             at = next;
@@ -142,7 +154,7 @@ __device__ Range find_range(const AttentionArgs &a, int per_seq, int mine) {
     r.group = blockIdx.x * GROUPS + mine;
     r.begin = first_tile(r.total, r.groups, r.group);
     r.end = first_tile(r.total, r.groups, r.group + 1);
-    r.block_end = first_tile(r.total, r.groups, (blockIdx.x + 1) * GROUPS);
+    r.together = together;
     r.n = found[mine];
     r.len = found_len[mine];
     r.base = found_base[mine];

@@ -72,18 +72,6 @@ __device__ __forceinline__ uint32_t widen(uint32_t two) {
     return r;
 }
 
-// Asks for a unit's rows of x, a line of 128 bytes per lane.
-template <int D, typename T>
-__device__ __forceinline__ void prefetch_rows(const AttentionArgs &a, const Unit &u, const T *x,
-                                              int64_t stride, int64_t head_stride, int lane) {
-    constexpr int LINES = D * (int)sizeof(T) / 128;
-    for (int i = lane; i < u.rows * LINES; i += 32) {
-        const RowPlace p = row_place(a, u, i / LINES);
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(x + p.token * stride + p.head * head_stride +
-                                                      i % LINES * (D / LINES)));
-    }
-}
-
 // Eight elements, in one word where the rows allow it.
 __device__ __forceinline__ Vec<__nv_bfloat16, 8> load8(const __nv_bfloat16 *p, bool words) {
     if (words) return Vec<__nv_bfloat16, 8>::load(p);
@@ -143,7 +131,6 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     extern __shared__ __align__(16) char smem[];
     __shared__ float2 ml[GR][S::kRows];
     __shared__ float inverses[S::kRows];
-    __shared__ int4 joined;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int group = warp / MT, mt = warp % MT;
     const int g8 = lane / 4, c4 = lane % 4;
@@ -176,19 +163,10 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     c.tiles = tiles_of<TK, SETUP>(c.len);
     c.unit = (int)((range.begin - range.base) / c.tiles);
     c.tile = (int)((range.begin - range.base) % c.tiles);
-    // Where a whole block lies inside one unit its groups' sums are joined
-    // here, and it has one piece: {whether, n, unit, its first and last tile}.
-    if (threadIdx.x == 0) {
-        const int64_t last = c.tile + range.block_end - range.begin;
-        joined = make_int4(GR > 1 && c.left > 0 && last <= c.tiles, c.n, c.unit,
-                           (c.tile == 0 ? 1 : 0) | (last == c.tiles ? 2 : 0));
-    }
     const int range_tiles = c.tiles;  // of the unit that the range begins in
     Piece piece;
     piece.unit = c.unit, piece.first = c.tile, piece.tiles = c.tiles;
     int n = c.n, len = c.len;
-    if (c.left > 0)
-        prefetch_rows<D>(a, unit_of<S::kRows>(a, n, c.unit, len), queries, a.qs, a.qh, lane);
 
     // Sixteen tokens that follow one another share a page where the size allows
     // it: then a lane knows the places of a whole segment, else of one token.
@@ -279,18 +257,9 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     int stage = 0;  // the next to be used; the one before it is free
     auto free_stage = [&] { return stage == 0 ? ST - 1 : stage - 1; };
     look_up();
-    if constexpr (ST == 2) {
-        place(0);
-        copy(0, a.k, a.kts, k_at);
-    } else {
-#pragma unroll 1
-        for (int i = 0; i < AHEAD; ++i) {
-            place(i);
-            copy(2 * i, a.k, a.kts, k_at);
-            copy(2 * i + 1, a.v, a.vts, v_at);
-        }
-    }
-    __syncthreads();
+    // Where a whole block lies inside one unit its groups' sums are joined here,
+    // and it has one piece.
+    const int4 joined = range.together;
     const bool together = joined.x != 0;
 
     // Sums of the piece's unit: element 16 d + g8 (and + 8; of 8-bit tiles 2 g8
@@ -341,15 +310,6 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
     for (int64_t pos = range.begin; pos < range.end;) {
         piece.last = (int)min((int64_t)piece.tiles, piece.first + (range.end - pos));
         const Unit u = unit_of<S::kRows>(a, n, piece.unit, len);
-        // What is wanted later: the gates, and the next unit's queries.
-        if (!together) {
-            if (piece.whole() && a.gate) prefetch_rows<D>(a, u, gates, a.gs, a.gh, lane);
-            if (pos + piece.last - piece.first < range.end) {
-                const bool same = piece.unit + 1 < per_seq;
-                prefetch_rows<D>(a, unit_of<S::kRows>(a, same ? n : n + 1, same ? piece.unit + 1 : 0, 0),
-                                 queries, a.qs, a.qh, lane);
-            }
-        }
         const int t0 = piece.template first_token<TK, SETUP>(len), t1 = piece.template last_token<TK, SETUP>(len);
 
         // Queries, times the sign of the scale: rows 8 b + g8, elements 16 k + 2 c4
@@ -374,6 +334,19 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
                     else q[k][b][h] = (uint32_t) reinterpret_cast<const uint16_t *>(x)[0] |
                                       (uint32_t) reinterpret_cast<const uint16_t *>(x)[1] << 16;
                 }
+        }
+        if (pos == range.begin) {  // the first copies, while the queries are on their way
+            if constexpr (ST == 2) {
+                place(0);
+                copy(0, a.k, a.kts, k_at);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < AHEAD; ++i) {
+                    place(i);
+                    copy(2 * i, a.k, a.kts, k_at);
+                    copy(2 * i + 1, a.v, a.vts, v_at);
+                }
+            }
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -673,17 +646,18 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
             for (int b = 0; b < NB; ++b) {
                 const int r0 = mt * S::kWarpRows + b * 8;
                 constexpr int Q8 = D / 8, EACH = 8 * Q8 / 32;
-                Vec<T, 8> gate[EACH];
-                if (whole && a.gate) {
-#pragma unroll
-                    for (int i = 0; i < EACH; ++i) {
-                        const int at = i * 32 + lane, r = r0 + at / Q8;
-                        if (r >= u.rows) continue;
-                        const RowPlace p = row_place(a, u, r);
-                        gate[i] = load8(gates + p.token * a.gs + p.head * a.gh + at % Q8 * 8,
-                                        a.gate_words);
-                    }
-                }
+                // Rows and their places: of row lane % 8 by each lane, from there by
+                // those that have its elements.
+                const RowPlace p = row_place(a, u, min(r0 + lane % 8, u.rows - 1));
+                const int64_t out_at = p.token * a.os + p.head * a.oh, gate_at = p.token * a.gs + p.head * a.gh;
+                auto gate_of = [&](int i) {
+                    const int at = i * 32 + lane, r = at / Q8;
+                    const int64_t from = __shfl_sync(0xffffffffu, gate_at, r);
+                    return r0 + r < u.rows ? load8(gates + from + at % Q8 * 8, a.gate_words) : Vec<T, 8>::zero();
+                };
+                Vec<T, 8> gate = Vec<T, 8>::zero();
+                const bool gated = whole && a.gate;
+                if (gated) gate = gate_of(0);
                 lay_out(sums, b, whole ? inverse(l[b][0]) * v_scale : v_scale,
                         whole ? inverse(l[b][1]) * v_scale : v_scale);
                 if (g8 == 0) {
@@ -696,26 +670,28 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
                     }
                 }
                 __syncwarp();
-#pragma unroll
+#pragma unroll 1  // little code: a unit's end is where instructions are not at hand
                 for (int i = 0; i < EACH; ++i) {
-                    const int at = i * 32 + lane, r = r0 + at / Q8, e = at % Q8 * 8;
-                    if (r >= u.rows) continue;
-                    const float4 *x = reinterpret_cast<const float4 *>(sums + at / Q8 * S::kSumPitch + e);
+                    const Vec<T, 8> now = gate;
+                    if (gated && i + 1 < EACH) gate = gate_of(i + 1);
+                    const int at = i * 32 + lane, r = at / Q8, e = at % Q8 * 8;
+                    const float4 *x = reinterpret_cast<const float4 *>(sums + r * S::kSumPitch + e);
                     const float4 x0 = x[0], x1 = x[1];
+                    const int64_t to = __shfl_sync(0xffffffffu, out_at, r);
+                    if (r0 + r >= u.rows) continue;
                     if (whole) {
                         float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-                        if (a.gate) {
+                        if (gated) {
                             float by[8];
-                            gate[i].to(by);
+                            now.to(by);
 #pragma unroll
                             for (int k = 0; k < 8; ++k) y[k] *= sigmoid(by[k]);
                         }
-                        const RowPlace p = row_place(a, u, r);
-                        store8((T *)a.out + p.token * a.os + p.head * a.oh + e, a.out_words, y);
+                        store8((T *)a.out + to + e, a.out_words, y);
                     } else {
-                        float4 *to = reinterpret_cast<float4 *>(a.sums + ((int64_t)slot * S::kRows + r) * D + e);
-                        to[0] = x0;
-                        to[1] = x1;
+                        float4 *sum = reinterpret_cast<float4 *>(a.sums + ((int64_t)slot * S::kRows + r0 + r) * D + e);
+                        sum[0] = x0;
+                        sum[1] = x1;
                     }
                 }
                 __syncwarp();
