@@ -5,13 +5,19 @@
 // Per head one read and one write of D elements and some ten operations on
 // each: bound by memory.  A warp takes a token, or a part of its heads where
 // there are few tokens, so the sines and cosines of the token's angles are
-// computed once for all its heads, one per lane, and kept in shared memory.
+// computed once for all its heads, one per lane.  With a weight w and x' the
+// partner of x, norm and rotation are
+//     y = (x (w cos) + x' (-+ w' sin)) / sqrt(mean(x^2) + eps)
+// with factors that all heads share: a lane keeps those of its elements in
+// registers, loads its words of several heads at once, and gets the partners by a
+// shuffle.
 #include "attention.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kWarps = 4;  // per block
+constexpr int kWarpsPerSm = 24;
 
 // The head's elements of one tensor: from, to (null: nothing is stored) and
 // the strides between heads.
@@ -21,8 +27,8 @@ struct RopeArgs {
     const float *q_weight, *k_weight, *inv_freq;
     const int32_t *positions;
     int64_t qs, qh, ks, kh, vs, vh, qos, qoh, kos, koh, axis_stride;
-    int T, Hq, Hk, D, half, interleaved, lanes, parts;
-    float eps;
+    int T, Hq, Hk, D, half, interleaved, parts;
+    float eps, inv_dim;
     // the append's
     void *k_cache, *v_cache;
     const float *k_scale, *v_scale;
@@ -37,10 +43,12 @@ struct RopeArgs {
 // bits, so the angle of position p is off by |p| 2^-53 of inv_freq: 1e-7 radians
 // at 2^29 and one radian per position.  (One double product per pair and warp;
 // the positions' products are of integers.)
+// Odd: not a number, for an infinite or NaN inv_freq.
 __device__ __forceinline__ uint64_t turn_of(float inv_freq) {
+    if (!isfinite(inv_freq)) return 1;
     double t = (double)inv_freq * 0.15915494309189533577;  // 1 / 2 pi
     t -= floor(t);
-    return (uint64_t)(t * 18446744073709551616.0);
+    return (uint64_t)(t * 18446744073709551616.0) & ~1ull;
 }
 // cos and sin of position times turn.  The upper 32 bits, in half turns, round
 // to fp32's 24: half a step is 2^-25 half turns, 9e-8 radians.
@@ -48,10 +56,11 @@ __device__ __forceinline__ float2 angle_of(int32_t position, uint64_t turn) {
     const int32_t top = (int32_t)(((uint64_t)(int64_t)position * turn) >> 32);
     float2 r;
     sincospif((float)top * 0x1p-31f, &r.y, &r.x);
+    if (turn & 1) r.x = r.y = __int_as_float(0x7fffffff);
     return r;
 }
 
-// V elements as they are stored in the cache, times 1 / scale of it.
+// V elements as they are stored in the cache, over its scale.
 template <typename TC, int V> struct Stored {
     static __device__ __forceinline__ void store(TC *p, float (&y)[V], float) {
         Vec<TC, V>::from(y).store(p);
@@ -59,222 +68,374 @@ template <typename TC, int V> struct Stored {
 };
 template <int V> struct Stored<__nv_fp8_e4m3, V> {
     static __device__ __forceinline__ void store(__nv_fp8_e4m3 *p, float (&y)[V], float scale) {
-        uint8_t b[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i)  // a quotient, as the definition has it: no reciprocal
-            b[i] = __nv_cvt_float_to_fp8(__fdiv_rn(y[i], scale), __NV_SATFINITE, __NV_E4M3);
         if constexpr (V == 8) {
-            uint2 w;
-            w.x = b[0] | b[1] << 8 | b[2] << 16 | (uint32_t)b[3] << 24;
-            w.y = b[4] | b[5] << 8 | b[6] << 16 | (uint32_t)b[7] << 24;
-            *reinterpret_cast<uint2 *>(p) = w;
-        } else {
+            uint32_t two[4];
 #pragma unroll
-            for (int i = 0; i < V; ++i) reinterpret_cast<uint8_t *>(p)[i] = b[i];
-        }
-    }
-};
-
-// What a lane does with its j-th word of a head: its first element, whether it
-// lies in the head, and for rotated ones the partner's element and the pair.
-struct Word {
-    int e, partner, pair;
-    float sign;  // of the sine's term: -1 for a pair's first element
-    bool in, turned;
-};
-
-// T: of the tensors, TC: of the cache.  V elements per word, NW words per lane.
-template <typename T, typename TC, int V, int NW, bool APPEND>
-__global__ void __launch_bounds__(kWarps * 32) gdn_qk_rope_kernel(const __grid_constant__ RopeArgs a) {
-    __shared__ float2 turns[kWarps][kMaxRotary / 2];
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t at = (int64_t)blockIdx.x * kWarps + warp;
-    const int t = (int)(at / a.parts), part = (int)(at % a.parts);
-    if (t >= a.T) return;
-    float2 *cs = turns[warp];
-
-    // The token's place.
-    int index = 0;
-    int64_t k_at = -1, v_at = -1;
-    if (APPEND) {
-        int n, after;  // the sequence, and its tokens from this one on
-        if (a.cu) {
-            if (t < a.cu[0] || t >= a.cu[a.N]) return;
-            const Span s = locate_by_warp(a.cu, a.N, a.T, t);
-            n = s.n, after = s.end - t;
+            for (int i = 0; i < 4; ++i)  // a quotient, as the definition has it: no reciprocal
+                two[i] = __nv_cvt_float2_to_fp8x2(
+                    make_float2(__fdiv_rn(y[2 * i], scale), __fdiv_rn(y[2 * i + 1], scale)),
+                    __NV_SATFINITE, __NV_E4M3);
+            *reinterpret_cast<uint2 *>(p) = make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
         } else {
-            const int each = a.T / a.N;
-            n = t / each, after = each - t % each;
-        }
-        index = min(max(a.lens[n], 0), a.capacity) - after;
-        if (index >= 0) {
-            const int page = a.table[n * a.table_stride + index / a.page_size];
-            if (page >= 0 && page < a.pages) {
-                const int place = index % a.page_size;
-                k_at = page * a.kps + place * a.kts;
-                v_at = page * a.vps + place * a.vts;
-            }
+            static_assert(V == 1, "");
+            *reinterpret_cast<uint8_t *>(p) =
+                __nv_cvt_float_to_fp8(__fdiv_rn(y[0], scale), __NV_SATFINITE, __NV_E4M3);
         }
     }
-    for (int i = lane; i < a.half; i += 32) {
-        const float f = a.inv_freq[i];
-        const int32_t p = a.positions ? a.positions[a.axis[i] * a.axis_stride + t] : index;
-        float2 r = angle_of(p, turn_of(f));
-        if (!isfinite(f)) r.x = r.y = __int_as_float(0x7fffffff);
-        cs[i] = r;
-    }
-    __syncwarp();
+};
 
-    const int lanes = a.lanes, row = lane / lanes, mine = lane % lanes, rows = 32 / lanes;
-    Word word[NW];
+// Where an appended token goes.
+struct Placed {
+    bool live;           // whether it belongs to a sequence
+    int index;           // in it
+    int64_t k_at, v_at;  // in the cache; -1: nowhere
+};
+__device__ __forceinline__ Placed place_of(const RopeArgs &a, int t) {
+    Placed r = {false, 0, -1, -1};
+    int n, after;  // the sequence, and its tokens from this one on
+    if (a.cu) {
+        if (t < a.cu[0] || t >= a.cu[a.N]) return r;
+        const Span s = locate_by_warp(a.cu, a.N, a.T, t);
+        n = s.n, after = s.end - t;
+    } else {
+        const int each = a.T / a.N;
+        n = t / each, after = each - t % each;
+    }
+    r.live = true;
+    r.index = min(max(a.lens[n], 0), a.capacity) - after;
+    if (r.index < 0) return r;
+    const int page = a.table[n * a.table_stride + r.index / a.page_size];
+    if (page < 0 || page >= a.pages) return r;
+    const int place = r.index % a.page_size;
+    r.k_at = page * a.kps + place * a.kts;
+    r.v_at = page * a.vps + place * a.vts;
+    return r;
+}
+// The token's cosines and sines, pair by pair.
+__device__ __forceinline__ void find_angles(const RopeArgs &a, int t, int index, const uint64_t *turn,
+                                            float2 *cs, int lane) {
+    for (int i = lane; i < a.half; i += 32) {
+        const int32_t p = a.positions ? a.positions[a.axis[i] * a.axis_stride + t] : index;
+        cs[i] = angle_of(p, turn[i]);
+    }
+}
+// V floats from a 16-byte boundary of shared memory.
+template <int V> __device__ __forceinline__ void words_of(const float *p, float (&x)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        const float4 w = *reinterpret_cast<const float4 *>(p + i);
+        x[i] = w.x, x[i + 1] = w.y, x[i + 2] = w.z, x[i + 3] = w.w;
+    }
+}
+// Another lane's word.
+template <typename T, int V> __device__ __forceinline__ Vec<T, V> shuffle_word(const Vec<T, V> &w, int from) {
+    uint32_t r[sizeof(w) / 4];
+    memcpy(r, &w, sizeof(w));
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(w) / 4); ++i) r[i] = __shfl_sync(0xffffffffu, r[i], from);
+    Vec<T, V> x;
+    memcpy(&x, r, sizeof(w));
+    return x;
+}
+
+
+// Words of V elements, NW for each of a head's LANES lanes: all rows start on
+// their boundaries, and a
+// word's elements are rotated, with partners in one other word or its own, or not
+// at all.  T: of the tensors, TC: of the cache.
+template <typename T, typename TC, int V, int LANES, int NW, bool APPEND>
+__global__ void __launch_bounds__(kWarps * 32) gdn_qk_rope_kernel(const __grid_constant__ RopeArgs a) {
+    constexpr int U = NW == 1 ? 4 : NW == 2 ? 2 : 1;  // heads that a lane loads at once
+    __shared__ float2 angles[kWarps][kMaxRotary / 2];
+    __shared__ uint64_t turns[kMaxRotary / 2];
+    __shared__ __align__(16) float weights[2][NW * 32 * V];  // ones where there are none
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    constexpr int ROWS = 32 / LANES;          // heads of a warp at once
+    const int row = lane / LANES, mine = lane % LANES;
+    bool in[NW], turned[NW];  // whether a word is in the head, and rotated
 #pragma unroll
     for (int j = 0; j < NW; ++j) {
-        Word &w = word[j];
-        w.e = (mine + j * lanes) * V;
-        w.in = w.e < a.D;
-        w.turned = w.e < 2 * a.half;
-        if (a.interleaved) {
-            w.pair = w.e / 2;
-            w.partner = w.e ^ 1;  // of one element; longer words hold both
-            w.sign = w.e & 1 ? 1.f : -1.f;
-        } else {
-            const bool first = w.e < a.half;
-            w.pair = first ? w.e : w.e - a.half;
-            w.partner = first ? w.e + a.half : w.e - a.half;
-            w.sign = first ? -1.f : 1.f;
-        }
+        in[j] = (mine + j * LANES) * V < a.D;
+        turned[j] = (mine + j * LANES) * V < 2 * a.half;
     }
-    const bool beside = !(V > 1 && a.interleaved);  // whether partners are in other words
+    for (int i = threadIdx.x; i < a.half; i += kWarps * 32) turns[i] = turn_of(a.inv_freq[i]);
+    for (int i = threadIdx.x; i < NW * 32 * V; i += kWarps * 32) {
+        weights[0][i] = a.q_weight && i < a.D ? a.q_weight[i] : 1.f;
+        weights[1][i] = a.k_weight && i < a.D ? a.k_weight[i] : 1.f;
+    }
+    __syncthreads();
+    const int64_t all = (int64_t)a.T * a.parts, step = (int64_t)gridDim.x * kWarps;
+    const int heads = a.Hq + (APPEND ? 2 : 1) * a.Hk, groups = (heads + ROWS - 1) / ROWS;
+    float2 *cs = angles[warp];
 
-    // Heads [h0, h1) of x, `heads` in all, of which this warp takes every
-    // parts-th group.
-    auto norm_and_turn = [&](const T *x, int64_t hs, const float *weight, int first, int last,
-                             auto &&put) {
-        float w[NW][V], pw[NW][V];
-        if (weight) {
-#pragma unroll
-            for (int j = 0; j < NW; ++j) {
-                if (!word[j].in) continue;
-#pragma unroll
-                for (int i = 0; i < V; ++i) w[j][i] = weight[word[j].e + i];
-                if (beside && word[j].turned)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) pw[j][i] = weight[word[j].partner + i];
-            }
+    for (int64_t at = (int64_t)blockIdx.x * kWarps + warp; at < all; at += step) {
+        const int t = a.parts == 1 ? (int)at : (int)(at / a.parts);
+        const int part = a.parts == 1 ? 0 : (int)(at - (int64_t)t * a.parts);
+        Placed place = {true, 0, -1, -1};
+        if (APPEND) {
+            place = place_of(a, t);
+            if (!place.live) continue;
         }
-        for (int h0 = first; h0 < last; h0 += rows) {
-            const int h = h0 + row;
-            const bool live = h < last;
-            const T *from = x + (int64_t)h * hs;
-            float y[NW][V], py[NW][V];
-            float sum = 0.f;
+        __syncwarp();
+        find_angles(a, t, place.index, turns, cs, lane);
+        __syncwarp();
+
+        // Heads [first, last) of x to `out`.
+        auto norm_and_turn = [&](const T *x, int64_t hs, const float *weight, bool normed, int first,
+                                 int last, auto *out, int64_t ohs, const float *scales) {
+            using TO = std::remove_pointer_t<decltype(out)>;
+            uint64_t own[NW][V / 2], other[NW][V / 2];  // factors of x and x', in pairs
 #pragma unroll
             for (int j = 0; j < NW; ++j) {
+                const int e0 = (mine + j * LANES) * V;
+                const bool second = e0 >= a.half;
+                float f[V], g[V], c[V], d[V];  // w, w', cosine and sine
+                words_of<V>(weight + e0, f);
+                if (a.interleaved) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) y[j][i] = py[j][i] = 0.f;
-                if (!live || !word[j].in) continue;
-                Vec<T, V>::load(from + word[j].e).to(y[j]);
-                if (beside && word[j].turned) Vec<T, V>::load(from + word[j].partner).to(py[j]);
-            }
-            if (weight) {
-#pragma unroll
-                for (int j = 0; j < NW; ++j)
-#pragma unroll
-                    for (int i = 0; i < V; ++i) sum = fmaf(y[j][i], y[j][i], sum);
-                for (int o = lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                const float inv = rsqrtf(sum / (float)a.D + a.eps);
-#pragma unroll
-                for (int j = 0; j < NW; ++j)
+                    for (int i = 0; i < V; i += 2) {
+                        const float2 q = turned[j] ? cs[(e0 + i) / 2] : make_float2(1.f, 0.f);
+                        c[i] = c[i + 1] = q.x;
+                        d[i] = -q.y, d[i + 1] = q.y;
+                        g[i] = f[i + 1], g[i + 1] = f[i];
+                    }
+                } else {
+                    const int partner = !turned[j] ? e0 : second ? e0 - a.half : e0 + a.half;
+                    words_of<V>(weight + partner, g);
+                    const float2 *pairs = cs + (turned[j] ? second ? partner : e0 : 0);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        y[j][i] *= inv * w[j][i];
-                        if (beside) py[j][i] *= inv * pw[j][i];
-                    }
-            }
-            __syncwarp();  // every lane has read before any writes: rows may be in place
-            if (!live) continue;
-#pragma unroll
-            for (int j = 0; j < NW; ++j) {
-                const Word &d = word[j];
-                if (!d.in) continue;
-                if (d.turned) {
-                    if (beside) {
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float2 c = cs[d.pair + i];
-                            y[j][i] = fmaf(d.sign * py[j][i], c.y, y[j][i] * c.x);
-                        }
-                    } else if constexpr (V > 1) {
-#pragma unroll
-                        for (int i = 0; i < V; i += 2) {
-                            const float2 c = cs[d.pair + i / 2];
-                            const float b = y[j][i + 1];
-                            y[j][i + 1] = fmaf(y[j][i], c.y, b * c.x);
-                            y[j][i] = fmaf(-b, c.y, y[j][i] * c.x);
-                        }
+                        const float2 q = turned[j] ? pairs[i] : make_float2(1.f, 0.f);
+                        c[i] = q.x;
+                        d[i] = second ? q.y : -q.y;
                     }
                 }
-                put(h, d.e, y[j]);
-            }
-        }
-    };
-
-    // The part's heads, of queries, keys and values counted together.
-    const int all = a.Hq + (APPEND ? 2 : 1) * a.Hk;
-    const int groups = (all + rows - 1) / rows;  // shares in whole groups of rows
-    const int begin = (int)((int64_t)groups * part / a.parts) * rows,
-              end = (int)((int64_t)groups * (part + 1) / a.parts) * rows;
-    if (begin < a.Hq) {
-        T *to = (T *)a.q_out + t * a.qos;
-        norm_and_turn((const T *)a.q + t * a.qs, a.qh, a.q_weight, begin, min(end, a.Hq),
-                      [&](int h, int e, float(&y)[V]) {
-                          Vec<T, V>::from(y).store(to + (int64_t)h * a.qoh + e);
-                      });
-    }
-    const int k0 = max(begin - a.Hq, 0), k1 = min(end - a.Hq, a.Hk);
-    if (k0 < k1 && (!APPEND || k_at >= 0)) {
-        const T *x = (const T *)a.k + t * a.ks;
-        if (APPEND) {
-            TC *to = (TC *)a.k_cache + k_at;
-            norm_and_turn(x, a.kh, a.k_weight, k0, k1, [&](int h, int e, float(&y)[V]) {
-                Stored<TC, V>::store(to + h * a.khs + e, y, a.k_scale ? a.k_scale[h] : 1.f);
-            });
-        } else {
-            T *to = (T *)a.k_out + t * a.kos;
-            norm_and_turn(x, a.kh, a.k_weight, k0, k1, [&](int h, int e, float(&y)[V]) {
-                Vec<T, V>::from(y).store(to + (int64_t)h * a.koh + e);
-            });
-        }
-    }
-    if (APPEND && v_at >= 0) {
-        const T *x = (const T *)a.v + t * a.vs;
-        TC *to = (TC *)a.v_cache + v_at;
-        const int v0 = max(begin - a.Hq - a.Hk, 0), v1 = min(end - a.Hq - a.Hk, a.Hk);
-        for (int h = v0 + row; h < v1; h += rows) {
 #pragma unroll
-            for (int j = 0; j < NW; ++j) {
-                if (!word[j].in) continue;
-                float y[V];
-                Vec<T, V>::load(x + (int64_t)h * a.vh + word[j].e).to(y);
-                Stored<TC, V>::store(to + h * a.vhs + word[j].e, y, a.v_scale ? a.v_scale[h] : 1.f);
+                for (int i = 0; i < V; i += 2) {
+                    own[j][i / 2] = pack2f(f[i] * c[i], f[i + 1] * c[i + 1]);
+                    other[j][i / 2] = pack2f(g[i] * d[i], g[i + 1] * d[i + 1]);
+                }
+            }
+            // Where a lane's partner word is, for one word per lane.
+            const int from = !turned[0] ? lane : mine * V < a.half ? lane + a.half / V : lane - a.half / V;
+            x += (first + row) * hs + mine * V;
+            out += (first + row) * ohs + mine * V;
+            for (int h = first + row; h - row < last; h += ROWS * U) {
+                Vec<T, V> w[U][NW];
+                [[maybe_unused]] Vec<T, V> v[U][NW];  // partners
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool live = h + u * ROWS < last;
+#pragma unroll
+                    for (int j = 0; j < NW; ++j) {
+                        w[u][j] = Vec<T, V>::zero();
+                        if (live && in[j]) w[u][j] = Vec<T, V>::load(x + j * LANES * V);
+                        if constexpr (NW > 1) {
+                            const int e = (mine + j * LANES) * V;
+                            v[u][j] = Vec<T, V>::zero();
+                            if (live && turned[j] && !a.interleaved)
+                                v[u][j] = Vec<T, V>::load(x + j * LANES * V + (e < a.half ? a.half : -a.half));
+                        }
+                    }
+                    x += ROWS * hs;
+                }
+                float inv[U];
+                if (normed) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        uint64_t sums = 0;
+#pragma unroll
+                        for (int j = 0; j < NW; ++j) {
+                            uint64_t y[V / 2];
+                            to_pairs<V>(w[u][j], y);
+#pragma unroll
+                            for (int i = 0; i < V / 2; ++i) sums = ffma2(y[i], y[i], sums);
+                        }
+                        const float2 two = unpack2f(sums);
+                        inv[u] = two.x + two.y;
+                    }
+#pragma unroll
+                    for (int o = LANES / 2; o > 0; o >>= 1)
+#pragma unroll
+                        for (int u = 0; u < U; ++u) inv[u] += __shfl_xor_sync(0xffffffffu, inv[u], o);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) inv[u] = rsqrtf(fmaf(inv[u], a.inv_dim, a.eps));
+                } else {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) inv[u] = 1.f;
+                }
+                if constexpr (NW > 1) __syncwarp();  // rows in place: partners have been read
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const uint64_t by = pack2f(inv[u], inv[u]);
+                    float scale = 1.f;
+                    if constexpr (sizeof(TO) == 1) scale = h + u * ROWS < last ? scales[h + u * ROWS] : 1.f;
+#pragma unroll
+                    for (int j = 0; j < NW; ++j) {
+                        uint64_t y[V / 2], z[V / 2];
+                        to_pairs<V>(w[u][j], y);
+                        if (a.interleaved) {
+#pragma unroll
+                            for (int i = 0; i < V / 2; ++i) {
+                                const float2 q = unpack2f(y[i]);
+                                z[i] = pack2f(q.y, q.x);
+                            }
+                        } else if constexpr (NW > 1) {
+                            to_pairs<V>(v[u][j], z);
+                        } else {
+                            to_pairs<V>(shuffle_word(w[u][0], from), z);
+                        }
+                        float r[V];
+#pragma unroll
+                        for (int i = 0; i < V / 2; ++i) {
+                            // What is not rotated has no partner: not one of zero, which
+                            // would spread infinities.
+                            uint64_t q = fmul2(y[i], own[j][i]);
+                            if (turned[j]) q = ffma2(z[i], other[j][i], q);
+                            const float2 two = unpack2f(fmul2(q, by));
+                            r[2 * i] = two.x, r[2 * i + 1] = two.y;
+                        }
+                        if (h + u * ROWS < last && in[j]) Stored<TO, V>::store(out + j * LANES * V, r, scale);
+                    }
+                    out += ROWS * ohs;
+                }
+            }
+        };
+
+        // The part's heads, of queries, keys and values counted together, in whole
+        // groups of rows.
+        const int begin = (int)((int64_t)groups * part / a.parts) * ROWS,
+                  end = (int)((int64_t)groups * (part + 1) / a.parts) * ROWS;
+        if (begin < a.Hq)
+            norm_and_turn((const T *)a.q + t * a.qs, a.qh, weights[0], a.q_weight, begin, min(end, a.Hq),
+                          (T *)a.q_out + t * a.qos, a.qoh, nullptr);
+        const int k0 = max(begin - a.Hq, 0), k1 = min(end - a.Hq, a.Hk);
+        const T *keys = (const T *)a.k + t * a.ks;
+        if (!APPEND && k0 < k1)
+            norm_and_turn(keys, a.kh, weights[1], a.k_weight, k0, k1, (T *)a.k_out + t * a.kos, a.koh,
+                          nullptr);
+        if (APPEND && k0 < k1 && place.k_at >= 0)
+            norm_and_turn(keys, a.kh, weights[1], a.k_weight, k0, k1, (TC *)a.k_cache + place.k_at, a.khs,
+                          a.k_scale);
+        if (APPEND && place.v_at >= 0) {
+            const T *x = (const T *)a.v + t * a.vs;
+            TC *to = (TC *)a.v_cache + place.v_at;
+            const int v0 = max(begin - a.Hq - a.Hk, 0), v1 = min(end - a.Hq - a.Hk, a.Hk);
+            for (int h0 = v0; h0 < v1; h0 += ROWS * U) {
+                Vec<T, V> w[U][NW];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < NW; ++j) {
+                        const int h = h0 + u * ROWS + row, e = (mine + j * LANES) * V;
+                        w[u][j] = Vec<T, V>::zero();
+                        if (h < v1 && e < a.D) w[u][j] = Vec<T, V>::load(x + (int64_t)h * a.vh + e);
+                    }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < NW; ++j) {
+                        const int h = h0 + u * ROWS + row, e = (mine + j * LANES) * V;
+                        if (h >= v1 || e >= a.D) continue;
+                        float y[V];
+                        w[u][j].to(y);
+                        Stored<TC, V>::store(to + h * a.vhs + e, y, a.v_scale ? a.v_scale[h] : 1.f);
+                    }
             }
         }
     }
 }
 
-template <typename T, typename TC, int V, int NW, bool APPEND>
+// The same element by element, for any alignment and sizes: lanes take every
+// 32nd element of a head, NW of them.
+template <typename T, typename TC, int NW, bool APPEND>
+__global__ void __launch_bounds__(kWarps * 32)
+gdn_qk_rope_elements_kernel(const __grid_constant__ RopeArgs a) {
+    __shared__ float2 angles[kWarps][kMaxRotary / 2];
+    __shared__ uint64_t turns[kMaxRotary / 2];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int i = threadIdx.x; i < a.half; i += kWarps * 32) turns[i] = turn_of(a.inv_freq[i]);
+    __syncthreads();
+    const int64_t all = (int64_t)a.T * a.parts, step = (int64_t)gridDim.x * kWarps;
+    const int heads = a.Hq + (APPEND ? 2 : 1) * a.Hk;
+    float2 *cs = angles[warp];
+    for (int64_t at = (int64_t)blockIdx.x * kWarps + warp; at < all; at += step) {
+        const int t = (int)(at / a.parts), part = (int)(at % a.parts);
+        Placed place = {true, 0, -1, -1};
+        if (APPEND) {
+            place = place_of(a, t);
+            if (!place.live) continue;
+        }
+        __syncwarp();
+        find_angles(a, t, place.index, turns, cs, lane);
+        __syncwarp();
+        const int begin = (int)((int64_t)heads * part / a.parts),
+                  end = (int)((int64_t)heads * (part + 1) / a.parts);
+        for (int i = begin; i < end; ++i) {
+            const bool is_q = i < a.Hq, is_k = !is_q && i < a.Hq + a.Hk;
+            const int h = is_q ? i : is_k ? i - a.Hq : i - a.Hq - a.Hk;
+            const T *x = is_q   ? (const T *)a.q + t * a.qs + h * a.qh
+                         : is_k ? (const T *)a.k + t * a.ks + h * a.kh
+                                : (const T *)a.v + t * a.vs + h * a.vh;
+            const float *weight = is_q ? a.q_weight : is_k ? a.k_weight : nullptr;
+            float y[NW], z[NW], sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < NW; ++j) {
+                const int e = lane + j * 32;
+                y[j] = z[j] = 0.f;
+                if (e < a.D) y[j] = to_f32(x[e]);
+                if (e < 2 * a.half && (is_q || is_k))
+                    z[j] = to_f32(x[a.interleaved ? e ^ 1 : e < a.half ? e + a.half : e - a.half]);
+                sum = fmaf(y[j], y[j], sum);
+            }
+            const float inv = weight ? rsqrtf(fmaf(warp_sum(sum), a.inv_dim, a.eps)) : 1.f;
+            __syncwarp();  // every lane has read before any writes: rows may be in place
+#pragma unroll
+            for (int j = 0; j < NW; ++j) {
+                const int e = lane + j * 32;
+                if (e >= a.D) continue;
+                float r = y[j] * (weight ? weight[e] : 1.f);
+                if (e < 2 * a.half && (is_q || is_k)) {
+                    const bool second = a.interleaved ? e & 1 : e >= a.half;
+                    const int partner = a.interleaved ? e ^ 1 : second ? e - a.half : e + a.half;
+                    const float2 c = cs[a.interleaved ? e / 2 : second ? partner : e];
+                    const float p = z[j] * (weight ? weight[partner] : 1.f);
+                    r = fmaf(second ? p : -p, c.y, r * c.x);
+                }
+                r *= inv;
+                float one[1] = {r};
+                if (is_q)
+                    ((T *)a.q_out)[t * a.qos + h * a.qoh + e] = from_f32<T>(r);
+                else if (!APPEND)
+                    ((T *)a.k_out)[t * a.kos + h * a.koh + e] = from_f32<T>(r);
+                else if (is_k && place.k_at >= 0)
+                    Stored<TC, 1>::store((TC *)a.k_cache + place.k_at + h * a.khs + e, one,
+                                         a.k_scale ? a.k_scale[h] : 1.f);
+                else if (!is_k && place.v_at >= 0)
+                    Stored<TC, 1>::store((TC *)a.v_cache + place.v_at + h * a.vhs + e, one,
+                                         a.v_scale ? a.v_scale[h] : 1.f);
+            }
+        }
+    }
+}
+
+// LANES 0: element by element.
+template <typename T, typename TC, int V, int LANES, int NW, bool APPEND>
 gdn_status run(RopeArgs &a, cudaStream_t stream) {
-    const int words = (a.D + V - 1) / V;
-    a.lanes = 32;
-    while (NW == 1 && a.lanes / 2 >= words) a.lanes /= 2;
-    const int rows = 32 / a.lanes, heads = a.Hq + (APPEND ? 2 : 1) * a.Hk;
-    const int groups = (heads + rows - 1) / rows;
-    // Few tokens are cut into parts until every SM has eight warps.
-    const int want = (kGridSms * 8 + a.T - 1) / a.T;
-    a.parts = want < 1 ? 1 : want < groups ? want : groups;
-    const int64_t warps = (int64_t)a.T * a.parts;
-    gdn_qk_rope_kernel<T, TC, V, NW, APPEND>
-        <<<(unsigned)((warps + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(a);
+    constexpr int ROWS = LANES > 0 ? 32 / LANES : 1, U = LANES == 0 ? 1 : NW == 1 ? 4 : NW == 2 ? 2 : 1;
+    const int heads = a.Hq + (APPEND ? 2 : 1) * a.Hk, groups = (heads + ROWS - 1) / ROWS;
+    // Tokens are cut into parts until every SM has its warps twice, but not
+    // below what a lane loads at once unless there are too few to start with.
+    constexpr int warps = kGridSms * kWarpsPerSm;
+    const int most = (int64_t)a.T * groups < warps ? groups : (groups + U - 1) / U;
+    const int want = (2 * warps + a.T - 1) / a.T;
+    a.parts = want < 1 ? 1 : want < most ? want : most;
+    const int64_t blocks = ((int64_t)a.T * a.parts + kWarps - 1) / kWarps;
+    const unsigned grid = (unsigned)(blocks < warps / kWarps ? blocks : warps / kWarps);
+    if constexpr (LANES > 0)
+        gdn_qk_rope_kernel<T, TC, V, LANES, NW, APPEND><<<grid, kWarps * 32, 0, stream>>>(a);
+    else
+        gdn_qk_rope_elements_kernel<T, TC, NW, APPEND><<<grid, kWarps * 32, 0, stream>>>(a);
     return launch_status();
 }
 
@@ -297,16 +458,18 @@ gdn_status sized(RopeArgs &a, cudaStream_t stream) {
         (APPEND ? rows(a.v, e, {a.vs, a.vh}) && rows(a.k_cache, c, {a.kps, a.kts, a.khs}) &&
                       rows(a.v_cache, c, {a.vps, a.vts, a.vhs})
                 : rows(a.k_out, e, {a.kos, a.koh}));
-    const int words = wide ? a.D / V : a.D;
     if (wide) {
-        if (words <= 32) return run<T, TC, V, 1, APPEND>(a, stream);
-        if (words <= 64) return run<T, TC, V, 2, APPEND>(a, stream);
-        return run<T, TC, V, 4, APPEND>(a, stream);
+        const int words = a.D / V;
+        if (words <= 8) return run<T, TC, V, 8, 1, APPEND>(a, stream);
+        if (words <= 16) return run<T, TC, V, 16, 1, APPEND>(a, stream);
+        if (words <= 32) return run<T, TC, V, 32, 1, APPEND>(a, stream);
+        if (V == 8 || words <= 64) return run<T, TC, V, 32, 2, APPEND>(a, stream);
+        if constexpr (V < 8) return run<T, TC, V, 32, 4, APPEND>(a, stream);
     }
-    if (words <= 64) return run<T, TC, 1, 2, APPEND>(a, stream);
-    if (words <= 128) return run<T, TC, 1, 4, APPEND>(a, stream);
-    if (words <= 256) return run<T, TC, 1, 8, APPEND>(a, stream);
-    return run<T, TC, 1, 16, APPEND>(a, stream);
+    if (a.D <= 64) return run<T, TC, 1, 0, 2, APPEND>(a, stream);
+    if (a.D <= 128) return run<T, TC, 1, 0, 4, APPEND>(a, stream);
+    if (a.D <= 256) return run<T, TC, 1, 0, 8, APPEND>(a, stream);
+    return run<T, TC, 1, 0, 16, APPEND>(a, stream);
 }
 
 }  // namespace
@@ -326,7 +489,7 @@ gdn_status launch_qk_rope(const gdn_rope_problem &p, const gdn_paged_cache *cach
     a.axis_stride = p.axis_stride;
     a.T = (int)p.total_tokens, a.Hq = p.q_heads, a.Hk = p.kv_heads, a.D = p.head_dim;
     a.half = p.rotary_dim / 2, a.interleaved = p.interleaved != 0;
-    a.eps = p.eps;
+    a.eps = p.eps, a.inv_dim = 1.f / (float)p.head_dim;
     if (p.freq_axis)
         for (int i = 0; i < a.half; ++i) a.axis[i] = p.freq_axis[i];
     if (!cache)
