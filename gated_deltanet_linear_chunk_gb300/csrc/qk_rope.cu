@@ -171,19 +171,46 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_qk_rope_kernel(const __grid_c
     for (int64_t at = (int64_t)blockIdx.x * kWarps + warp; at < all; at += step) {
         const int t = a.parts == 1 ? (int)at : (int)(at / a.parts);
         const int part = a.parts == 1 ? 0 : (int)(at - (int64_t)t * a.parts);
+        // The token's place and angles, found while its first heads are on their way.
         Placed place = {true, 0, -1, -1};
-        if (APPEND) {
-            place = place_of(a, t);
-            if (!place.live) continue;
-        }
-        __syncwarp();
-        find_angles(a, t, place.index, turns, cs, lane);
-        __syncwarp();
+        bool ready = false;
+        auto prepare = [&] {
+            if (ready) return;
+            ready = true;
+            if (APPEND) place = place_of(a, t);
+            __syncwarp();
+            find_angles(a, t, place.index, turns, cs, lane);
+            __syncwarp();
+        };
 
         // Heads [first, last) of x to `out`.
         auto norm_and_turn = [&](const T *x, int64_t hs, const float *weight, bool normed, int first,
                                  int last, auto *out, int64_t ohs, const float *scales) {
             using TO = std::remove_pointer_t<decltype(out)>;
+            x += (first + row) * hs + mine * V;
+            Vec<T, V> w[U][NW];
+            [[maybe_unused]] Vec<T, V> v[U][NW];  // partners
+            auto load = [&](int h) {  // heads from h on
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const bool live = h + u * ROWS < last;
+#pragma unroll
+                    for (int j = 0; j < NW; ++j) {
+                        w[u][j] = Vec<T, V>::zero();
+                        if (live && in[j]) w[u][j] = Vec<T, V>::load(x + j * LANES * V);
+                        if constexpr (NW > 1) {
+                            const int e = (mine + j * LANES) * V;
+                            v[u][j] = Vec<T, V>::zero();
+                            if (live && turned[j] && !a.interleaved)
+                                v[u][j] = Vec<T, V>::load(x + j * LANES * V + (e < a.half ? a.half : -a.half));
+                        }
+                    }
+                    x += ROWS * hs;
+                }
+            };
+            load(first + row);
+            prepare();
+            if (APPEND && !place.live) return;
             uint64_t own[NW][V / 2], other[NW][V / 2];  // factors of x and x', in pairs
 #pragma unroll
             for (int j = 0; j < NW; ++j) {
@@ -218,27 +245,8 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_qk_rope_kernel(const __grid_c
             }
             // Where a lane's partner word is, for one word per lane.
             const int from = !turned[0] ? lane : mine * V < a.half ? lane + a.half / V : lane - a.half / V;
-            x += (first + row) * hs + mine * V;
             out += (first + row) * ohs + mine * V;
             for (int h = first + row; h - row < last; h += ROWS * U) {
-                Vec<T, V> w[U][NW];
-                [[maybe_unused]] Vec<T, V> v[U][NW];  // partners
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const bool live = h + u * ROWS < last;
-#pragma unroll
-                    for (int j = 0; j < NW; ++j) {
-                        w[u][j] = Vec<T, V>::zero();
-                        if (live && in[j]) w[u][j] = Vec<T, V>::load(x + j * LANES * V);
-                        if constexpr (NW > 1) {
-                            const int e = (mine + j * LANES) * V;
-                            v[u][j] = Vec<T, V>::zero();
-                            if (live && turned[j] && !a.interleaved)
-                                v[u][j] = Vec<T, V>::load(x + j * LANES * V + (e < a.half ? a.half : -a.half));
-                        }
-                    }
-                    x += ROWS * hs;
-                }
                 float inv[U];
                 if (normed) {
 #pragma unroll
@@ -299,6 +307,7 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_qk_rope_kernel(const __grid_c
                     }
                     out += ROWS * ohs;
                 }
+                if (h - row + ROWS * U < last) load(h + ROWS * U);
             }
         };
 
@@ -314,6 +323,7 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_qk_rope_kernel(const __grid_c
         if (!APPEND && k0 < k1)
             norm_and_turn(keys, a.kh, weights[1], a.k_weight, k0, k1, (T *)a.k_out + t * a.kos, a.koh,
                           nullptr);
+        if (APPEND) prepare();
         if (APPEND && k0 < k1 && place.k_at >= 0)
             norm_and_turn(keys, a.kh, weights[1], a.k_weight, k0, k1, (TC *)a.k_cache + place.k_at, a.khs,
                           a.k_scale);
