@@ -3,9 +3,9 @@
 // on their way into a paged cache (gdn_paged_append).
 //
 // Per head one read and one write of D elements and some ten operations on
-// each: bound by memory.  A warp takes a token, or a part of its heads where
-// there are few tokens, so the sines and cosines of the token's angles are
-// computed once for all its heads, one per lane.  With a weight w and x' the
+// each: bound by memory.  Every warp takes an equal
+// share of all heads, token by token, so the sines and cosines of the token's angles are
+// computed once for its heads, one per lane.  With a weight w and x' the
 // partner of x, norm and rotation are
 //     y = (x (w cos) + x' (-+ w' sin)) / sqrt(mean(x^2) + eps)
 // with factors that all heads share: a lane keeps those of its elements in
@@ -17,7 +17,9 @@ namespace gdn {
 namespace {
 
 constexpr int kWarps = 4;  // per block
-constexpr int kWarpsPerSm = 24;
+constexpr int kSetup = 6;  // what a token costs beside its heads, in groups of them
+// Blocks per SM, by a lane's words of a head: all blocks run at once.
+__host__ __device__ constexpr int blocks_per_sm(int words) { return words <= 1 ? 6 : words <= 4 ? 4 : 3; }
 
 // The head's elements of one tensor: from, to (null: nothing is stored) and
 // the strides between heads.
@@ -27,7 +29,7 @@ struct RopeArgs {
     const float *q_weight, *k_weight, *inv_freq;
     const int32_t *positions;
     int64_t qs, qh, ks, kh, vs, vh, qos, qoh, kos, koh, axis_stride;
-    int T, Hq, Hk, D, half, interleaved, parts;
+    int T, Hq, Hk, D, half, interleaved, warps, setup;
     float eps, inv_dim;
     // the append's
     void *k_cache, *v_cache;
@@ -39,16 +41,26 @@ struct RopeArgs {
 };
 
 // A turn's fraction as 64 bits: angles are positions times it, modulo 2^64,
-// which is exact in the position.  inv_freq / 2 pi is rounded to double's 53
-// bits, so the angle of position p is off by |p| 2^-53 of inv_freq: 1e-7 radians
-// at 2^29 and one radian per position.  (One double product per pair and warp;
-// the positions' products are of integers.)
-// Odd: not a number, for an infinite or NaN inv_freq.
+// which is exact in the position.  inv_freq = m 2^e is multiplied by the first 64
+// bits of 1 / 2 pi = 0.159.. (from its third binary place on), so the angle of
+// position p is off by 2^-64 of itself and |p| 2^-63 turns.  Odd: not a number,
+// for an infinite or NaN inv_freq.  (Integers: double arithmetic, at a 64th of
+// fp32's rate, takes a microsecond of a token's call.)
 __device__ __forceinline__ uint64_t turn_of(float inv_freq) {
-    if (!isfinite(inv_freq)) return 1;
-    double t = (double)inv_freq * 0.15915494309189533577;  // 1 / 2 pi
-    t -= floor(t);
-    return (uint64_t)(t * 18446744073709551616.0) & ~1ull;
+    constexpr uint64_t kInverse = 0xa2f9836e4e441529;  // 2^66 / 2 pi
+    const uint32_t bits = __float_as_uint(inv_freq);
+    int e = bits >> 23 & 255;
+    if (e == 255) return 1;
+    uint64_t m = bits & 0x7fffff;
+    if (e > 0) m |= 0x800000;
+    else e = 1;
+    const uint64_t low = m * kInverse, high = __umul64hi(m, kInverse);
+    const int down = 152 - e;  // the product is 2^(150 - e + 2) of 2^64 turns
+    uint64_t t;
+    if (down >= 64) t = down < 88 ? high >> (down - 64) : 0;
+    else if (down > 0) t = low >> down | high << (64 - down);
+    else t = down > -64 ? low << -down : 0;
+    return (bits >> 31 ? 0 - t : t) & ~1ull;
 }
 // cos and sin of position times turn.  The upper 32 bits, in half turns, round
 // to fp32's 24: half a step is 2^-25 half turns, 9e-8 radians.
@@ -139,12 +151,34 @@ template <typename T, int V> __device__ __forceinline__ Vec<T, V> shuffle_word(c
 }
 
 
+// A warp's share of all tokens' groups of heads, one token after the other.  A
+// token counts a few groups more than it has, for its angles and factors: the
+// first ones, which are nothing.
+struct Share {
+    int64_t begin, end;
+    __device__ __forceinline__ Share(const RopeArgs &a, int groups, int warp) {
+        const int64_t all = (int64_t)a.T * (groups + a.setup), w = (int64_t)blockIdx.x * kWarps + warp;
+        begin = w < a.warps ? all * w / a.warps : all;
+        end = w < a.warps ? all * (w + 1) / a.warps : all;
+    }
+    // The token of `at` and what the share has of its groups; where the next begins.
+    __device__ __forceinline__ int64_t next(const RopeArgs &a, int64_t at, int groups, int &t, int &first,
+                                            int &last) const {
+        const int each = groups + a.setup;
+        t = (int)(at / each);
+        const int from = (int)(at - (int64_t)t * each), to = (int)min((int64_t)each, from + (end - at));
+        first = max(from - a.setup, 0);
+        last = max(to - a.setup, 0);
+        return at + (to - from);
+    }
+};
+
 // Words of V elements, NW for each of a head's LANES lanes: all rows start on
 // their boundaries, and a
 // word's elements are rotated, with partners in one other word or its own, or not
 // at all.  T: of the tensors, TC: of the cache.
 template <typename T, typename TC, int V, int LANES, int NW, bool APPEND>
-__global__ void __launch_bounds__(kWarps * 32) gdn_qk_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(NW)) gdn_qk_rope_kernel(const __grid_constant__ RopeArgs a) {
     constexpr int U = NW == 1 ? 4 : NW == 2 ? 2 : 1;  // heads that a lane loads at once
     __shared__ float2 angles[kWarps][kMaxRotary / 2];
     __shared__ uint64_t turns[kMaxRotary / 2];
@@ -164,13 +198,13 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_qk_rope_kernel(const __grid_c
         weights[1][i] = a.k_weight && i < a.D ? a.k_weight[i] : 1.f;
     }
     __syncthreads();
-    const int64_t all = (int64_t)a.T * a.parts, step = (int64_t)gridDim.x * kWarps;
     const int heads = a.Hq + (APPEND ? 2 : 1) * a.Hk, groups = (heads + ROWS - 1) / ROWS;
     float2 *cs = angles[warp];
-
-    for (int64_t at = (int64_t)blockIdx.x * kWarps + warp; at < all; at += step) {
-        const int t = a.parts == 1 ? (int)at : (int)(at / a.parts);
-        const int part = a.parts == 1 ? 0 : (int)(at - (int64_t)t * a.parts);
+    const Share share(a, groups, warp);
+    for (int64_t at = share.begin; at < share.end;) {
+        int t, begin, end;
+        at = share.next(a, at, groups, t, begin, end);
+        if (begin == end) continue;
         // The token's place and angles, found while its first heads are on their way.
         Placed place = {true, 0, -1, -1};
         bool ready = false;
@@ -244,7 +278,7 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_qk_rope_kernel(const __grid_c
                 }
             }
             // Where a lane's partner word is, for one word per lane.
-            const int from = !turned[0] ? lane : mine * V < a.half ? lane + a.half / V : lane - a.half / V;
+            [[maybe_unused]] const int from = !turned[0] ? lane : mine * V < a.half ? lane + a.half / V : lane - a.half / V;
             out += (first + row) * ohs + mine * V;
             for (int h = first + row; h - row < last; h += ROWS * U) {
                 float inv[U];
@@ -311,10 +345,8 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_qk_rope_kernel(const __grid_c
             }
         };
 
-        // The part's heads, of queries, keys and values counted together, in whole
-        // groups of rows.
-        const int begin = (int)((int64_t)groups * part / a.parts) * ROWS,
-                  end = (int)((int64_t)groups * (part + 1) / a.parts) * ROWS;
+        // The share's heads, of queries, keys and values counted together.
+        begin *= ROWS, end *= ROWS;
         if (begin < a.Hq)
             norm_and_turn((const T *)a.q + t * a.qs, a.qh, weights[0], a.q_weight, begin, min(end, a.Hq),
                           (T *)a.q_out + t * a.qos, a.qoh, nullptr);
@@ -359,18 +391,20 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_qk_rope_kernel(const __grid_c
 // The same element by element, for any alignment and sizes: lanes take every
 // 32nd element of a head, NW of them.
 template <typename T, typename TC, int NW, bool APPEND>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(NW))
 gdn_qk_rope_elements_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ float2 angles[kWarps][kMaxRotary / 2];
     __shared__ uint64_t turns[kMaxRotary / 2];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     for (int i = threadIdx.x; i < a.half; i += kWarps * 32) turns[i] = turn_of(a.inv_freq[i]);
     __syncthreads();
-    const int64_t all = (int64_t)a.T * a.parts, step = (int64_t)gridDim.x * kWarps;
     const int heads = a.Hq + (APPEND ? 2 : 1) * a.Hk;
     float2 *cs = angles[warp];
-    for (int64_t at = (int64_t)blockIdx.x * kWarps + warp; at < all; at += step) {
-        const int t = (int)(at / a.parts), part = (int)(at % a.parts);
+    const Share share(a, heads, warp);
+    for (int64_t at = share.begin; at < share.end;) {
+        int t, begin, end;
+        at = share.next(a, at, heads, t, begin, end);
+        if (begin == end) continue;
         Placed place = {true, 0, -1, -1};
         if (APPEND) {
             place = place_of(a, t);
@@ -379,8 +413,6 @@ gdn_qk_rope_elements_kernel(const __grid_constant__ RopeArgs a) {
         __syncwarp();
         find_angles(a, t, place.index, turns, cs, lane);
         __syncwarp();
-        const int begin = (int)((int64_t)heads * part / a.parts),
-                  end = (int)((int64_t)heads * (part + 1) / a.parts);
         for (int i = begin; i < end; ++i) {
             const bool is_q = i < a.Hq, is_k = !is_q && i < a.Hq + a.Hk;
             const int h = is_q ? i : is_k ? i - a.Hq : i - a.Hq - a.Hk;
@@ -432,16 +464,14 @@ gdn_qk_rope_elements_kernel(const __grid_constant__ RopeArgs a) {
 // LANES 0: element by element.
 template <typename T, typename TC, int V, int LANES, int NW, bool APPEND>
 gdn_status run(RopeArgs &a, cudaStream_t stream) {
-    constexpr int ROWS = LANES > 0 ? 32 / LANES : 1, U = LANES == 0 ? 1 : NW == 1 ? 4 : NW == 2 ? 2 : 1;
+    constexpr int ROWS = LANES > 0 ? 32 / LANES : 1;
     const int heads = a.Hq + (APPEND ? 2 : 1) * a.Hk, groups = (heads + ROWS - 1) / ROWS;
-    // Tokens are cut into parts until every SM has its warps twice, but not
-    // below what a lane loads at once unless there are too few to start with.
-    constexpr int warps = kGridSms * kWarpsPerSm;
-    const int most = (int64_t)a.T * groups < warps ? groups : (groups + U - 1) / U;
-    const int want = (2 * warps + a.T - 1) / a.T;
-    a.parts = want < 1 ? 1 : want < most ? want : most;
-    const int64_t blocks = ((int64_t)a.T * a.parts + kWarps - 1) / kWarps;
-    const unsigned grid = (unsigned)(blocks < warps / kWarps ? blocks : warps / kWarps);
+    // Every SM has its warps; of few heads each warp has one group.
+    constexpr int most = kGridSms * blocks_per_sm(NW) * kWarps;
+    const int64_t all = (int64_t)a.T * groups;
+    a.warps = (int)(all < most ? all : most);
+    a.setup = all < most ? 0 : kSetup;
+    const unsigned grid = (unsigned)((a.warps + kWarps - 1) / kWarps);
     if constexpr (LANES > 0)
         gdn_qk_rope_kernel<T, TC, V, LANES, NW, APPEND><<<grid, kWarps * 32, 0, stream>>>(a);
     else
