@@ -180,20 +180,10 @@ Plan plan(const gdn_attention_problem &p, const gdn_paged_cache &c) {
 
 template <typename T, int D>
 gdn_status join(const AttentionArgs &a, const Plan &pl, cudaStream_t stream) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
     const int rows = pl.rows < a.R ? pl.rows : a.R;
     const int fit = kJoinBlocks > pl.units ? (int)(kJoinBlocks / pl.units) : 1;
-    cfg.gridDim = dim3((unsigned)pl.units, rows < fit ? rows : fit);
-    cfg.blockDim = dim3(kJoinThreads);
-    return cudaLaunchKernelEx(&cfg, gdn_attention_join_kernel<T, D>, a, pl.rows) == cudaSuccess
-               ? GDN_OK
-               : GDN_ERR_CUDA;
+    return launch_programmatic(gdn_attention_join_kernel<T, D>, dim3((unsigned)pl.units, rows < fit ? rows : fit),
+                               kJoinThreads, 0, stream, a, pl.rows);
 }
 
 }  // namespace

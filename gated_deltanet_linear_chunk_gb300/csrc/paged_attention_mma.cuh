@@ -89,15 +89,19 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, bool words, const float
     }
 }
 
+// The tokens of a tile: a half stage of 8 KB, or of 16 KB where warps share it.
+__host__ __device__ constexpr int tile_tokens(int row_bytes, int mt) {
+    return mt > 1 ? (16384 / row_bytes < 64 ? 16384 / row_bytes : 64) : (8192 / row_bytes < 64 ? 8192 / row_bytes : 64);
+}
 // What a unit costs beside its tokens, in tiles.
-__host__ __device__ constexpr int setup_tiles(int nb, int mt) { return mt > 1 ? 6 : nb > 1 ? 3 : 2; }
+__host__ __device__ constexpr int setup_tiles(int nb, int mt) { return mt > 2 ? 4 : nb > 1 || mt > 1 ? 3 : 2; }
 
 // What a variant keeps in shared memory.  EIGHT: an 8-bit cache; NB blocks of 8
 // rows per warp, MT warps that share a ring, GR such groups.
 template <bool EIGHT, int D, int NB, int MT, int GR> struct Tiles {
     static constexpr int kRowBytes = D * (EIGHT ? 1 : 2);
     static constexpr int kPitch = kRowBytes + 16;  // rows of a matrix on different banks
-    static constexpr int kTokens = 8192 / kRowBytes < 64 ? 8192 / kRowBytes : 64;
+    static constexpr int kTokens = tile_tokens(kRowBytes, MT);
     static constexpr int kTile = kTokens * kPitch;
     static constexpr int kSetup = setup_tiles(NB, MT);
     static constexpr int kThreads = MT * GR * 32, kWarpRows = NB * 8, kRows = MT * kWarpRows;
@@ -111,7 +115,7 @@ template <bool EIGHT, int D, int NB, int MT, int GR> struct Tiles {
     // then end later (three stages per warp, 128 KB: 262144 tokens 179 us, two
     // stages 172; the last SM at 186 us of 162 on average).
     static constexpr int kBlocks = 2;
-    static constexpr int kStages = MT > 2 ? 5 : MT > 1 ? 3 : 2;
+    static constexpr int kStages = MT > 2 ? 3 : 2;
     static constexpr int kRing = GR * kStages * kTile;
     static constexpr int kBytes = kRing + kOwn;
     static_assert(kBytes <= 233472 / kBlocks - 2048 && kSums <= kTile, "");
@@ -146,6 +150,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
         else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(MT * 32) : "memory");
     };
 
+    ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int per_seq = a.Hkv * a.row_blocks;
     const Range range = find_range<TK, SETUP, S::kThreads, GR>(a, per_seq, group);
@@ -799,24 +804,46 @@ gdn_status mma_run(int blocks, const AttentionArgs &a, cudaStream_t stream) {
     const auto kernel = gdn_attention_mma_kernel<EIGHT, D, NB, MT, GR>;
     if (!raise_shared_memory(done, {reinterpret_cast<const void *>(kernel)}, {(size_t)S::kBytes}))
         return GDN_ERR_CUDA;
-    kernel<<<blocks, S::kThreads, S::kBytes, stream>>>(a);
-    return launch_status();
+    return launch_programmatic(kernel, dim3(blocks), S::kThreads, S::kBytes, stream, a);
 }
 
-// Up to 64 rows of a unit at a time: 8 or 16 by a warp, up to four warps.
+// Up to 64 rows of a unit at a time.  Eight per warp leave registers for two
+// blocks of six warps and no spills; sixteen read a tile's matrices half as often,
+// which heads of up to 128 have the registers for.  (8 x 24 / 4 heads of 256, 48
+// rows, 1024 tokens each: 3270 GB/s of cache with six warps of 8 rows, 2710 with
+// three of 16.  Heads of 128: 32 rows 4890 with four of 8, 5830 with two of 16;
+// 64 rows 2150 and 4060, heads of 256 2290 and 2690.)
+struct Warps {
+    int nb, mt;
+};
+constexpr Warps warps_of(int R, int D) {
+    if (R <= 8) return {1, 1};
+    if (R <= 16) return {1, 2};
+    if (R <= 24) return {1, 3};
+    if (R <= 32) return D > 128 ? Warps{1, 4} : Warps{2, 2};
+    if (R <= 48) return D > 128 ? Warps{1, 6} : Warps{2, 3};
+    return {2, 4};
+}
+constexpr int groups_of(Warps w) { return w.mt == 1 ? 4 : w.mt == 2 ? 2 : 1; }
 inline AttentionShape mma_shape(bool eight, int R, int D) {
-    const int bytes = D * (eight ? 1 : 2), tokens = 8192 / bytes < 64 ? 8192 / bytes : 64;
-    return {R <= 8 ? 8 : R > 48 ? 64 : (R + 15) / 16 * 16, tokens,
-            setup_tiles(R <= 8 ? 1 : 2, R <= 16 ? 1 : 2), R <= 16 ? 4 : R <= 32 ? 2 : 1, 2 * kGridSms};
+    const Warps w = warps_of(R, D);
+    return {w.nb * w.mt * 8, tile_tokens(D * (eight ? 1 : 2), w.mt), setup_tiles(w.nb, w.mt), groups_of(w),
+            2 * kGridSms};
+}
+template <bool EIGHT, int D, int R>
+gdn_status mma_rows(int blocks, const AttentionArgs &a, cudaStream_t stream) {
+    constexpr Warps w = warps_of(R, D);
+    return mma_run<EIGHT, D, w.nb, w.mt, groups_of(w)>(blocks, a, stream);
 }
 
 template <bool EIGHT, int D>
 gdn_status mma_rows(int blocks, const AttentionArgs &a, cudaStream_t stream) {
-    if (a.R <= 8) return mma_run<EIGHT, D, 1, 1, 4>(blocks, a, stream);
-    if (a.R <= 16) return mma_run<EIGHT, D, 2, 1, 4>(blocks, a, stream);
-    if (a.R <= 32) return mma_run<EIGHT, D, 2, 2, 2>(blocks, a, stream);
-    if (a.R <= 48) return mma_run<EIGHT, D, 2, 3, 1>(blocks, a, stream);
-    return mma_run<EIGHT, D, 2, 4, 1>(blocks, a, stream);
+    if (a.R <= 8) return mma_rows<EIGHT, D, 8>(blocks, a, stream);
+    if (a.R <= 16) return mma_rows<EIGHT, D, 16>(blocks, a, stream);
+    if (a.R <= 24) return mma_rows<EIGHT, D, 24>(blocks, a, stream);
+    if (a.R <= 32) return mma_rows<EIGHT, D, 32>(blocks, a, stream);
+    if (a.R <= 48) return mma_rows<EIGHT, D, 48>(blocks, a, stream);
+    return mma_rows<EIGHT, D, 64>(blocks, a, stream);
 }
 
 template <bool EIGHT> gdn_status mma_attention(int D, int blocks, const AttentionArgs &a, cudaStream_t stream) {

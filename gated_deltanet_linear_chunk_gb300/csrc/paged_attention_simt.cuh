@@ -27,6 +27,7 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int tok = lane / 4, s = lane % 4;
     float *pw = ps + warp * RR * kSimtTokens;
+    ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const Range range = find_range<kSimtChunk, 1, kSimtWarps * 32, 1>(a, a.Hkv * a.row_blocks, 0);
     for_pieces<kSimtChunk, 1, RR>(a, range, [&](const Unit &u, const Piece &piece) {
@@ -169,8 +170,7 @@ gdn_status simt_run(int blocks, const AttentionArgs &a, cudaStream_t stream) {
     const auto kernel = gdn_attention_simt_kernel<T, TC, D, RR>;
     if (!raise_shared_memory(done, {reinterpret_cast<const void *>(kernel)}, {bytes}))
         return GDN_ERR_CUDA;
-    kernel<<<blocks, kSimtWarps * 32, bytes, stream>>>(a);
-    return launch_status();
+    return launch_programmatic(kernel, dim3(blocks), kSimtWarps * 32, bytes, stream, a);
 }
 
 template <typename T, typename TC, int D>
