@@ -73,14 +73,16 @@ gdn_attention_join_kernel(const __grid_constant__ AttentionArgs a, int rows) {
             const unsigned have = __ballot_sync(0xffffffffu, some);
             const RowPlace p = row_place(a, u, r);
 #pragma unroll
-            for (int w = lane; w < WORDS; w += 32) {
+            for (int w0 = 0; w0 < WORDS; w0 += 32) {  // all lanes take part in the shuffles
+                const int w = w0 + lane;
+                const bool mine = WORDS >= 32 || w < WORDS;
                 float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
                 for (int i = 0; i < pieces; ++i) {
                     const float fi = __shfl_sync(0xffffffffu, f, i);
-                    if (have >> i & 1) add_piece<D>(a, y, slot(i), rows, r, w, fi);
+                    if (mine && (have >> i & 1)) add_piece<D>(a, y, slot(i), rows, r, w, fi);
                 }
-                store_joined<T>(a, p, w * 4, inverse(total), y);
+                if (mine) store_joined<T>(a, p, w * 4, inverse(total), y);
             }
             if (lane == 0) store_lse(a, p, top, total);
         }

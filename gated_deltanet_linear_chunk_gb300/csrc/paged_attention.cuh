@@ -284,24 +284,6 @@ template <int E> __device__ __forceinline__ void load_cached(const __nv_fp8_e4m3
     }
 }
 
-// Launches a kernel that waits itself for what is before it on the stream: its
-// blocks may be set up while that ends.
-template <typename... Params, typename... Args>
-gdn_status launch_programmatic(void (*kernel)(Params...), dim3 grid, int threads, size_t bytes,
-                               cudaStream_t stream, Args... args) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = bytes;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
-}
-
 // What a kernel takes at a time, for units of R rows: rows, the tokens of a
 // tile, a unit's tiles without any, groups per block and its blocks on a GB300.
 struct AttentionShape {

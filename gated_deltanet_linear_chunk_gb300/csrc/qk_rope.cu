@@ -183,6 +183,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(NW)) gdn_qk_rope_ke
     __shared__ float2 angles[kWarps][kMaxRotary / 2];
     __shared__ uint64_t turns[kMaxRotary / 2];
     __shared__ __align__(16) float weights[2][NW * 32 * V];  // ones where there are none
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     constexpr int ROWS = 32 / LANES;          // heads of a warp at once
     const int row = lane / LANES, mine = lane % LANES;
@@ -395,6 +397,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(NW))
 gdn_qk_rope_elements_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ float2 angles[kWarps][kMaxRotary / 2];
     __shared__ uint64_t turns[kMaxRotary / 2];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     for (int i = threadIdx.x; i < a.half; i += kWarps * 32) turns[i] = turn_of(a.inv_freq[i]);
     __syncthreads();
@@ -473,10 +477,11 @@ gdn_status run(RopeArgs &a, cudaStream_t stream) {
     a.setup = all < most ? 0 : kSetup;
     const unsigned grid = (unsigned)((a.warps + kWarps - 1) / kWarps);
     if constexpr (LANES > 0)
-        gdn_qk_rope_kernel<T, TC, V, LANES, NW, APPEND><<<grid, kWarps * 32, 0, stream>>>(a);
+        return launch_programmatic(gdn_qk_rope_kernel<T, TC, V, LANES, NW, APPEND>, dim3(grid), kWarps * 32,
+                                   0, stream, a);
     else
-        gdn_qk_rope_elements_kernel<T, TC, NW, APPEND><<<grid, kWarps * 32, 0, stream>>>(a);
-    return launch_status();
+        return launch_programmatic(gdn_qk_rope_elements_kernel<T, TC, NW, APPEND>, dim3(grid), kWarps * 32,
+                                   0, stream, a);
 }
 
 template <typename T, typename TC, bool APPEND>

@@ -340,6 +340,8 @@ ATTENTION = [  # dtype, cache, lens, L, Hq, Hkv, D, page, gate, order
     (BF16, BF16, [900], 2, 16, 1, 256, 128, False, "heads"),
     (BF16, BF16, [900], 3, 16, 1, 256, 128, True, "heads"),
     (BF16, BF16, [90] * 200, 1, 3, 3, 64, 16, False, "heads"),   # more sequences than threads
+    (BF16, BF16, [150, 40] * 80, 4, 24, 4, 64, 16, True, "heads"),  # narrow heads of many rows, a few pieces each
+    (BF16, BF16, [300, 1, 77], 2, 16, 1, 64, 16, False, "tokens"),
     (BF16, E4M3, EDGES, 1, 16, 2, 128, 32, True, "heads"),
     (BF16, E4M3, EDGES, 2, 6, 3, 64, 10, False, "tokens"),
     (BF16, E4M3, [3000, 1, 0], 4, 6, 1, 256, 16, True, "heads"),
@@ -348,6 +350,8 @@ ATTENTION = [  # dtype, cache, lens, L, Hq, Hkv, D, page, gate, order
     (F32, F32, EDGES, 3, 3, 1, 128, 10, False, "tokens"),
     (F32, F32, [2000, 1, 0, 9], 8, 6, 2, 256, 16, True, "both"),
     (F32, F32, [300], 1, 1, 1, 256, 300, False, "heads"),
+    (F32, F32, [150, 40] * 80, 4, 24, 4, 64, 16, True, "heads"),
+    (F32, F32, [500, 130, 64], 3, 4, 1, 64, 16, False, "tokens"),
 ]
 
 
