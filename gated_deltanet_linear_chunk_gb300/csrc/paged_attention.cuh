@@ -236,13 +236,6 @@ __device__ __forceinline__ void for_pieces(const AttentionArgs &a, const Range &
     }
 }
 
-// A row's element i, divided by the sum and gated.
-template <typename T>
-__device__ __forceinline__ float finish(float sum, float inv, const T *gate) {
-    float y = sum * inv;
-    if (gate) y *= sigmoid(to_f32(*gate));
-    return y;
-}
 __device__ __forceinline__ void store_lse(const AttentionArgs &a, const RowPlace &p, float m,
                                           float l) {
     if (a.lse)
@@ -258,32 +251,10 @@ __device__ __forceinline__ float against(float m) {
     return m == __int_as_float(0xff800000) ? 0.f : m;
 }
 
-// E consecutive elements of the cache as fp32, in words of up to 16 bytes.
-template <int E> __device__ __forceinline__ void load_cached(const float *p, float (&x)[E]) {
-    constexpr int V = E < 4 ? E : 4;
-#pragma unroll
-    for (int i = 0; i < E; i += V) {
-        float w[V];
-        Vec<float, V>::load(p + i).to(w);
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[i + j] = w[j];
-    }
-}
-template <int E> __device__ __forceinline__ void load_cached(const __nv_bfloat16 *p, float (&x)[E]) {
-    Vec<__nv_bfloat16, E>::load(p).to(x);
-}
 __device__ __forceinline__ float2 from_e4m3x2(uint32_t two) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
     return __half22float2(__half2(h));
 }
-template <int E> __device__ __forceinline__ void load_cached(const __nv_fp8_e4m3 *p, float (&x)[E]) {
-#pragma unroll
-    for (int i = 0; i < E; i += 2) {
-        const float2 v = from_e4m3x2(*reinterpret_cast<const uint16_t *>(p + i));
-        x[i] = v.x, x[i + 1] = v.y;
-    }
-}
-
 // What a kernel takes at a time, for units of R rows: rows, the tokens of a
 // tile, a unit's tiles without any, groups per block and its blocks on a GB300.
 struct AttentionShape {

@@ -4,10 +4,12 @@
 
 namespace gdn {
 
-AttentionShape shape_f32(int R, int) { return simt_shape(R); }
+AttentionShape shape_f32(int R, int D) { return simt_shape(R, D); }
 
 gdn_status attention_f32(int D, int blocks, const AttentionArgs &a, cudaStream_t stream) {
-    return simt_attention<float, float>(D, blocks, a, stream);
+    if (D == 64) return simt_rows<64>(blocks, a, stream);
+    if (D == 128) return simt_rows<128>(blocks, a, stream);
+    return simt_rows<256>(blocks, a, stream);
 }
 
 }  // namespace gdn

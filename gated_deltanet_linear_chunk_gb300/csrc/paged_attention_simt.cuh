@@ -1,9 +1,11 @@
-// paged_attention_simt.cuh -- the attention of paged_attention.cuh in fp32
-// arithmetic.
+// paged_attention_simt.cuh -- the attention of paged_attention.cuh in fp32.
 //
-// A warp takes eight tokens at a time: four lanes share a token's scores, each
-// with a quarter of its key, then every lane sums its own elements of the
-// values.
+// A warp takes eight tokens at a time, whose keys and then values asynchronous
+// copies bring to shared memory: the values while the scores are computed, the
+// next keys while the values are added.  Four lanes share a token's scores, each
+// with every fourth word of its key; then every lane sums its own elements of
+// the values.  Two fp32 products per row and element are what bounds it from
+// four rows or so on.
 #pragma once
 
 #include "paged_attention.cuh"
@@ -11,42 +13,97 @@
 namespace gdn {
 
 constexpr int kSimtWarps = 4, kSimtTokens = 8, kSimtChunk = 64;
+// Blocks per SM: as registers and shared memory allow.
+constexpr int simt_blocks(int D, int rows) { return rows > 8 || D > 128 ? 2 : 3; }
 
-// RR rows at a time, TC in the cache.
-template <typename T, typename TC, int D, int RR>
-__global__ void __launch_bounds__(kSimtWarps * 32)
+// RR rows at a time.
+template <int D, int RR> struct Simt {
+    static constexpr int kPitch = D + 16;  // floats: eight tokens' words on different banks
+    static constexpr int kHalf = kSimtTokens * kPitch;
+    static constexpr int kQueries = RR * D, kWeights = kSimtWarps * RR * kSimtTokens;
+    static constexpr int kTiles = kSimtWarps * 2 * kHalf, kSums = kSimtWarps * RR * D;
+    // The warps' sums lie over the tiles at a piece's end.
+    static constexpr int kBytes = 4 * (kQueries + kWeights + (kTiles > kSums ? kTiles : kSums));
+    static_assert(kBytes <= 233472 / simt_blocks(D, RR) - 2048, "");
+};
+
+template <int D, int RR>
+__global__ void __launch_bounds__(kSimtWarps * 32, simt_blocks(D, RR))
 gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
-    constexpr int W = 16 / (int)sizeof(TC), WORDS = D / W, E = D / 32;
+    using S = Simt<D, RR>;
+    constexpr int WORDS = D / 4, E = D / 32, PER = E < 4 ? E : 4;
     constexpr float kNone = -__builtin_huge_valf();
     extern __shared__ __align__(16) float smem[];
-    float *qs = smem;                                // [RR][D]
-    float *ps = qs + RR * D;                         // [warps][RR][tokens]
-    float *os = ps + kSimtWarps * RR * kSimtTokens;  // [warps][RR][D]
+    float *qs = smem;                // [RR][D]
+    float *ps = qs + S::kQueries;    // [warps][RR][tokens]
+    float *tiles = ps + S::kWeights;
+    float *os = tiles;               // [warps][RR][D]
     __shared__ float2 ml[kSimtWarps][RR];
     __shared__ int lims[RR];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int tok = lane / 4, s = lane % 4;
     float *pw = ps + warp * RR * kSimtTokens;
+    float *keys = tiles + warp * 2 * S::kHalf, *values = keys + S::kHalf;
+    // Element e of a lane's part of a row.
+    auto element = [&](int e) { return e / PER * 32 * PER + lane * PER + e % PER; };
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const Range range = find_range<kSimtChunk, 1, kSimtWarps * 32, 1>(a, a.Hkv * a.row_blocks, 0);
     for_pieces<kSimtChunk, 1, RR>(a, range, [&](const Unit &u, const Piece &piece) {
         const int t0 = piece.first_token<kSimtChunk, 1>(u.len), t1 = piece.last_token<kSimtChunk, 1>(u.len);
         const int slot = piece.whole() ? -1 : piece.slot(range.group);
-        __syncthreads();  // the last piece's rows
+        const int32_t *table = a.table + u.n * a.table_stride;
+        bool bad = false;
+        int64_t k_at = -1, v_at = -1;  // of this lane's token in the tile that is copied
+        int entry = -1;                // and of the next one, its page
+        auto look_up = [&](int j0) {
+            const int j = j0 + tok;
+            entry = j < t1 ? table[a.by_page.of(j)] : -1;
+        };
+        auto place = [&](int j0) {
+            const int j = j0 + tok;
+            k_at = v_at = -1;
+            if (j >= t1) return;
+            if (entry < 0 || entry >= a.num_pages) {
+                bad = true;
+                return;
+            }
+            const int at = j - a.by_page.of(j) * a.page_size;
+            k_at = (uint32_t)entry * a.kps + (uint32_t)at * a.kts + (uint32_t)u.head * a.khs;
+            v_at = (uint32_t)entry * a.vps + (uint32_t)at * a.vts + (uint32_t)u.head * a.vhs;
+        };
+        // Rows that do not exist become zeros.
+        auto copy = [&](float *to, const void *from, int64_t at) {
+#pragma unroll
+            for (int w0 = 0; w0 < kSimtTokens * WORDS; w0 += 32) {
+                const int r = (w0 + lane) / WORDS, w = (w0 + lane) % WORDS;
+                const int64_t off = __shfl_sync(0xffffffffu, at, r * 4);
+                copy_async_head(to + r * S::kPitch + w * 4,
+                                static_cast<const char *>(from) + (off < 0 ? 0 : off + w * 16), off < 0 ? 0 : 16);
+            }
+            copies_commit();
+        };
+        constexpr int kStep = kSimtWarps * kSimtTokens;
+        const int first = t0 + warp * kSimtTokens;
+        __syncthreads();  // the last piece's sums and rows
+        look_up(first);
         for (int i = threadIdx.x; i < RR * D; i += kSimtWarps * 32) {
             const int r = i / D;
             float v = 0.f;
             if (r < u.rows) {
                 const RowPlace p = row_place(a, u, r);
-                v = to_f32(((const T *)a.q)[p.token * a.qs + p.head * a.qh + i % D]);
+                v = ((const float *)a.q)[p.token * a.qs + p.head * a.qh + i % D];
             }
             qs[i] = v;
         }
         if (threadIdx.x < RR)
             lims[threadIdx.x] = threadIdx.x < u.rows ? seen_by(a, u, threadIdx.x) : 0;
+        if (first < t1) {
+            place(first);
+            copy(keys, a.k, k_at);
+            look_up(first + kStep);
+        }
         __syncthreads();
-        const float scale = a.scale_log2 * (a.k_scale ? a.k_scale[u.head] : 1.f);
         float m[RR], l[RR], o[RR][E];
 #pragma unroll
         for (int r = 0; r < RR; ++r) {
@@ -54,32 +111,27 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
 #pragma unroll
             for (int e = 0; e < E; ++e) o[r][e] = 0.f;
         }
-        bool bad = false;
-        for (int j0 = t0 + warp * kSimtTokens; j0 < t1; j0 += kSimtWarps * kSimtTokens) {
+        const int all_see = u.len - a.L + 1;  // from here on not every row sees a token
+#pragma unroll 1
+        for (int j0 = first; j0 < t1; j0 += kStep) {
             const int j = j0 + tok;
-            int64_t page = -1;
-            if (j < t1) {
-                page = a.table[u.n * a.table_stride + j / a.page_size];
-                if (page < 0 || page >= a.num_pages) page = -1, bad = true;
-            }
-            const int place = j % a.page_size;
-            const TC *k = (const TC *)((const char *)a.k + page * a.kps + place * a.kts + u.head * a.khs);
-            const int64_t v_at = page * a.vps + place * a.vts + u.head * a.vhs;
+            copies_wait<0>();
+            __syncwarp();
+            copy(values, a.v, v_at);
             float acc[RR];
 #pragma unroll
             for (int r = 0; r < RR; ++r) acc[r] = 0.f;
+#pragma unroll 4
             for (int i = s; i < WORDS; i += 4) {
-                float x[W];
-                if (page < 0) {
+                const float4 x = *reinterpret_cast<const float4 *>(keys + tok * S::kPitch + i * 4);
 #pragma unroll
-                    for (int e = 0; e < W; ++e) x[e] = 0.f;
-                } else {
-                    load_cached(k + i * W, x);
+                for (int r = 0; r < RR; ++r) {
+                    const float4 y = *reinterpret_cast<const float4 *>(qs + r * D + i * 4);
+                    acc[r] = fmaf(y.x, x.x, acc[r]);
+                    acc[r] = fmaf(y.y, x.y, acc[r]);
+                    acc[r] = fmaf(y.z, x.z, acc[r]);
+                    acc[r] = fmaf(y.w, x.w, acc[r]);
                 }
-#pragma unroll
-                for (int r = 0; r < RR; ++r)
-#pragma unroll
-                    for (int e = 0; e < W; ++e) acc[r] = fmaf(qs[r * D + i * W + e], x[e], acc[r]);
             }
             float fade[RR];
 #pragma unroll
@@ -87,7 +139,7 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
                 float x = acc[r];
                 x += __shfl_xor_sync(0xffffffffu, x, 1);
                 x += __shfl_xor_sync(0xffffffffu, x, 2);
-                x = j < t1 && j < lims[r] ? x * scale : kNone;
+                x = j < t1 && j < lims[r] ? x * a.scale_log2 : kNone;
                 float top = x;
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -98,19 +150,29 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
                 l[r] = l[r] * fade[r] + p;
                 if (s == 0) pw[r * kSimtTokens + tok] = p;
             }
-            __syncwarp();
 #pragma unroll
             for (int r = 0; r < RR; ++r)
 #pragma unroll
                 for (int e = 0; e < E; ++e) o[r][e] *= fade[r];
-            for (int t = 0; t < kSimtTokens && j0 + t < t1; ++t) {
-                const int64_t at = __shfl_sync(0xffffffffu, v_at, t * 4);
-                if (__shfl_sync(0xffffffffu, (int)(page < 0), t * 4)) continue;
+            copies_wait<0>();
+            __syncwarp();
+            if (j0 + kStep < t1) {
+                place(j0 + kStep);
+                copy(keys, a.k, k_at);
+                look_up(j0 + 2 * kStep);
+            }
+            // Not every row sees the newest tokens, and what it does not see may
+            // be infinite or NaN.
+            const bool edge = j0 + kSimtTokens > all_see;
+#pragma unroll
+            for (int t = 0; t < kSimtTokens; ++t) {
                 float x[E];
-                load_cached((const TC *)((const char *)a.v + at) + lane * E, x);
+#pragma unroll
+                for (int e = 0; e < E; e += PER)
+                    Vec<float, PER>::load(values + t * S::kPitch + element(e)).to(x + e);
 #pragma unroll
                 for (int r = 0; r < RR; ++r) {
-                    if (j0 + t >= lims[r]) continue;
+                    if (edge && j0 + t >= lims[r]) continue;
                     const float p = pw[r * kSimtTokens + t];
 #pragma unroll
                     for (int e = 0; e < E; ++e) o[r][e] = fmaf(p, x[e], o[r][e]);
@@ -119,6 +181,7 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
             __syncwarp();
         }
         bad = __any_sync(0xffffffffu, bad);
+        __syncthreads();  // the tiles
         // The warps' sums, joined.
 #pragma unroll
         for (int r = 0; r < RR; ++r) {
@@ -127,10 +190,9 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
             if (bad) l[r] = __int_as_float(0x7fffffff);
             if (lane == 0) ml[warp][r] = make_float2(m[r], l[r]);
 #pragma unroll
-            for (int e = 0; e < E; ++e) os[(warp * RR + r) * D + lane * E + e] = o[r][e];
+            for (int e = 0; e < E; ++e) os[(warp * RR + r) * D + element(e)] = o[r][e];
         }
         __syncthreads();
-        const float v_scale = a.v_scale ? a.v_scale[u.head] : 1.f;
         for (int i = threadIdx.x; i < u.rows * D; i += kSimtWarps * 32) {
             const int r = i / D, e = i % D;
             float top = kNone, sum = 0.f, y = 0.f;
@@ -142,12 +204,13 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
                 sum += ml[w][r].y * f;
                 y += os[(w * RR + r) * D + e] * f;
             }
-            y *= v_scale;
             if (slot < 0) {
                 const RowPlace p = row_place(a, u, r);
-                const T *gate = a.gate ? (const T *)a.gate + p.token * a.gs + p.head * a.gh + e : nullptr;
-                ((T *)a.out)[p.token * a.os + p.head * a.oh + e] =
-                    from_f32<T>(finish(y, inverse(sum), gate));
+                const float *gate =
+                    a.gate ? (const float *)a.gate + p.token * a.gs + p.head * a.gh + e : nullptr;
+                y *= inverse(sum);
+                if (gate) y *= sigmoid(*gate);
+                ((float *)a.out)[p.token * a.os + p.head * a.oh + e] = y;
                 if (e == 0) store_lse(a, p, top, sum);
             } else {
                 a.sums[((int64_t)slot * RR + r) * D + e] = y;
@@ -158,33 +221,25 @@ gdn_attention_simt_kernel(const __grid_constant__ AttentionArgs a) {
 }
 
 // Rows at a time: those of a unit, up to 16.
-inline AttentionShape simt_shape(int R) {
-    return {R <= 4 ? 4 : R <= 8 ? 8 : 16, kSimtChunk, 1, 1, 2 * kGridSms};
+inline AttentionShape simt_shape(int R, int D) {
+    const int rows = R <= 4 ? 4 : R <= 8 ? 8 : 16;
+    return {rows, kSimtChunk, 1, 1, simt_blocks(D, rows) * kGridSms};
 }
 
-template <typename T, typename TC, int D, int RR>
+template <int D, int RR>
 gdn_status simt_run(int blocks, const AttentionArgs &a, cudaStream_t stream) {
-    constexpr size_t bytes =
-        sizeof(float) * RR * (D + kSimtWarps * kSimtTokens + kSimtWarps * D);
+    constexpr size_t bytes = Simt<D, RR>::kBytes;
     static std::atomic<bool> done[kMaxDevices];
-    const auto kernel = gdn_attention_simt_kernel<T, TC, D, RR>;
+    const auto kernel = gdn_attention_simt_kernel<D, RR>;
     if (!raise_shared_memory(done, {reinterpret_cast<const void *>(kernel)}, {bytes}))
         return GDN_ERR_CUDA;
     return launch_programmatic(kernel, dim3(blocks), kSimtWarps * 32, bytes, stream, a);
 }
 
-template <typename T, typename TC, int D>
-gdn_status simt_rows(int blocks, const AttentionArgs &a, cudaStream_t stream) {
-    if (a.R <= 4) return simt_run<T, TC, D, 4>(blocks, a, stream);
-    if (a.R <= 8) return simt_run<T, TC, D, 8>(blocks, a, stream);
-    return simt_run<T, TC, D, 16>(blocks, a, stream);
-}
-
-template <typename T, typename TC>
-gdn_status simt_attention(int D, int blocks, const AttentionArgs &a, cudaStream_t stream) {
-    if (D == 64) return simt_rows<T, TC, 64>(blocks, a, stream);
-    if (D == 128) return simt_rows<T, TC, 128>(blocks, a, stream);
-    return simt_rows<T, TC, 256>(blocks, a, stream);
+template <int D> gdn_status simt_rows(int blocks, const AttentionArgs &a, cudaStream_t stream) {
+    if (a.R <= 4) return simt_run<D, 4>(blocks, a, stream);
+    if (a.R <= 8) return simt_run<D, 8>(blocks, a, stream);
+    return simt_run<D, 16>(blocks, a, stream);
 }
 
 }  // namespace gdn
