@@ -98,7 +98,7 @@ gdn_status check_angles(const gdn_rope_problem &p, const int32_t *positions, con
 
 // 16-byte rows: what the attention reads.
 gdn_status check_cache(const gdn_paged_cache &c, int32_t dtype, int heads, int D, bool words) {
-    if (c.num_pages < 0 || c.num_pages > INT32_MAX || c.page_size < 1 || c.page_size > 1 << 20 ||
+    if (c.num_pages < 1 || c.num_pages > INT32_MAX || c.page_size < 1 || c.page_size > 1 << 20 ||
         c.num_seqs < 0 || c.num_seqs > kMostTokens || c.max_pages < 0 ||
         (int64_t)c.max_pages * c.page_size > kMaxCached)
         return GDN_ERR_INVALID_ARG;
@@ -106,7 +106,7 @@ gdn_status check_cache(const gdn_paged_cache &c, int32_t dtype, int heads, int D
     if (c.num_seqs > 1 && c.table_stride < c.max_pages) return GDN_ERR_INVALID_ARG;
     if (c.num_seqs > 0 && (!c.seq_lens || (c.max_pages > 0 && !c.page_table)))
         return GDN_ERR_INVALID_ARG;
-    if (c.num_pages > 0 && any_null({c.k, c.v})) return GDN_ERR_INVALID_ARG;
+    if (any_null({c.k, c.v})) return GDN_ERR_INVALID_ARG;
     if ((c.k_scale != nullptr) != (c.dtype == GDN_E4M3) ||
         (c.v_scale != nullptr) != (c.dtype == GDN_E4M3))
         return GDN_ERR_INVALID_ARG;

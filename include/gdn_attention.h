@@ -89,7 +89,7 @@ GDN_API gdn_status gdn_qk_norm_rope(const gdn_rope_problem *problem, const void 
  *                p page_stride + s token_stride + h head_stride
  *   dtype        GDN_BF16, GDN_F32, or GDN_E4M3: 8-bit floating point (4 bits of
  *                exponent, 3 of mantissa, no infinities) times a scale
- *   num_pages    P, 0 to 2^31 - 1;  page_size 1 to 2^20
+ *   num_pages    P, 1 to 2^31 - 1;  page_size 1 to 2^20
  *   k_scale, v_scale   fp32 [kv heads] of GDN_E4M3, positive; NULL otherwise
  *   num_seqs     N;  max_pages: columns of page_table; max_pages page_size at
  *                most 2^30 - 1
@@ -173,7 +173,8 @@ typedef struct {
 /*
  * Bytes of device workspace gdn_paged_attention needs (from the descriptor's
  * sizes and the cache's type, page_size and max_pages); 0 when either is
- * invalid or no workspace is needed.
+ * invalid or there are no sequences.  A workspace needs no initial value and
+ * belongs to one call at a time.
  */
 GDN_API size_t gdn_paged_attention_workspace_size(const gdn_attention_problem *problem,
                                                   const gdn_paged_cache *cache);
@@ -190,11 +191,12 @@ GDN_API size_t gdn_paged_attention_workspace_size(const gdn_attention_problem *p
  * strides): others are refused.  out may equal q or gate, with the same
  * strides; nothing else may overlap.
  *
- * Every block takes an equal share of the cache's tokens, over the
- * sequences' ends; where one ends inside a sequence, its sums go through the
- * workspace to a second launch, which joins them and may start while the first
- * ends (a programmatic launch on `stream`).  The order of the sums depends on
- * the sizes and lengths alone, so a call gives the same bits every time.
+ * Every group of warps takes an equal share of the cache's tokens, over the
+ * sequences' ends; where a share ends inside a sequence, its sums go through the
+ * workspace to a second launch, which joins them.  All launches of this header
+ * are programmatic ones on `stream`: they may be set up, but read and write
+ * nothing, before what is ahead of them has ended.  The order of the sums depends
+ * on the sizes and lengths alone, so a call gives the same bits every time.
  */
 GDN_API gdn_status gdn_paged_attention(const gdn_attention_problem *problem,
                                        const gdn_paged_cache *cache, const void *q,

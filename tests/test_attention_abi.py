@@ -80,7 +80,7 @@ def cache(dtype=0, N=3, P=20, S=16, H=2, D=64, width=5, scales=False, **kw):
     return c
 
 
-BAD_CACHES = (dict(N=-1), dict(P=-1), dict(P=1 << 31), dict(S=0), dict(S=(1 << 20) + 1),
+BAD_CACHES = (dict(N=-1), dict(P=-1), dict(P=0), dict(P=1 << 31), dict(S=0), dict(S=(1 << 20) + 1),
               dict(width=-1), dict(width=1 << 28), dict(table_stride=4), dict(page_table=None),
               dict(seq_lens=None), dict(k=None), dict(v=None), dict(scales=True),
               dict(dtype=3), dict(dtype=3, scales=True, k_scale=None), dict(k_page_stride=2047),
@@ -139,6 +139,7 @@ def test_attention_refusals(lib):
     assert attend(lib, attention_problem(), None) == INVALID
     for kw in BAD_CACHES:
         assert attend(lib, attention_problem(), cache(**kw)) == INVALID, kw
+    assert attend(lib, attention_problem(L=8, Hq=4096, Hkv=4096, q_stride=1 << 20), cache(N=1 << 17)) == INVALID
     for kw in (dict(L=0), dict(Hq=0), dict(Hkv=0), dict(D=0), dict(Hq=8192), dict(q_stride=255),
                dict(q_head_stride=63), dict(out_stride=255)):
         assert attend(lib, attention_problem(**kw), cache()) == INVALID, kw

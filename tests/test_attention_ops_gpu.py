@@ -661,6 +661,69 @@ def test_captured_steps_replay_with_new_lengths():
         assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
 
 
+def test_captured_behind_copies_and_events():
+    """The launches follow a copy, and another stream's work, in a captured
+    graph as they follow a kernel."""
+    layer = Layer(BF16, BF16, [64, 200, 3], 10)
+    qg, k, v = layer.tokens(3)
+    layer.lens.add_(1)
+    c, q = layer.cache, qg[:, :6]
+    want_q = layer.append(q, k, v)
+    want = gdn.gdn_paged_attention(want_q, c.k, c.v, c.page_table, layer.lens)
+    hold_k, hold_lens = torch.zeros_like(k), torch.zeros_like(layer.lens)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hold_k.copy_(k)  # copies: contiguous tensors
+        got_q = gdn.gdn_paged_append(hold_k, v, c.k, c.v, c.page_table, layer.lens, q=q,
+                                     inv_freq=layer.f, q_weight=layer.qw, k_weight=layer.kw)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            hold_lens.copy_(layer.lens)
+            a = gdn.gdn_paged_attention(got_q, c.k, c.v, c.page_table, hold_lens)
+        b = gdn.gdn_paged_attention(got_q, c.k, c.v, c.page_table, layer.lens)
+        torch.cuda.current_stream().wait_stream(side)
+        r, _ = gdn.gdn_qk_norm_rope(a, q_weight=layer.qw)
+    for _ in range(5):
+        hold_lens.zero_()
+        hold_k.zero_()
+        c.k.zero_()
+        layer.append(q, k, v)
+        prefix = c.k.clone()
+        graph.replay()
+        assert torch.equal(got_q, want_q) and torch.equal(c.k, prefix)
+        assert torch.equal(a, b)
+        assert torch.equal(r, gdn.gdn_qk_norm_rope(b, q_weight=layer.qw)[0])
+    assert want.shape == a.shape
+
+
+def test_calls_from_host_threads():
+    """Calls from several host threads, each on a stream of its own."""
+    import threading
+    layer = Layer(BF16, BF16, [500, 64, 1, 900], 4)
+    c = layer.cache
+    qs = [normal(generator(40 + i), 4, 6, 128) for i in range(4)]
+    want = [gdn.gdn_paged_attention(q, c.k, c.v, c.page_table, layer.lens) for q in qs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                out = gdn.gdn_paged_attention(qs[i], c.k, c.v, c.page_table, layer.lens)
+                s.synchronize()
+                if not torch.equal(out, want[i]):
+                    wrong.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_calls_on_a_stream():
     """`stream=` runs the call there, after what was put on it before."""
     layer = Layer(BF16, BF16, [64, 200], 10)
