@@ -2,15 +2,18 @@
 // position, in one pass, to tensors (gdn_qk_norm_rope) or with keys and values
 // on their way into a paged cache (gdn_paged_append).
 //
-// Per head one read and one write of D elements and some ten operations on
-// each: bound by memory.  Every warp takes an equal
-// share of all heads, token by token, so the sines and cosines of the token's angles are
-// computed once for its heads, one per lane.  With a weight w and x' the
-// partner of x, norm and rotation are
+// Per head one read and one write of D elements and some ten operations on each:
+// bound by memory.  Every warp takes an equal share of all heads, token by token,
+// so the sines and cosines of a token's angles are computed once for its heads,
+// one per lane.  With a weight w and x' the partner of x, norm and rotation are
 //     y = (x (w cos) + x' (-+ w' sin)) / sqrt(mean(x^2) + eps)
 // with factors that all heads share: a lane keeps those of its elements in
 // registers, loads its words of several heads at once, and gets the partners by a
-// shuffle.
+// shuffle.  Measured in bf16: 4000 tokens of 28 heads of 256, 64 of them rotated,
+// 24 us (4.8 TB/s, 70 % of a copy's bandwidth), 20480 of 40 heads of 128 76 us (81
+// %), 8192 of 32 heads of 256 into an 8-bit cache 61 us (60 %): issue slots are 60
+// to 66 % busy, with 60 to 130 instructions per head and some 400 where a share or
+// a token begins.
 #include "attention.cuh"
 
 namespace gdn {
@@ -21,8 +24,8 @@ constexpr int kSetup = 6;  // what a token costs beside its heads, in groups of 
 // Blocks per SM, by a lane's words of a head: all blocks run at once.
 __host__ __device__ constexpr int blocks_per_sm(int words) { return words <= 1 ? 6 : words <= 4 ? 4 : 3; }
 
-// The head's elements of one tensor: from, to (null: nothing is stored) and
-// the strides between heads.
+// Strides are in elements: between tokens (s), heads (h) and the cache's pages,
+// places and heads.
 struct RopeArgs {
     const void *q, *k, *v;
     void *q_out, *k_out;
@@ -44,8 +47,8 @@ struct RopeArgs {
 // which is exact in the position.  inv_freq = m 2^e is multiplied by the first 64
 // bits of 1 / 2 pi = 0.159.. (from its third binary place on), so the angle of
 // position p is off by 2^-64 of itself and |p| 2^-63 turns.  Odd: not a number,
-// for an infinite or NaN inv_freq.  (Integers: double arithmetic, at a 64th of
-// fp32's rate, takes a microsecond of a token's call.)
+// for an infinite or NaN inv_freq.  (In integers: a double has eleven bits less,
+// and its arithmetic runs at a 64th of fp32's rate.)
 __device__ __forceinline__ uint64_t turn_of(float inv_freq) {
     constexpr uint64_t kInverse = 0xa2f9836e4e441529;  // 2^66 / 2 pi
     const uint32_t bits = __float_as_uint(inv_freq);
