@@ -822,7 +822,7 @@ gdn_status mma_run(int blocks, const AttentionArgs &a, cudaStream_t stream) {
 // Up to 64 rows of a unit at a time.  Eight per warp leave registers for two
 // blocks of six warps and no spills; sixteen read a tile's matrices half as often,
 // which heads of up to 128 have the registers for.  (8 x 24 / 4 heads of 256, 48
-// rows, 1024 tokens each: 3270 GB/s of cache with six warps of 8 rows, 2710 with
+// rows, 1024 tokens each: 3380 GB/s of cache with six warps of 8 rows, 2710 with
 // three of 16.  Heads of 128: 32 rows 4890 with four of 8, 5830 with two of 16;
 // 64 rows 2150 and 4060, heads of 256 2290 and 2690.)
 struct Warps {
