@@ -14,7 +14,8 @@
 //            usual group of query heads) leave no part of a product empty
 //   softmax  a running maximum and sum per row; sums are scaled down only when a
 //            maximum grows by more than 2^8, weights are up to that
-//   values   O^T += V^T P^T: 16 elements by 8 rows
+//   values   O^T += V^T P^T: 16 elements by 8 rows, the weights in one or two
+//            parts of 16 bits (weight_parts)
 // Measured, 24 / 4 heads of 256 in bf16, whole calls: one sequence of 262144
 // tokens 171 us (6.3 TB/s, 92 % of a copy's bandwidth), 64 of up to 8192 tokens
 // 95 us (5.3), one of 4000 14 us (latency); eight drafted tokens of 32 sequences,
@@ -71,6 +72,21 @@ template <bool HALF> __device__ __forceinline__ uint32_t pack_weights(float a, f
         return *reinterpret_cast<const uint32_t *>(&h);
     }
 }
+template <bool HALF> __device__ __forceinline__ float2 unpack_weights(uint32_t two) {
+    if constexpr (HALF) return __half22float2(*reinterpret_cast<const __half2 *>(&two));
+    else return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+}
+// Parts of 16 bits that a weight is the sum of in the products.  Two, where MT
+// warps of a ring have up to 16 rows together: a weight is then off by 2^-16 of
+// itself (2^-22 in fp16, beside an 8-bit cache), which an fp32 result does not
+// show once it is rounded, and the stream hides the products (4.3 GB of cache, 8
+// rows of 256: 699 us with one part, 701 with two; 16 rows 731 and 730; an 8-bit
+// cache 717 and 709, 910 and 934).  More rows are bound by their products and
+// reads of shared memory, of which a second part takes its own (24 rows of 256
+// 843 and 883 us, 48 rows 1277 and 1376, 64 rows 1615 and 2200; 64 rows of 128
+// 1077 and 1324): there a weight is rounded once, by up to 2^-8 of itself (fp16:
+// 2^-11), which is the step of the bf16 results that it goes into.
+__host__ __device__ constexpr int weight_parts(int mt) { return mt > 2 ? 1 : 2; }
 // Two elements of 8 bits as two of fp16: exact.
 __device__ __forceinline__ uint32_t widen(uint32_t two) {
     uint32_t r;
@@ -513,7 +529,8 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
                         }
                     }
             }
-            uint32_t p[TT][NB][2];
+            constexpr int PARTS = weight_parts(MT);
+            uint32_t p[PARTS][TT][NB][2];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 const float low[2] = {against(m[b][0]), against(m[b][1])};
@@ -524,8 +541,16 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
                         s[t][b][e] = ex2(fmaf(s[t][b][e], scale[b][e & 1], -low[e & 1]));
                         l[b][e & 1] += s[t][b][e];
                     }
-                    p[t][b][0] = transpose_matrix(pack_weights<EIGHT>(s[t][b][0], s[t][b][1]));
-                    p[t][b][1] = transpose_matrix(pack_weights<EIGHT>(s[t][b][2], s[t][b][3]));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float w0 = s[t][b][h * 2], w1 = s[t][b][h * 2 + 1];
+                        const uint32_t two = pack_weights<EIGHT>(w0, w1);
+                        p[0][t][b][h] = transpose_matrix(two);
+                        if constexpr (PARTS == 2) {
+                            const float2 first = unpack_weights<EIGHT>(two);
+                            p[1][t][b][h] = transpose_matrix(pack_weights<EIGHT>(w0 - first.x, w1 - first.y));
+                        }
+                    }
                 }
             }
 
@@ -594,17 +619,22 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
                                 for (int i = 0; i < 8; ++i) y[i / 4][i % 4] = kept(y[i / 4][i % 4], j + (i % 4 / 2) * 8);
                             }
 #pragma unroll
-                            for (int b = 0; b < NB; ++b) {
-                                multiply<true>(o[d][b], y[0], p[t][b][0], p[t][b][1]);
-                                multiply<true>(o[d + 1][b], y[1], p[t][b][0], p[t][b][1]);
-                            }
+                            for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+                                for (int b = 0; b < NB; ++b) {
+                                    multiply<true>(o[d][b], y[0], p[i][t][b][0], p[i][t][b][1]);
+                                    multiply<true>(o[d + 1][b], y[1], p[i][t][b][0], p[i][t][b][1]);
+                                }
                         } else {
                             if (masked) {
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) x[i] = kept(x[i], j + (i / 2) * 8);
                             }
 #pragma unroll
-                            for (int b = 0; b < NB; ++b) multiply<false>(o[d][b], x, p[t][b][0], p[t][b][1]);
+                            for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+                                for (int b = 0; b < NB; ++b)
+                                    multiply<false>(o[d][b], x, p[i][t][b][0], p[i][t][b][1]);
                         }
                     }
                 }

@@ -15,8 +15,9 @@
  *     contiguous, and neither heads nor tokens of an output may overlap.
  *   - tokens behind the last sequence are allowed (a batch padded to a fixed
  *     size): their outputs are left as they were.
- * Sums, statistics, angles' sines and cosines and softmax are fp32; results
- * are rounded once, to nearest even.
+ * Sums, statistics, angles' sines and cosines and the softmax's maxima, weights
+ * and sums are fp32; results are rounded once, to nearest even.  (What bf16
+ * attention rounds on the way to its products is said there.)
  */
 #ifndef GDN_ATTENTION_H
 #define GDN_ATTENTION_H
@@ -187,6 +188,12 @@ GDN_API size_t gdn_paged_attention_workspace_size(const gdn_attention_problem *p
  *   lse = log sum_j e^s_j                        (fp32 [N L, Hq] or NULL)
  * A row that sees no token, or only scores of -infinity, gets zeros and
  * -infinity.  What a row does not see has no effect on it, whatever it holds.
+ * With bf16 queries the products take their operands in 16 bits.  Where up to 16
+ * rows share a key head (L Hq / Hkv), a weight e^s_j goes in as the sum of two
+ * parts, off by 2^-16 of itself; of more rows it is rounded to bf16, or to fp16
+ * beside a GDN_E4M3 cache.  The sum that divides is that of the fp32 weights, and
+ * so is lse.  Beside a GDN_E4M3 cache an element of a query is fp16 over a power
+ * of two of its row's largest: exact, unless it is below 2^-14 of that.
  * k and v of the cache start on 16-byte boundaries, as do all their rows (the
  * strides): others are refused.  out may equal q or gate, with the same
  * strides; nothing else may overlap.
