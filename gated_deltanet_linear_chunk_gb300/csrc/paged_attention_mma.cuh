@@ -13,7 +13,8 @@
 //   keys     S^T = K Q^T: 16 tokens by 8 rows at a time, so that eight rows (the
 //            usual group of query heads) leave no part of a product empty
 //   softmax  a running maximum and sum per row; sums are scaled down only when a
-//            maximum grows by more than 2^8, weights are up to that
+//            maximum grows by more than 2^8, weights are up to that (times 2^7
+//            beside an 8-bit cache: weight_lift)
 //   values   O^T += V^T P^T: 16 elements by 8 rows, the weights in one or two
 //            parts of 16 bits (weight_parts)
 // Measured, 24 / 4 heads of 256 in bf16, whole calls: one sequence of 262144
@@ -87,6 +88,12 @@ template <bool HALF> __device__ __forceinline__ float2 unpack_weights(uint32_t t
 // 1077 and 1324): there a weight is rounded once, by up to 2^-8 of itself (fp16:
 // 2^-11), which is the step of the bf16 results that it goes into.
 __host__ __device__ constexpr int weight_parts(int mt) { return mt > 2 ? 1 : 2; }
+// Weights, and with them their sums, are taken against the maximum less this, and
+// so stand in `m`, the statistics and the log-sum-exp: nothing else knows of it.
+// fp16 holds no less than 2^-24 and up to 65504, so weights of 1 to 2^8 at their
+// largest would lose what is below 2^-25 of it, which many tokens beside a dominant
+// one add up to.  Up to 2^15 they lose 2^-32 each.  (bf16 has the exponents of fp32.)
+__host__ __device__ constexpr float weight_lift(bool half) { return half ? 7.f : 0.f; }
 // Two elements of 8 bits as two of fp16: exact.
 __device__ __forceinline__ uint32_t widen(uint32_t two) {
     uint32_t r;
@@ -511,7 +518,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
                     for (int t = 1; t < TT; ++t) x = fmaxf(x, fmaxf(s[t][b][e], s[t][b][e + 2]));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-                    top[b][e] = x * scale[b][e];
+                    top[b][e] = fmaf(x, scale[b][e], -weight_lift(EIGHT));
                     grown |= top[b][e] > m[b][e] + 8.f;
                 }
             if (__any_sync(0xffffffffu, grown)) {

@@ -191,7 +191,8 @@ GDN_API size_t gdn_paged_attention_workspace_size(const gdn_attention_problem *p
  * With bf16 queries the products take their operands in 16 bits.  Where up to 16
  * rows share a key head (L Hq / Hkv), a weight e^s_j goes in as the sum of two
  * parts, off by 2^-16 of itself; of more rows it is rounded to bf16, or to fp16
- * beside a GDN_E4M3 cache.  The sum that divides is that of the fp32 weights, and
+ * beside a GDN_E4M3 cache (where either way up to 2^-32 of a row's largest weight
+ * is lost of each other one).  The sum that divides is that of the fp32 weights, and
  * so is lse.  Beside a GDN_E4M3 cache an element of a query is fp16 over a power
  * of two of its row's largest: exact, unless it is below 2^-14 of that.
  * k and v of the cache start on 16-byte boundaries, as do all their rows (the

@@ -104,3 +104,33 @@ def test_one_token_that_outweighs_the_rest(ct, D, rows):
     out, _ = attend(q, c, [200] * N, scale=math.log(2.0))
     y, e = exact(q[0], c, 0, 200, math.log(2.0), TWO)
     check(out, y.expand(N, -1, -1), rounded(y, e))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [8, 16, 24, 64])
+@pytest.mark.parametrize("nats", [12.0, 14.0, 16.0])
+def test_many_small_weights_beside_a_large_one_over_8_bits(D, rows, nats):
+    """A leading token of value zero that outweighs each of the others by e^12
+    to e^16: the result is what the small ones bring.  Sequences enough (of the
+    same tokens) that warps have whole ones."""
+    N, length = 1600, 300
+    c = Cache(generator(D), [length], 16, 1, D, E4M3)
+    c.page_table = c.page_table.expand(N, -1).contiguous()
+    for name in c.scales:
+        c.scales[name] = torch.ones(1, device="cuda")
+    put(c, c.k, range(length), torch.zeros(D))
+    put(c, c.v, range(length), 1.0 + torch.arange(D) % 8 / 8)
+    one = torch.zeros(D)
+    one[0] = 1.0
+    put(c, c.k, [0], one)
+    put(c, c.v, [0], torch.zeros(D))
+    q = torch.zeros(N, rows, D, dtype=BF16, device="cuda")
+    q[..., 0] = nats
+    out, lse = attend(q, c, [length] * N, scale=1.0)
+    # Two parts of fp16 or one, and 2^-25 at the weights' scale of 2^7 for each.
+    y, e = exact(q[0], c, 0, length, 1.0, 2.0 ** -22 if rows <= 16 else 2.0 ** -11)
+    v = c.v.view(torch.uint8)[c.table[0][0], 1, 0].view(E4M3).double()
+    e = e + 2.0 ** -32 * (length - 1) * v
+    check(out, y.expand(N, -1, -1), rounded(y, e))
+    want = math.log(1.0 + (length - 1) * math.exp(-nats)) + nats
+    assert float((lse.double() - want).abs().max()) <= (12 + 3 * length) * U * want
