@@ -526,7 +526,10 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float next = fmaxf(m[b][e], top[b][e]), fade = ex2(m[b][e] - against(next));
+                        // Rows whose own maximum has not grown so far keep theirs: what
+                        // the others see must not show in their last bits.
+                        const float next = top[b][e] > m[b][e] + 8.f ? top[b][e] : m[b][e];
+                        const float fade = ex2(m[b][e] - against(next));
                         m[b][e] = next;
                         l[b][e] *= fade;
 #pragma unroll
