@@ -401,20 +401,18 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
                                                fabsf(__uint_as_float(q[k][b][h] & 0xffff0000u))));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // 2^x <= top < 2^(x + 1), from the exponent's bits.
-                const int x = top > 0x1p-120f && top < 0x1p120f ? (__float_as_int(top) >> 23) - 127 : 0;
+                // 2^x <= top < 2^(x + 1), from the exponent's bits: as far as 2^x and
+                // 2^-x are normal numbers, so that top 2^-x is below 4 for the largest
+                // queries and below 1 for denormal ones.
+                const int x = min(max((__float_as_int(top) >> 23) - 127, -126), 126);
                 up = __int_as_float((127 + x) << 23);
                 const float down = __int_as_float((127 - x) << 23) * sign;
-                auto fit = [&](float v) {  // infinities stay, nothing becomes one
-                    const float y = v * down;
-                    return fabsf(v) < __builtin_huge_valf() ? fminf(fmaxf(y, -65504.f), 65504.f) : y;
-                };
 #pragma unroll
                 for (int k = 0; k < DT; ++k)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        q[k][b][h] = pack_weights<true>(fit(__uint_as_float(q[k][b][h] << 16)),
-                                                        fit(__uint_as_float(q[k][b][h] & 0xffff0000u)));
+                        q[k][b][h] = pack_weights<true>(__uint_as_float(q[k][b][h] << 16) * down,
+                                                        __uint_as_float(q[k][b][h] & 0xffff0000u) * down);
             } else if (sign != 1.f) {
 #pragma unroll
                 for (int k = 0; k < DT; ++k)
