@@ -73,9 +73,22 @@ template <bool HALF> __device__ __forceinline__ uint32_t pack_weights(float a, f
         return *reinterpret_cast<const uint32_t *>(&h);
     }
 }
-template <bool HALF> __device__ __forceinline__ float2 unpack_weights(uint32_t two) {
-    if constexpr (HALF) return __half22float2(*reinterpret_cast<const __half2 *>(&two));
-    else return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+// The same in two parts, the second of what the first leaves.  In bf16 neither is
+// negative, and neither zero for a weight of 2^-109 or more, so that infinite
+// values stay infinite: the first is cut instead of rounded, and the second has
+// 2^-24 of the weight besides, which is a rounding of fp32.  (An 8-bit cache has no
+// infinities.)
+template <bool HALF> __device__ __forceinline__ uint2 split_weights(float a, float b) {
+    if constexpr (HALF) {
+        const uint32_t two = pack_weights<true>(a, b);
+        const float2 first = __half22float2(*reinterpret_cast<const __half2 *>(&two));
+        return make_uint2(two, pack_weights<true>(a - first.x, b - first.y));
+    } else {
+        const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+        return make_uint2(__byte_perm(x, y, 0x7632),
+                          pack_weights<false>(fmaf(a, 0x1p-24f, a - __uint_as_float(x & 0xffff0000u)),
+                                              fmaf(b, 0x1p-24f, b - __uint_as_float(y & 0xffff0000u))));
+    }
 }
 // Parts of 16 bits that a weight is the sum of in the products.  Two, where MT
 // warps of a ring have up to 16 rows together: a weight is then off by 2^-16 of
@@ -552,11 +565,12 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float w0 = s[t][b][h * 2], w1 = s[t][b][h * 2 + 1];
-                        const uint32_t two = pack_weights<EIGHT>(w0, w1);
-                        p[0][t][b][h] = transpose_matrix(two);
                         if constexpr (PARTS == 2) {
-                            const float2 first = unpack_weights<EIGHT>(two);
-                            p[1][t][b][h] = transpose_matrix(pack_weights<EIGHT>(w0 - first.x, w1 - first.y));
+                            const uint2 parts = split_weights<EIGHT>(w0, w1);
+                            p[0][t][b][h] = transpose_matrix(parts.x);
+                            p[1][t][b][h] = transpose_matrix(parts.y);
+                        } else {
+                            p[0][t][b][h] = transpose_matrix(pack_weights<EIGHT>(w0, w1));
                         }
                     }
                 }

@@ -134,3 +134,32 @@ def test_many_small_weights_beside_a_large_one_over_8_bits(D, rows, nats):
     check(out, y.expand(N, -1, -1), rounded(y, e))
     want = math.log(1.0 + (length - 1) * math.exp(-nats)) + nats
     assert float((lse.double() - want).abs().max()) <= (12 + 3 * length) * U * want
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("L,rows", [(1, 3), (1, 8), (1, 16), (1, 24), (4, 1), (4, 4), (8, 8)])
+@pytest.mark.parametrize("length", [1, 40, 300])
+def test_infinite_values_are_infinite_for_the_rows_that_see_them(dtype, D, L, rows, length):
+    """A value of infinity, with weights of one and others: of the first, the
+    newest or any token between."""
+    g = generator(D + rows)
+    N = 4
+    c = Cache(g, [length] * N, 16, 1, D, dtype)
+    q = normal(g, N, L, rows, D, dtype=dtype, std=0.3)
+    q[1] = 0.0  # weights of one
+    for n, j in enumerate((0, length // 2, length - 1, length - 1)):
+        c.v[c.table[n][j // 16], j % 16, 0, 5] = math.inf
+        c.v[c.table[n][j // 16], j % 16, 0, 8] = -math.inf
+    out, lse = attend(q, c, [length] * N)
+    for n, j in enumerate((0, length // 2, length - 1, length - 1)):
+        for t in range(L):
+            sees = length - L + t
+            if sees < 0:
+                assert (out[n, t] == 0).all()
+                continue
+            assert torch.isfinite(lse[n, t]).all()
+            if sees >= j:
+                assert (out[n, t, :, 5] == math.inf).all() and (out[n, t, :, 8] == -math.inf).all()
+                out[n, t, :, [5, 8]] = 0.0
+            assert torch.isfinite(out[n, t]).all()
