@@ -96,13 +96,17 @@ gdn_status check_angles(const gdn_rope_problem &p, const int32_t *positions, con
     return misaligned(4, {positions, inv_freq, q_weight, k_weight}) ? GDN_ERR_MISALIGNED : GDN_OK;
 }
 
+bool cache_type(int32_t cache, int32_t dtype) {
+    return cache == dtype || (cache == GDN_E4M3 && dtype == GDN_BF16);
+}
+
 // 16-byte rows: what the attention reads.
 gdn_status check_cache(const gdn_paged_cache &c, int32_t dtype, int heads, int D, bool words) {
     if (c.num_pages < 1 || c.num_pages > INT32_MAX || c.page_size < 1 || c.page_size > 1 << 20 ||
         c.num_seqs < 0 || c.num_seqs > kMostTokens || c.max_pages < 0 ||
         (int64_t)c.max_pages * c.page_size > kMaxCached)
         return GDN_ERR_INVALID_ARG;
-    if (c.dtype != dtype && !(c.dtype == GDN_E4M3 && dtype == GDN_BF16)) return GDN_ERR_UNSUPPORTED;
+    if (!cache_type(c.dtype, dtype)) return GDN_ERR_UNSUPPORTED;
     if (c.num_seqs > 1 && c.table_stride < c.max_pages) return GDN_ERR_INVALID_ARG;
     if (c.num_seqs > 0 && (!c.seq_lens || (c.max_pages > 0 && !c.page_table)))
         return GDN_ERR_INVALID_ARG;
@@ -215,7 +219,8 @@ GDN_API size_t gdn_paged_attention_workspace_size(const gdn_attention_problem *p
                                                   const gdn_paged_cache *cache) {
     if (!problem || !cache || check_attention(*problem, *cache) != GDN_OK) return 0;
     const gdn_paged_cache &c = *cache;
-    if (c.max_pages < 0 || c.page_size < 1 || c.page_size > 1 << 20 || (int64_t)c.max_pages * c.page_size > kMaxCached)
+    if (!cache_type(c.dtype, problem->dtype) || c.max_pages < 0 || c.page_size < 1 || c.page_size > 1 << 20 ||
+        (int64_t)c.max_pages * c.page_size > kMaxCached)
         return 0;
     return paged_attention_workspace(*problem, c);
 }
