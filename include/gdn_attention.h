@@ -11,8 +11,10 @@
  * untouched.  Where they differ:
  *   - token-major tensors [T, H, D] may be strided between tokens and between
  *     heads (queries that lie beside their gates, head by head, in one
- *     projection); strides are given in elements, the D elements of a head are
- *     contiguous, and neither heads nor tokens of an output may overlap.
+ *     projection); strides are given in elements, and the D elements of a head
+ *     are contiguous.  Neither heads nor tokens of a tensor may overlap, an
+ *     input's no more than an output's (one key for all heads is kv_heads = 1),
+ *     nor pages, places and heads of a cache: such strides are refused.
  *   - tokens behind the last sequence are allowed (a batch padded to a fixed
  *     size): their outputs are left as they were.
  * Sums, statistics, angles' sines and cosines and the softmax's maxima, weights

@@ -144,7 +144,7 @@ def test_scores_of_minus_infinity(name, L, G):
 
 
 @pytest.mark.parametrize("name", TYPES)
-def test_one_token_of_minus_infinity_over_8_bits(name):
+def test_queries_of_minus_infinity(name):
     """Queries of -infinity in one column against keys that are positive there but
     for one token's: a score of +infinity beside those of -infinity is NaN."""
     dtype, ct = TYPES[name]
