@@ -91,16 +91,17 @@ template <bool HALF> __device__ __forceinline__ uint2 split_weights(float a, flo
     }
 }
 // Parts of 16 bits that a weight is the sum of in the products.  Two, where MT
-// warps of a ring have up to 16 rows together: a weight is then off by 2^-16 of
-// itself (2^-22 in fp16, beside an 8-bit cache), which an fp32 result does not
-// show once it is rounded, and the stream hides the products (4.3 GB of cache, 8
-// rows of 256: 699 us with one part, 701 with two; 16 rows 731 and 730; an 8-bit
-// cache 717 and 709, 910 and 934).  More rows are bound by their products and
-// reads of shared memory, of which a second part takes its own (24 rows of 256
-// 843 and 883 us, 48 rows 1277 and 1376, 64 rows 1615 and 2200; 64 rows of 128
-// 1077 and 1324): there a weight is rounded once, by up to 2^-8 of itself (fp16:
-// 2^-11), which is the step of the bf16 results that it goes into.
-__host__ __device__ constexpr int weight_parts(int mt) { return mt > 2 ? 1 : 2; }
+// warps of a ring with NB blocks of 8 rows each have up to 16 rows: a weight is
+// then off by 2^-16 of itself (2^-22 in fp16, beside an 8-bit cache), which a bf16
+// result hardly shows, and the stream hides the products (4.3 GB of cache, one and
+// two parts: 8 rows of 256 700 and 702 us, 16 rows 730 and 730; over 8 bits 717 and
+// 710, 914 and 922; the most, 16 rows of 128 over 8 bits, 1044 and 1076).  More
+// rows are bound by their products and reads of shared memory, of which a second
+// part takes its own (24 rows of 256 843 and 883 us, 48 rows 1277 and 1376, 64 rows
+// 1615 and 2200; 64 rows of 128 1077 and 1324): there a weight is rounded once, by up
+// to 2^-8 of itself (fp16: 2^-11), which is the step of the bf16 results that it
+// goes into.
+__host__ __device__ constexpr int weight_parts(int nb, int mt) { return nb * mt > 2 ? 1 : 2; }
 // Weights, and with them their sums, are taken against the maximum less this, and
 // so stand in `m`, the statistics and the log-sum-exp: nothing else knows of it.
 // fp16 holds no less than 2^-24 and up to 65504, so weights of 1 to 2^8 at their
@@ -550,7 +551,7 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
                         }
                     }
             }
-            constexpr int PARTS = weight_parts(MT);
+            constexpr int PARTS = weight_parts(NB, MT);
             uint32_t p[PARTS][TT][NB][2];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
