@@ -20,9 +20,9 @@
 // Measured, 24 / 4 heads of 256 in bf16, whole calls: one sequence of 262144
 // tokens 171 us (6.3 TB/s, 92 % of a copy's bandwidth), 64 of up to 8192 tokens
 // 95 us (5.3), one of 4000 14 us (latency); eight drafted tokens of 32 sequences,
-// 48 rows, 63 us (2.1), bound by what six warps read of each tile from shared
+// 48 rows, 62 us (2.2), bound by what six warps read of each tile from shared
 // memory and by waits between products; 128 sequences, 64 / 8 heads of 128 over 8
-// bits, 100 us (5.3).
+// bits, 101 us (5.2).
 #pragma once
 
 #include "paged_attention.cuh"
@@ -873,8 +873,12 @@ gdn_status mma_run(int blocks, const AttentionArgs &a, cudaStream_t stream) {
 }
 
 // Up to 64 rows of a unit at a time.  Eight per warp leave registers for two
-// blocks of six warps and no spills; sixteen read a tile's matrices half as often,
-// which heads of up to 128 have the registers for.  (8 x 24 / 4 heads of 256, 48
+// blocks of six warps; sixteen read a tile's matrices half as often, which heads of
+// up to 128 have the registers for.  Not all do without spills (bytes of stores and
+// loads per thread, an 8-bit cache's in brackets): six warps of heads of 256 116 and
+// 152 (196 and 272), four of sixteen rows 512 and 428 (800 and 604), four of eight
+// none (12 and 12), two 4 and 4 (none); heads of 128, three warps of sixteen rows, 64
+// and 76 (96 and 124), two none (24 and 20).  One warp per ring has none.  (8 x 24 / 4 heads of 256, 48
 // rows, 1024 tokens each: 3380 GB/s of cache with six warps of 8 rows, 2710 with
 // three of 16.  Heads of 128: 32 rows 4890 with four of 8, 5830 with two of 16;
 // 64 rows 2150 and 4060, heads of 256 2290 and 2690.)
