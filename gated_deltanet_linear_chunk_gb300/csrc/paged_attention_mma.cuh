@@ -64,10 +64,18 @@ __device__ __forceinline__ void multiply(float (&c)[4], const uint32_t (&a)[4], 
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Two as fp16, infinities as they are.
+__device__ __forceinline__ uint32_t pack_halves(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// (fp16: 65504 at most.  Scores from 2^24 on are rounded to whole numbers, so a
+// weight can pass the 2^15 that it is meant to have.)
 template <bool HALF> __device__ __forceinline__ uint32_t pack_weights(float a, float b) {
     if constexpr (HALF) {
-        const __half2 h = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
+        uint32_t r;
+        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+        return r;
     } else {
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&h);
@@ -425,8 +433,8 @@ gdn_attention_mma_kernel(const __grid_constant__ AttentionArgs a) {
                 for (int k = 0; k < DT; ++k)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        q[k][b][h] = pack_weights<true>(__uint_as_float(q[k][b][h] << 16) * down,
-                                                        __uint_as_float(q[k][b][h] & 0xffff0000u) * down);
+                        q[k][b][h] = pack_halves(__uint_as_float(q[k][b][h] << 16) * down,
+                                                 __uint_as_float(q[k][b][h] & 0xffff0000u) * down);
             } else if (sign != 1.f) {
 #pragma unroll
                 for (int k = 0; k < DT; ++k)

@@ -163,3 +163,32 @@ def test_infinite_values_are_infinite_for_the_rows_that_see_them(dtype, D, L, ro
                 assert (out[n, t, :, 5] == math.inf).all() and (out[n, t, :, 8] == -math.inf).all()
                 out[n, t, :, [5, 8]] = 0.0
             assert torch.isfinite(out[n, t]).all()
+
+
+@pytest.mark.parametrize("ct", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("rows", [8, 24])
+@pytest.mark.parametrize("power", [24, 25, 26, 30])
+def test_scores_too_large_for_steps_of_one(ct, rows, power):
+    """Scores of 2^power and some more, in powers of two, where a step of fp32 is
+    one or far more: whatever the weights come to, the result lies between the
+    values.  Sequences enough that warps have whole ones."""
+    N, length = 1600, 300
+    c = Cache(generator(power), [length], 16, 1, 64, ct)
+    c.page_table = c.page_table.expand(N, -1).contiguous()
+    for name in c.scales:
+        c.scales[name] = torch.ones(1, device="cuda")
+    put(c, c.v, range(length), 1.0 + torch.arange(64) % 8 / 8)
+    key = torch.zeros(64)
+    key[0] = 256.0
+    q = torch.zeros(N, rows, 64, dtype=BF16, device="cuda")
+    q[..., 0] = 2.0 ** (power - 8)
+    q[..., 1] = 2.0 ** (power - 24)
+    for step in range(0, 64, 4):  # the later tiles' scores: that of the first and up to 2^(power - 18) more
+        put(c, c.k, range(length), key)
+        later = key.clone()
+        later[1] = step
+        put(c, c.k, range(70, length), later)
+        out, lse = attend(q, c, [length] * N, scale=math.log(2.0))
+        assert torch.isfinite(lse).all()
+        want = (1.0 + torch.arange(64, device="cuda") % 8 / 8).double()
+        assert float(((out.double() - want).abs() / want).max()) <= 2.0 ** -6, step
