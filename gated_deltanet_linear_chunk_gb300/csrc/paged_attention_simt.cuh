@@ -5,10 +5,10 @@
 // next keys while the values are added.  Four lanes share a token's scores, each
 // with every fourth word of its key; then every lane sums its own elements of
 // the values.  A row or four are bound by memory: 4096 units of 1024 tokens, one row
-// of 128, 687 us (6.3 TB/s), four 712.  More are by reads of shared memory, where a
+// of 128, 687 us (6.3 TB/s), four 709.  More are by reads of shared memory, where a
 // lane gets every row's query word and weight again for its token: six rows of 128
-// (taken as eight) 1073 us, its shared memory 70 % busy and the fp32 units 26 %; six
-// of 256 1454 us for 512 tokens (3.0 TB/s), shared memory 44 %, fp32 18 %, memory 34
+// (taken as eight) 1070 us, its shared memory 70 % busy and the fp32 units 26 %; six
+// of 256 1452 us for 512 tokens (3.0 TB/s), shared memory 44 %, fp32 18 %, memory 34
 // %: there the two warps of a scheduler wait for those reads, and for the copies of
 // a tile that nothing but the other half's arithmetic covers.  (Sixteen rows of 256
 // spill 132 bytes of stores and 152 of loads.)
